@@ -372,6 +372,106 @@ LORA_API lora_status_t lora_linear_merge_check(void *stream);
 LORA_API lora_status_t lora_linear_selftest_timeout(void *workspace, size_t ws_bytes, uint32_t limit_us,
                                                     void *stream);
 
+/* ---- operators around the layer ------------------------------------------------
+ * What a transformer block computes right beside its projections: gated projections and
+ * a projection with bias, activation and residual.  The conventions above hold for all of them.
+ * The pages list these parts of a block's kernel fusion without formulas (page
+ * "UnSloth加速库集成：编译级优化带来的性能飞跃", section 核心技术一); the formulas are
+ * given at each entry point.
+ */
+
+/* Activations.  Values: relu max(v, 0); silu v / (1 + e^-v); gelu v P(v) with the normal
+ * distribution P; gelu_tanh v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+typedef enum {
+    LORA_ACT_NONE = 0,
+    LORA_ACT_RELU = 1,
+    LORA_ACT_SILU = 2,
+    LORA_ACT_GELU = 3,
+    LORA_ACT_GELU_TANH = 4
+} lora_act_t;
+
+/* Storage formats of the frozen weight, as the entry points above define them. */
+typedef enum { LORA_W_BF16 = 0, LORA_W_Q4 = 1, LORA_W_FP8 = 2, LORA_W_NF4 = 3 } lora_weight_format_t;
+
+/* A frozen weight [d_out, d_in] in one of the formats (the struct lives in host memory). */
+typedef struct {
+    int32_t format;        /* lora_weight_format_t */
+    const void *data;      /* bf16 W, or the codes (Wq / W8) */
+    const uint16_t *scale; /* coded formats: the bf16 scales; LORA_W_BF16: NULL */
+    const float *codebook; /* LORA_W_NF4: 16 finite values in HOST memory; else NULL */
+} lora_weight_t;
+
+/*
+ * Gated projections of one x:
+ *     [g | u] = x.W^T + s.(x.A^T).B^T        p = act(g) * u         s = alpha / r
+ * W [2 d_ff, d_in] holds the gate's rows and then the up projection's; A [r, d_in] and
+ * B [2 d_ff, r] are adapters of the stacked layer (block-diagonal B for an adapter of each
+ * projection's own).  The activation and the product run in the GEMM's epilogue on the
+ * fp32 accumulators: p is rounded once, and g, u never reach memory unless asked for.
+ *   p        output [M, d_ff] (bf16).
+ *   gu_save  optional output [M, 2 d_ff] (bf16) = [g | u], for lora_glu_bwd.  May be NULL.
+ *   xa_save  as lora_linear_fwd.
+ *   act      a lora_act_t; LORA_ACT_NONE gives p = g * u.
+ * d_ff % 8 == 0 (W's sizes as in the layer with d_out = 2 d_ff); the workspace is
+ * lora_linear_workspace_size(the format's forward op, M, d_in, 2 d_ff, r).  Needs CTA pairs
+ * (LORA_ERR_UNSUPPORTED without them).
+ */
+LORA_API lora_status_t lora_glu_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A, const uint16_t *B,
+                                    uint16_t *p, uint16_t *gu_save, uint16_t *xa_save, int64_t M, int64_t d_in,
+                                    int64_t d_ff, int r, float alpha, int act, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Backward: dg = dP * u * act'(g), du = dP * act(g), then the layer's backward with
+ * dY = [dg | du].
+ *   dP   input [M, d_ff];  gu: the forward's gu_save;  xa_save: the forward's, or NULL to
+ *        recompute it.
+ *   dGU  output [M, 2 d_ff] (bf16) = [dg | du]: the gradient of the pre-activations, which
+ *        the layer's backward reads.  Required; must not alias gu.
+ *   dX (or NULL), dA, dB: as lora_linear_bwd, of the stacked layer.
+ * Workspace: lora_linear_workspace_size(the format's backward op, M, d_in, 2 d_ff, r).
+ */
+LORA_API lora_status_t lora_glu_bwd(const uint16_t *dP, const uint16_t *gu, const uint16_t *x, const lora_weight_t *W,
+                                    const uint16_t *A, const uint16_t *B, const uint16_t *xa_save, uint16_t *dGU,
+                                    uint16_t *dX, float *dA, float *dB, int64_t M, int64_t d_in, int64_t d_ff, int r,
+                                    float alpha, int act, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Projection with bias, activation and residual in its epilogue:
+ *     pre = x.W^T + s.(x.A^T).B^T + bias        out = act(pre) + residual
+ *   bias      [d_out] (bf16) or NULL;  residual [M, d_out] (bf16) or NULL.
+ *   out       output [M, d_out] (bf16), rounded once from fp32.
+ *   pre_save  optional output [M, d_out] (bf16): pre, for the backward of an activation.
+ * Everything else as lora_linear_fwd; the workspace is that of
+ * lora_linear_workspace_size(the format's forward op, ...).  Needs CTA pairs.
+ */
+LORA_API lora_status_t lora_linear_act_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A,
+                                           const uint16_t *B, const uint16_t *bias, const uint16_t *residual,
+                                           uint16_t *out, uint16_t *pre_save, uint16_t *xa_save, int64_t M,
+                                           int64_t d_in, int64_t d_out, int r, float alpha, int act, void *workspace,
+                                           size_t workspace_bytes, void *stream);
+
+/*
+ * Backward: dPre = dOut * act'(pre), dbias = the sum of dPre over the tokens (formed in
+ * fp32 before dPre is rounded), then the layer's backward with dY = dPre.  The residual's
+ * gradient is dOut itself.
+ *   pre    the forward's pre_save; ignored (may be NULL) for LORA_ACT_NONE.
+ *   dPre   output [M, d_out] (bf16); required unless act is LORA_ACT_NONE, where dOut
+ *          itself is the layer's dY and dPre is ignored.
+ *   dbias  output [d_out] (fp32), or NULL.
+ * Sums run in a fixed order: the same call gives the same bits.  Workspace:
+ * lora_linear_act_workspace_size(the format's backward op, M, d_in, d_out, r).
+ */
+LORA_API lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t *pre, const uint16_t *x,
+                                           const lora_weight_t *W, const uint16_t *A, const uint16_t *B,
+                                           const uint16_t *xa_save, uint16_t *dPre, uint16_t *dX, float *dA, float *dB,
+                                           float *dbias, int64_t M, int64_t d_in, int64_t d_out, int r, float alpha,
+                                           int act, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_linear_act_fwd / _bwd for `op`, a lora_op_t of the weight's
+ * format (0 if the sizes are invalid).  Pure host function. */
+LORA_API size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r);
+
 /* ---- measurement hooks (no effect on results) ---------------------------------
  * Kernel kinds, in the order a forward + backward launches them. */
 typedef enum {

@@ -1,0 +1,221 @@
+"""The operators around the LoRA linear layer of a transformer block, with autograd.
+
+* ``lora_glu``: gated projections of one x, act(gate) * up in the GEMM's epilogue;
+* ``lora_linear_act``: a projection with bias, activation and residual in its epilogue.
+
+Both take the frozen weight as a bf16 tensor or as a ``FrozenWeight`` of any format, and
+trainable adapters A, B of the (stacked) layer; gradients flow to x, A, B, the bias and the
+residual.  As ``autograd.lora_linear``: the library's kernels run, or torch's unfused
+composition where the library answers LORA_ERR_UNSUPPORTED or LORA_LINEAR_FUSED=0 asks for
+it (warned once); a missing library raises.
+
+Workspaces are kept per device, stream and shape, so calls on two streams never share one;
+a call that is being captured into a CUDA graph takes a workspace of its own from the
+graph's memory pool, so two graphs can replay at the same time.  To capture a backward,
+capture the forward with it in the same graph (autograd runs a backward on the streams of
+its forward).
+"""
+from __future__ import annotations
+
+import collections
+import threading
+import warnings
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import autograd as LA
+from . import lora_linear as L
+
+_ws_lock = threading.Lock()
+_ws_cache: collections.OrderedDict = collections.OrderedDict()
+_WS_KEPT = 64  # workspaces kept (the least recently used goes first)
+
+
+def _workspace(size_fn, op: int, M: int, d_in: int, d_out: int, r: int, device) -> torch.Tensor:
+    """A zeroed workspace of size_fn(op, ...) bytes for the current stream."""
+    n = size_fn(op, M, d_in, d_out, r)
+    if n == 0:
+        raise ValueError(f"invalid sizes: {M} tokens, {d_in} -> {d_out}, rank {r}")
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream, size_fn, op, M, d_in, d_out, r, n)
+    with _ws_lock:
+        ws = _ws_cache.get(key)
+        if ws is None:
+            # evicted workspaces go back to their stream's pool of the caching allocator, in
+            # stream order behind the kernels that still use them
+            while len(_ws_cache) >= _WS_KEPT:
+                _ws_cache.popitem(last=False)
+            ws = _ws_cache[key] = torch.zeros(n, dtype=torch.uint8, device=device)
+        else:
+            _ws_cache.move_to_end(key)
+        return ws
+
+
+def _frozen(W) -> LA.FrozenWeight:
+    return W if isinstance(W, LA.FrozenWeight) else LA.FrozenWeight("bf16", (W,))
+
+
+def _fused_or(fused, unfused):
+    """fused(), or unfused() where the library declines (see the module docstring)."""
+    if LA.fused_enabled():
+        try:
+            return fused()
+        except L.LoraError as e:
+            if e.status != 3:  # only LORA_ERR_UNSUPPORTED falls back
+                raise
+            reason = str(e)
+    else:
+        reason = "LORA_LINEAR_FUSED=0"
+    LA.fallback_calls += 1
+    if LA.fallback_calls == 1:
+        warnings.warn(f"fused LoRA operator not used ({reason}); computing the unfused composition", RuntimeWarning)
+    return unfused()
+
+
+_TORCH_ACT = {
+    "none": lambda t: t,
+    "relu": torch.relu,
+    "silu": torch.nn.functional.silu,
+    "gelu": torch.nn.functional.gelu,
+    "gelu_tanh": lambda t: torch.nn.functional.gelu(t, approximate="tanh"),
+}
+
+
+def _grad_wanted(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+# ------------------------------------------------------------------ gated projections
+def _glu_forward(x, A, B, alpha, wt, act, save):
+    M, r, n = x.shape[0], A.shape[0], wt.d_out
+    p = torch.empty(M, n // 2, dtype=torch.bfloat16, device=x.device)
+    gu = torch.empty(M, n, dtype=torch.bfloat16, device=x.device) if save else None
+    xa = torch.empty(M, r, dtype=torch.bfloat16, device=x.device) if save else None
+    if M > 0:
+        ws = _workspace(L.lora_linear_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
+        L.lora_glu_fwd(x, wt, A, B, p, gu, xa, alpha, act, ws)
+    return p, gu, xa
+
+
+class LoraGluFunction(torch.autograd.Function):
+    """p = act(g) * u, [g | u] = x.w^T + (alpha / r).(x.A^T).B^T; x [M, d_in] bf16."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, alpha, wt, act):
+        p, gu, xa = _glu_forward(x, A, B, alpha, wt, act, save=True)
+        ctx.save_for_backward(x, A, B, xa, gu, *wt.tensors)
+        ctx.alpha, ctx.wt, ctx.act = alpha, wt, act
+        return p
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dP):
+        x, A, B, xa, gu = ctx.saved_tensors[:5]
+        wt = ctx.wt
+        M, r, n = x.shape[0], A.shape[0], wt.d_out
+        dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
+        if M == 0:
+            return dX, torch.zeros_like(A), torch.zeros_like(B), None, None, None
+        dA = torch.empty(A.shape, dtype=torch.float32, device=x.device)
+        dB = torch.empty(B.shape, dtype=torch.float32, device=x.device)
+        dGU = torch.empty_like(gu)
+        ws = _workspace(L.lora_linear_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
+        L.lora_glu_bwd(dP.contiguous(), gu, x, wt, A, B, xa, dGU, dX, dA, dB, ctx.alpha, ctx.act, ws)
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None
+
+
+def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
+    """act(g) * u for [g | u] = x.W^T + (alpha / r).(x.A^T).B^T, x [..., d_in] bf16.
+
+    W [2 d_ff, d_in] (a bf16 tensor or a FrozenWeight) holds the gate's rows and then the up
+    projection's; A [r, d_in] and B [2 d_ff, r] are the stacked layer's adapters, as
+    multi.SharedInputProjections lays them out (rank P r and P alpha for the call, B
+    block-diagonal).  act: one of L.ACTIVATIONS."""
+    wt = _frozen(W)
+    L._act(act)
+    x2 = x.reshape(-1, x.shape[-1]).contiguous()
+
+    def fused():
+        if _grad_wanted(x2, A, B):
+            return LoraGluFunction.apply(x2, A, B, alpha, wt, act)
+        return _glu_forward(x2, A, B, alpha, wt, act, save=False)[0]
+
+    def unfused():
+        g, u = LA._unfused(x2, wt, A, B, alpha).chunk(2, dim=-1)
+        return _TORCH_ACT[act](g) * u
+
+    p = _fused_or(fused, unfused)
+    return p if x.dim() == 2 else p.reshape(*x.shape[:-1], p.shape[-1])
+
+
+# ------------------------------------------------------------------ projection with an epilogue
+def _act_forward(x, A, B, bias, residual, alpha, wt, act, save):
+    M, r, n = x.shape[0], A.shape[0], wt.d_out
+    out = torch.empty(M, n, dtype=torch.bfloat16, device=x.device)
+    pre = torch.empty_like(out) if save and act != "none" else None
+    xa = torch.empty(M, r, dtype=torch.bfloat16, device=x.device) if save else None
+    if M > 0:
+        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
+        L.lora_linear_act_fwd(x, wt, A, B, bias, residual, out, pre, xa, alpha, act, ws)
+    return out, pre, xa
+
+
+class LoraLinearActFunction(torch.autograd.Function):
+    """out = act(x.w^T + (alpha / r).(x.A^T).B^T + bias) + residual; x [M, d_in] bf16."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, bias, residual, alpha, wt, act):
+        out, pre, xa = _act_forward(x, A, B, bias, residual, alpha, wt, act, save=True)
+        ctx.save_for_backward(x, A, B, xa, pre, *wt.tensors)
+        ctx.alpha, ctx.wt, ctx.act = alpha, wt, act
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dOut):
+        x, A, B, xa, pre = ctx.saved_tensors[:5]
+        wt = ctx.wt
+        M, r, n = x.shape[0], A.shape[0], wt.d_out
+        dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
+        dres = dOut if ctx.needs_input_grad[4] else None
+        want_bias = ctx.needs_input_grad[3]
+        if M == 0:
+            dbias = torch.zeros(n, dtype=ctx.bias_dtype, device=x.device) if want_bias else None
+            return dX, torch.zeros_like(A), torch.zeros_like(B), dbias, dres, None, None, None
+        dOut = dOut.contiguous()
+        dA = torch.empty(A.shape, dtype=torch.float32, device=x.device)
+        dB = torch.empty(B.shape, dtype=torch.float32, device=x.device)
+        dbias = torch.empty(n, dtype=torch.float32, device=x.device) if want_bias else None
+        dPre = torch.empty_like(dOut) if ctx.act != "none" else None
+        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
+        L.lora_linear_act_bwd(dOut, pre, x, wt, A, B, xa, dPre, dX, dA, dB, dbias, ctx.alpha, ctx.act, ws)
+        return (dX, dA.to(A.dtype), dB.to(B.dtype), dbias.to(ctx.bias_dtype) if want_bias else None, dres, None, None,
+                None)
+
+
+def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str = "none"):
+    """act(x.W^T + (alpha / r).(x.A^T).B^T + bias) + residual, x [..., d_in] bf16, residual
+    [..., d_out], bias [d_out] (bf16), each optional.  W: a bf16 tensor [d_out, d_in] or a
+    FrozenWeight.  act: one of L.ACTIVATIONS."""
+    wt = _frozen(W)
+    L._act(act)
+    x2 = x.reshape(-1, x.shape[-1]).contiguous()
+    if residual is not None and residual.shape != (*x.shape[:-1], wt.d_out):
+        raise ValueError(f"residual: expected shape {(*x.shape[:-1], wt.d_out)}, got {tuple(residual.shape)}")
+    res2 = None if residual is None else residual.reshape(-1, wt.d_out).contiguous()
+
+    def fused():
+        if _grad_wanted(x2, A, B, bias, res2):
+            return LoraLinearActFunction.apply(x2, A, B, bias, res2, alpha, wt, act)
+        return _act_forward(x2, A, B, bias, res2, alpha, wt, act, save=False)[0]
+
+    def unfused():
+        h = LA._unfused(x2, wt, A, B, alpha)
+        h = _TORCH_ACT[act](h if bias is None else h + bias)
+        return h if res2 is None else h + res2
+
+    out = _fused_or(fused, unfused)
+    return out if x.dim() == 2 else out.reshape(*x.shape[:-1], out.shape[-1])

@@ -1,0 +1,81 @@
+// act.cuh -- the activations of the gated and the epilogue projections, and their
+// derivatives, in fp32.
+//
+//   relu       max(v, 0)                              derivative 1 for v > 0, else 0
+//   silu       v s(v), s(v) = 1 / (1 + e^-v)          s (1 + v (1 - s))
+//   gelu       v P(v), P the normal distribution      P(v) + v p(v), p its density
+//   gelu_tanh  v/2 (1 + tanh z) = v s(2z),            s(2z) (1 + v (1 - s(2z)) 2 z'),
+//              z = c (v + 0.044715 v^3), c = sqrt(2/pi)   z' = c (1 + 3 * 0.044715 v^2)
+//
+// The logistic function goes through __expf and __fdividef (a few units in the last place of
+// fp32, far inside the one bf16 rounding that every result takes); at the ends, e^-v =
+// inf gives s = 0 and e^-v = 0 gives s = 1.  NaN stays NaN in each of them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/lora_linear.h"
+
+namespace lora {
+
+template <int A>
+struct ActCode {
+    static constexpr int value = A;
+};
+
+// f(ActCode<act>()) for the run-time code `act` (validated on the host).
+template <class F>
+__device__ __forceinline__ void act_dispatch(int act, F &&f) {
+    switch (act) {
+        case LORA_ACT_RELU: f(ActCode<LORA_ACT_RELU>()); break;
+        case LORA_ACT_SILU: f(ActCode<LORA_ACT_SILU>()); break;
+        case LORA_ACT_GELU: f(ActCode<LORA_ACT_GELU>()); break;
+        case LORA_ACT_GELU_TANH: f(ActCode<LORA_ACT_GELU_TANH>()); break;
+        default: f(ActCode<LORA_ACT_NONE>()); break;
+    }
+}
+
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float GELU_A = 0.044715f;
+constexpr float INV_SQRT2 = 0.70710678118654752f, INV_SQRT_2PI = 0.39894228040143268f;
+
+template <int A>
+__device__ __forceinline__ float act_value(float v) {
+    if constexpr (A == LORA_ACT_RELU) return v < 0.0f ? 0.0f : v;  // NaN stays
+    if constexpr (A == LORA_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+    if constexpr (A == LORA_ACT_GELU) return 0.5f * v * (1.0f + erff(v * INV_SQRT2));
+    if constexpr (A == LORA_ACT_GELU_TANH)
+        return __fdividef(v, 1.0f + __expf(-GELU_C2 * (v + GELU_A * v * v * v)));
+    return v;
+}
+
+// act(v) and act'(v).
+template <int A>
+__device__ __forceinline__ void act_both(float v, float &y, float &dy) {
+    if constexpr (A == LORA_ACT_RELU) {
+        y = v < 0.0f ? 0.0f : v;
+        dy = v > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (A == LORA_ACT_SILU) {
+        const float s = logistic(v);
+        y = v * s;
+        dy = s * (1.0f + v * (1.0f - s));
+    } else if constexpr (A == LORA_ACT_GELU) {
+        const float cdf = 0.5f * (1.0f + erff(v * INV_SQRT2));
+        y = v * cdf;
+        dy = cdf + v * INV_SQRT_2PI * __expf(-0.5f * v * v);
+    } else if constexpr (A == LORA_ACT_GELU_TANH) {
+        // beyond |v| = 100 s is exactly 0 or 1 and the derivative with it; the bound keeps
+        // 0 * v^3 from becoming 0 * inf
+        const float b = fabsf(v) > 100.0f ? copysignf(100.0f, v) : v;
+        const float s = logistic(GELU_C2 * (b + GELU_A * b * b * b));
+        y = v * s;
+        dy = s * (1.0f + b * (1.0f - s) * GELU_C2 * (1.0f + 3.0f * GELU_A * b * b));
+    } else {
+        y = v;
+        dy = 1.0f;
+    }
+}
+
+}  // namespace lora

@@ -29,6 +29,7 @@
 #include <vector>
 
 #include "../../include/lora_linear.h"
+#include "block.h"
 #include "side.cuh"
 #include "tc_gemm.cuh"
 #include "tc_gemm2.cuh"
@@ -202,11 +203,11 @@ constexpr int pair_stages() {
     return (WF == WF_Q4 || WF == WF_CB) ? PAIR_STAGES_Q4 : WF == WF_FP8 ? PAIR_STAGES_FP8 : PAIR_STAGES;
 }
 
-template <bool B_MN, int WF>
+template <bool B_MN, int WF, int OP = OP_STORE>
 cudaError_t launch_pair(const GemmArgs &args, int grid, cudaStream_t st, DevInfo *dev, int attr_bit, int kind) {
     constexpr int S = pair_stages<WF>();
     using Cfg = PairCfg<B_MN, WF, S>;
-    auto kern = k_tc_gemm_pair<B_MN, WF, S>;
+    auto kern = k_tc_gemm_pair<B_MN, WF, S, OP>;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!(dev->attr_set & (1ull << attr_bit))) {
@@ -397,6 +398,7 @@ enum {
     AB_PAIR_K = 12, AB_PAIR_MN = 13, AB_PAIR_K_Q4 = 14, AB_PAIR_MN_Q4 = 15,
     AB_SIDE_XA = 16, AB_SIDE_GDB = 17, AB_SIDE_DA = 18,
     AB_PAIR_K_FP8 = 19, AB_PAIR_MN_FP8 = 20, AB_PAIR_K_CB = 21, AB_PAIR_MN_CB = 22,
+    AB_PAIR_ACT = 23, AB_PAIR_GLU = 27,  // + the weight format (0..3)
 };
 
 int bn_class_kmajor(int r) { return r <= 16 ? 16 : r <= 64 ? 64 : r <= 128 ? 128 : 256; }
@@ -926,7 +928,24 @@ struct MainOperands {
     int64_t q_rows = 0, q_cols = 0;    // W shape [d_out, d_in]
     int wf = WF_BF16;
     const float *codebook = nullptr;   // 4-bit codebook weight: its 16 values (host)
+    // fused epilogue (PairOp): activation, bias [N], residual [M, N], and where the
+    // pre-activations go (OP_ACT [M, N]; OP_GLU [M, 2 N]), each optional
+    int op = OP_STORE;
+    int act = LORA_ACT_NONE;
+    const uint16_t *bias = nullptr, *residual = nullptr;
+    uint16_t *save = nullptr;
 };
+
+template <int OP>
+cudaError_t launch_pair_fused(int wf, const GemmArgs &a, int grid, cudaStream_t st, DevInfo *dev, int kind) {
+    const int ab = (OP == OP_GLU ? AB_PAIR_GLU : AB_PAIR_ACT) + wf;
+    switch (wf) {
+        case WF_Q4: return launch_pair<false, WF_Q4, OP>(a, grid, st, dev, ab, kind);
+        case WF_FP8: return launch_pair<false, WF_FP8, OP>(a, grid, st, dev, ab, kind);
+        case WF_CB: return launch_pair<false, WF_CB, OP>(a, grid, st, dev, ab, kind);
+        default: return launch_pair<false, WF_BF16, OP>(a, grid, st, dev, ab, kind);
+    }
+}
 
 // `idle_sms` (optional) receives how many SMs the last wave leaves without work.
 // `ksplit`: cut a partial last wave along K (bf16 weight, workspace permitting) rather
@@ -942,7 +961,22 @@ lora_status_t step_main(const Ctx &c, const MainOperands &o, int64_t M, int64_t 
     if (!tmap_bf16(&a.tmC, o.C, N, M, 64, 32)) return LORA_ERR_CUDA;
     const bool q4 = o.wf != WF_BF16;  // codes decoded in shared memory (4-bit or FP8)
     const int pair_C = pair_enabled() ? std::min(pair_clusters(c.info, b_mn, o.wf), PLAN_SMS / 2) : 0;
-    if (q4 && pair_C == 0) return LORA_ERR_UNSUPPORTED;  // decoded weights run on CTA pairs only
+    // decoded weights and fused epilogues run on CTA pairs only
+    if ((q4 || o.op != OP_STORE) && pair_C == 0) return LORA_ERR_UNSUPPORTED;
+    const int64_t b_rows = o.op == OP_GLU ? 2 * N : N;  // rows of W and B (forward)
+    if (o.op != OP_STORE) {
+        a.act = o.act;
+        a.out_cols = static_cast<int>(N);
+        a.out_rows = static_cast<int>(M);
+        a.bias = o.bias;
+        a.residual = o.residual;
+        a.save = o.save ? 1 : 0;
+        if (o.save) {
+            if (!lora_host::tmap_2d_bf16_ld(&a.tmS0, o.save, N, M, b_rows, 64, 32)) return LORA_ERR_CUDA;
+            if (o.op == OP_GLU && !lora_host::tmap_2d_bf16_ld(&a.tmS1, o.save + N, N, M, b_rows, 64, 32))
+                return LORA_ERR_CUDA;
+        }
+    }
     if (q4) {
         a.wscale = o.Wscale;
         a.scale_ld = o.wf == WF_FP8 ? 1 : static_cast<int>(o.q_cols / 64);
@@ -957,9 +991,10 @@ lora_status_t step_main(const Ctx &c, const MainOperands &o, int64_t M, int64_t 
     }
     if (pair_C > 0) {
         // CTA pairs: 256 x 256 tiles, each CTA stages 128 rows of B.
-        const int64_t T = cdiv(M, PAIR_BM) * cdiv(N, PAIR_BN);
+        const int bn = pair_out_cols(o.op);
+        const int64_t T = cdiv(M, PAIR_BM) * cdiv(N, bn);
         a.m_tiles = static_cast<int>(cdiv(M, PAIR_BM));
-        a.n_tiles = static_cast<int>(cdiv(N, PAIR_BN));
+        a.n_tiles = static_cast<int>(cdiv(N, bn));
         a.num_tiles = static_cast<int>(T);
         a.group_m = std::min(a.m_tiles, 8);
         const int64_t W = T / pair_C, R = T % pair_C;
@@ -987,17 +1022,21 @@ lora_status_t step_main(const Ctx &c, const MainOperands &o, int64_t M, int64_t 
             }
             if (!tmap_bf16(&a.tmB1, o.B1, N, r, 64, 64)) return LORA_ERR_CUDA;
         } else {
-            if (!q4 && !tmap_bf16(&a.tmB0, o.B0, K0, N, 64, CTA_BN)) return LORA_ERR_CUDA;
-            if (!tmap_bf16(&a.tmB1, o.B1, r, N, 64, CTA_BN)) return LORA_ERR_CUDA;
+            if (!q4 && !tmap_bf16(&a.tmB0, o.B0, K0, b_rows, 64, CTA_BN)) return LORA_ERR_CUDA;
+            if (!tmap_bf16(&a.tmB1, o.B1, r, b_rows, 64, CTA_BN)) return LORA_ERR_CUDA;
             if (split) {
-                if (!tmap_bf16(&a.tmB0n, o.B0, K0, N, 64, CTA_BN / 2)) return LORA_ERR_CUDA;
-                if (!tmap_bf16(&a.tmB1n, o.B1, r, N, 64, CTA_BN / 2)) return LORA_ERR_CUDA;
+                if (!tmap_bf16(&a.tmB0n, o.B0, K0, b_rows, 64, CTA_BN / 2)) return LORA_ERR_CUDA;
+                if (!tmap_bf16(&a.tmB1n, o.B1, r, b_rows, 64, CTA_BN / 2)) return LORA_ERR_CUDA;
             }
         }
         const int clusters = split || kcut ? pair_C : static_cast<int>(std::min<int64_t>(T, pair_C));
         if (idle_sms) *idle_sms = (!split && R > 0 && W >= 1) ? c.info->sms - static_cast<int>(2 * R) : 0;
         cudaError_t e;
-        if (o.wf == WF_Q4)
+        if (o.op == OP_ACT)
+            e = launch_pair_fused<OP_ACT>(o.wf, a, 2 * clusters, c.st, c.info, kind);
+        else if (o.op == OP_GLU)
+            e = launch_pair_fused<OP_GLU>(o.wf, a, 2 * clusters, c.st, c.info, kind);
+        else if (o.wf == WF_Q4)
             e = b_mn ? launch_pair<true, WF_Q4>(a, 2 * clusters, c.st, c.info, AB_PAIR_MN_Q4, kind)
                      : launch_pair<false, WF_Q4>(a, 2 * clusters, c.st, c.info, AB_PAIR_K_Q4, kind);
         else if (o.wf == WF_FP8)
@@ -1092,9 +1131,18 @@ MainOperands main_operands(const Weight &wt, const void *A0, const void *A1, con
     return o;
 }
 
+// A forward's fused epilogue: OP_STORE for the layer itself.
+struct Fused {
+    int op = OP_STORE;
+    int act = LORA_ACT_NONE;
+    const uint16_t *bias = nullptr, *residual = nullptr;
+    uint16_t *save = nullptr;
+};
+
+// d_out: rows of W (OP_GLU: twice the output's columns).
 lora_status_t fwd_impl(const uint16_t *x, const Weight &wt, const uint16_t *A, const uint16_t *B, uint16_t *h,
                        uint16_t *xa_save, int64_t M, int64_t d_in, int64_t d_out, int r, float alpha, void *ws,
-                       size_t ws_bytes, void *stream) {
+                       size_t ws_bytes, void *stream, const Fused &fu = Fused()) {
     LORA_TRY(check_shapes(M, d_in, d_out, r, alpha, wt.wf));
     if (!x || !wt.present() || !A || !B || !h) return LORA_ERR_INVALID_ARG;
     if (wt.wf == WF_CB)
@@ -1108,13 +1156,22 @@ lora_status_t fwd_impl(const uint16_t *x, const Weight &wt, const uint16_t *A, c
     const float s = alpha / static_cast<float>(r);
     uint16_t *sxa = xa_save ? xa_save : reinterpret_cast<uint16_t *>(c.ws + c.plan.xa);
     LORA_TRY(c.plan.side ? side_xa(c, x, A, sxa, M, d_in, r, s) : step_xa(c, x, A, sxa, M, d_in, r, s));
-    const MainOperands o = main_operands(wt, x, sxa, B, h, d_out, d_in);
-    return step_main(c, o, M, d_out, d_in, r, false, LORA_K_FWD_MAIN, c.plan.fwd_tail, nullptr, c.plan.fwd_ksplit);
+    MainOperands o = main_operands(wt, x, sxa, B, h, d_out, d_in);
+    o.op = fu.op;
+    o.act = fu.act;
+    o.bias = fu.bias;
+    o.residual = fu.residual;
+    o.save = fu.save;
+    return step_main(c, o, M, fu.op == OP_GLU ? d_out / 2 : d_out, d_in, r, false, LORA_K_FWD_MAIN, c.plan.fwd_tail,
+                     nullptr, c.plan.fwd_ksplit);
 }
 
-lora_status_t bwd_impl(const uint16_t *dY, const uint16_t *x, const Weight &wt, const uint16_t *A,
-                       const uint16_t *B, const uint16_t *xa_save, uint16_t *dX, float *dA, float *dB, int64_t M,
-                       int64_t d_in, int64_t d_out, int r, float alpha, void *ws, size_t ws_bytes, void *stream) {
+// Everything bwd_impl validates, without a launch: an operator that enqueues work before
+// the layer's backward asks here first.
+lora_status_t check_bwd(const uint16_t *dY, const uint16_t *x, const Weight &wt, const uint16_t *A, const uint16_t *B,
+                        const uint16_t *xa_save, uint16_t *dX, float *dA, float *dB, int64_t M, int64_t d_in,
+                        int64_t d_out, int r, float alpha, void *ws, size_t ws_bytes, Ctx *c = nullptr,
+                        void *stream = nullptr) {
     LORA_TRY(check_shapes(M, d_in, d_out, r, alpha, wt.wf));
     if (!dY || !x || !wt.present() || !A || !B || !dA || !dB) return LORA_ERR_INVALID_ARG;
     if (wt.wf == WF_CB)
@@ -1123,8 +1180,18 @@ lora_status_t bwd_impl(const uint16_t *dY, const uint16_t *x, const Weight &wt, 
     if (!aligned16(dY) || !aligned16(x) || !wt.aligned() || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
         !aligned16(dB) || (xa_save && !aligned16(xa_save)) || (dX && !aligned16(dX)))
         return LORA_ERR_MISALIGNED;
+    Ctx own;
+    LORA_TRY(prepare(wt.op_bwd(), M, d_in, d_out, r, ws, ws_bytes, stream, c ? c : &own));
+    if (wt.coded() && dX && (!pair_enabled() || pair_clusters((c ? c : &own)->info, true, wt.wf) == 0))
+        return LORA_ERR_UNSUPPORTED;  // decoded weights run on CTA pairs only
+    return LORA_OK;
+}
+
+lora_status_t bwd_impl(const uint16_t *dY, const uint16_t *x, const Weight &wt, const uint16_t *A,
+                       const uint16_t *B, const uint16_t *xa_save, uint16_t *dX, float *dA, float *dB, int64_t M,
+                       int64_t d_in, int64_t d_out, int r, float alpha, void *ws, size_t ws_bytes, void *stream) {
     Ctx c;
-    LORA_TRY(prepare(wt.op_bwd(), M, d_in, d_out, r, ws, ws_bytes, stream, &c));
+    LORA_TRY(check_bwd(dY, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, d_out, r, alpha, ws, ws_bytes, &c, stream));
     const float s = alpha / static_cast<float>(r);
     const uint16_t *sxa = xa_save;
     if (!sxa) {
@@ -1169,7 +1236,48 @@ lora_status_t bwd_impl(const uint16_t *dY, const uint16_t *x, const Weight &wt, 
     return LORA_OK;
 }
 
+// ------------------------------------------------------------------ operators around the layer
+// A lora_weight_t as the layer's Weight.
+lora_status_t to_weight(const lora_weight_t *w, Weight *out) {
+    if (!w || !w->data || w->format < LORA_W_BF16 || w->format > LORA_W_NF4) return LORA_ERR_INVALID_ARG;
+    out->wf = w->format;  // the same codes: bf16, 4-bit, FP8, codebook
+    static_assert(LORA_W_BF16 == int(WF_BF16) && LORA_W_Q4 == int(WF_Q4) && LORA_W_FP8 == int(WF_FP8) &&
+                  LORA_W_NF4 == int(WF_CB), "format codes");
+    if (w->format == LORA_W_BF16) {
+        out->W = static_cast<const uint16_t *>(w->data);
+        return LORA_OK;
+    }
+    if (!w->scale || (w->format == LORA_W_NF4 && !w->codebook)) return LORA_ERR_INVALID_ARG;
+    out->Wq = static_cast<const uint8_t *>(w->data);
+    out->Wscale = w->scale;
+    if (w->format == LORA_W_NF4) out->codebook = w->codebook;
+    return LORA_OK;
+}
+
+bool valid_act(int act) { return act >= LORA_ACT_NONE && act <= LORA_ACT_GELU_TANH; }
+
+// Where lora_linear_act_bwd's own part of the workspace lies: arrival counters and bias
+// partials behind the layer's part.
+struct ActBwdLayout {
+    size_t counters = 0, partials = 0, total = 0;
+    lora_host::BiasPlan bp;
+};
+
+ActBwdLayout act_bwd_layout(size_t layer_bytes, int64_t M, int64_t d_out) {
+    ActBwdLayout l;
+    l.bp = lora_host::bias_plan(M, d_out, PLAN_SMS);
+    l.counters = align256(layer_bytes);
+    l.partials = align256(l.counters + static_cast<size_t>(l.bp.col_blocks) * sizeof(int));
+    l.total = align256(l.partials + static_cast<size_t>(l.bp.chunks) * d_out * sizeof(float));
+    return l;
+}
+
 }  // namespace
+
+namespace lora_host {
+void count_launch() { g_launches.fetch_add(1); }
+bool programmatic_launch() { return pdl_enabled(); }
+}  // namespace lora_host
 
 // ====================================================================== C ABI
 extern "C" {
@@ -1353,6 +1461,91 @@ lora_status_t lora_linear_bwd_nf4(const uint16_t *dY, const uint16_t *x, const u
     if (!Wq || !Wscale || !codebook) return LORA_ERR_INVALID_ARG;
     return bwd_impl(dY, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, d_out, r, alpha, workspace, workspace_bytes,
                     stream);
+}
+
+lora_status_t lora_glu_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A, const uint16_t *B, uint16_t *p,
+                           uint16_t *gu_save, uint16_t *xa_save, int64_t M, int64_t d_in, int64_t d_ff, int r,
+                           float alpha, int act, void *workspace, size_t workspace_bytes, void *stream) {
+    Weight wt;
+    LORA_TRY(to_weight(W, &wt));
+    if (!valid_act(act) || d_ff < 8 || d_ff % 8 || d_ff > (int64_t(1) << 23)) return LORA_ERR_INVALID_ARG;
+    if (gu_save && !aligned16(gu_save)) return LORA_ERR_MISALIGNED;
+    Fused fu;
+    fu.op = OP_GLU;
+    fu.act = act;
+    fu.save = gu_save;
+    return fwd_impl(x, wt, A, B, p, xa_save, M, d_in, 2 * d_ff, r, alpha, workspace, workspace_bytes, stream, fu);
+}
+
+lora_status_t lora_glu_bwd(const uint16_t *dP, const uint16_t *gu, const uint16_t *x, const lora_weight_t *W,
+                           const uint16_t *A, const uint16_t *B, const uint16_t *xa_save, uint16_t *dGU, uint16_t *dX,
+                           float *dA, float *dB, int64_t M, int64_t d_in, int64_t d_ff, int r, float alpha, int act,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    Weight wt;
+    LORA_TRY(to_weight(W, &wt));
+    if (!valid_act(act) || d_ff < 8 || d_ff % 8 || d_ff > (int64_t(1) << 23)) return LORA_ERR_INVALID_ARG;
+    if (!dP || !gu || !dGU || gu == dGU) return LORA_ERR_INVALID_ARG;
+    if (!aligned16(dP) || !aligned16(gu) || !aligned16(dGU)) return LORA_ERR_MISALIGNED;
+    LORA_TRY(check_bwd(dGU, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, 2 * d_ff, r, alpha, workspace, workspace_bytes));
+    if (lora_host::launch_glu_bwd(dP, gu, dGU, M, d_ff, act, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return LORA_ERR_CUDA;
+    return bwd_impl(dGU, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, 2 * d_ff, r, alpha, workspace, workspace_bytes,
+                    stream);
+}
+
+lora_status_t lora_linear_act_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A, const uint16_t *B,
+                                  const uint16_t *bias, const uint16_t *residual, uint16_t *out, uint16_t *pre_save,
+                                  uint16_t *xa_save, int64_t M, int64_t d_in, int64_t d_out, int r, float alpha,
+                                  int act, void *workspace, size_t workspace_bytes, void *stream) {
+    Weight wt;
+    LORA_TRY(to_weight(W, &wt));
+    if (!valid_act(act)) return LORA_ERR_INVALID_ARG;
+    if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (pre_save && !aligned16(pre_save)))
+        return LORA_ERR_MISALIGNED;
+    Fused fu;
+    fu.op = OP_ACT;
+    fu.act = act;
+    fu.bias = bias;
+    fu.residual = residual;
+    fu.save = pre_save;
+    return fwd_impl(x, wt, A, B, out, xa_save, M, d_in, d_out, r, alpha, workspace, workspace_bytes, stream, fu);
+}
+
+lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t *pre, const uint16_t *x, const lora_weight_t *W,
+                                  const uint16_t *A, const uint16_t *B, const uint16_t *xa_save, uint16_t *dPre,
+                                  uint16_t *dX, float *dA, float *dB, float *dbias, int64_t M, int64_t d_in,
+                                  int64_t d_out, int r, float alpha, int act, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    Weight wt;
+    LORA_TRY(to_weight(W, &wt));
+    if (!valid_act(act) || !dOut) return LORA_ERR_INVALID_ARG;
+    const bool has_act = act != LORA_ACT_NONE;
+    if (has_act && (!pre || !dPre || dPre == dOut || dPre == pre)) return LORA_ERR_INVALID_ARG;
+    if (!aligned16(dOut) || (has_act && (!aligned16(pre) || !aligned16(dPre))) || (dbias && !aligned16(dbias)))
+        return LORA_ERR_MISALIGNED;
+    const uint16_t *dY = has_act ? dPre : dOut;
+    LORA_TRY(check_bwd(dY, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, d_out, r, alpha, workspace, workspace_bytes));
+    const size_t layer = lora_linear_workspace_size(wt.op_bwd(), M, d_in, d_out, r);
+    if (has_act || dbias) {
+        const ActBwdLayout l = act_bwd_layout(layer, M, d_out);
+        if (dbias && workspace_bytes < l.total) return LORA_ERR_WORKSPACE;
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        if (lora_host::launch_act_bwd(dOut, pre, has_act ? dPre : nullptr, dbias,
+                                      reinterpret_cast<float *>(ws + l.partials),
+                                      reinterpret_cast<int *>(ws + l.counters), M, d_out, act, l.bp,
+                                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return LORA_ERR_CUDA;
+    }
+    // the layer's part alone, so that its plan does not depend on what follows it
+    return bwd_impl(dY, x, wt, A, B, xa_save, dX, dA, dB, M, d_in, d_out, r, alpha, workspace,
+                    std::min(workspace_bytes, layer), stream);
+}
+
+size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r) {
+    const size_t layer = lora_linear_workspace_size(op, M, d_in, d_out, r);
+    if (layer == 0) return 0;
+    const bool bwd = op == LORA_OP_BWD || op == LORA_OP_BWD_Q4 || op == LORA_OP_BWD_FP8 || op == LORA_OP_BWD_NF4;
+    return bwd ? act_bwd_layout(layer, M, d_out).total : layer;
 }
 
 lora_status_t lora_linear_check(void *workspace, void *stream) {

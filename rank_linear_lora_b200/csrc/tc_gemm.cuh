@@ -119,6 +119,16 @@ struct GemmArgs {
     // CTA's 128 weight columns of a K block come in one copy instead of two; tmB0n is
     // then the weight's 2D map {64, 64}, for the 64-column halves of split tail tiles.
     int b3d;
+    // CTA-pair GEMM with a fused epilogue (PairOp): the activation code, the output
+    // column count (rows of the bias, extent of a residual row), the optional bias [n]
+    // and residual [M, n] (bf16), whether the pre-activations are stored too, and their
+    // maps (tmS0: pre-activations or the gate half, tmS1: the up half).
+    int act;
+    int out_cols, out_rows;
+    int save;
+    const uint16_t *bias;
+    const uint16_t *residual;
+    CUtensorMap tmS0, tmS1;
 };
 
 // Release / acquire of a global int at GPU scope (the K-split tail's hand-over).

@@ -30,6 +30,7 @@
 // brackets the work.
 #pragma once
 
+#include "act.cuh"
 #include "tc_gemm.cuh"
 
 namespace lora {
@@ -72,6 +73,17 @@ __host__ __device__ constexpr int dq_index(int w) {
     for (int v = 6; v < w; ++v) i += dq_idle_warp(v) ? 0 : 1;
     return i;
 }
+
+// What the epilogue makes of the accumulator:
+//   OP_STORE  the tile itself
+//   OP_ACT    act(acc + bias) + residual (each part optional), the pre-activation stored
+//             as well when asked for
+//   OP_GLU    act(gate) * up.  W holds the gate rows and then the up rows; the pair's first
+//             CTA stages 128 gate rows as its half of B and the second the 128 up rows of
+//             the same columns, so both halves of a column meet in one TMEM row and the
+//             product needs no exchange.  A tile is 128 output columns wide.
+enum PairOp { OP_STORE = 0, OP_ACT = 1, OP_GLU = 2 };
+__host__ __device__ constexpr int pair_out_cols(int op) { return op == OP_GLU ? 128 : 256; }
 
 template <bool B_MN, int WF, int STAGES>
 struct PairCfg {
@@ -208,6 +220,7 @@ __device__ __forceinline__ uint4 cb_decode8(const CbTable &t, uint32_t word) {
 }
 
 // Item i of this cluster: pair tile (m, n), its first output column and width split.
+template <int OP = OP_STORE>
 __device__ __forceinline__ bool get_pair_item(const GemmArgs &p, int cluster, int n_clusters, int i, WorkItem &w) {
     w.kb_lo = 0;
     w.kb_hi = p.kb0 + p.kb1;
@@ -227,7 +240,7 @@ __device__ __forceinline__ bool get_pair_item(const GemmArgs &p, int cluster, in
                 w.kb_hi = (cluster & 1) ? kb_all : kb_mid;
                 w.piece = 1 + (cluster & 1);
                 w.job = tt;
-                w.col0 = w.n * PAIR_BN;
+                w.col0 = w.n * pair_out_cols(OP);
                 return true;
             }
             --i;
@@ -236,7 +249,7 @@ __device__ __forceinline__ bool get_pair_item(const GemmArgs &p, int cluster, in
             const int t = cluster + i * n_clusters;
             if (t >= p.dp_tiles) return false;
             raster(p, t, w.m, w.n);
-            w.col0 = w.n * PAIR_BN;
+            w.col0 = w.n * pair_out_cols(OP);
             return true;
         }
         return false;
@@ -245,20 +258,246 @@ __device__ __forceinline__ bool get_pair_item(const GemmArgs &p, int cluster, in
         const int t = cluster + i * n_clusters;
         if (t >= p.dp_tiles) return false;
         raster(p, t, w.m, w.n);
-        w.col0 = w.n * PAIR_BN;
+        w.col0 = w.n * pair_out_cols(OP);
         return true;
     }
     if (i == p.dp_waves && p.tail_split > 1 && cluster < p.tail_tiles * p.tail_split) {
         const int tt = cluster / p.tail_split, h = cluster % p.tail_split;
         raster(p, p.dp_tiles + tt, w.m, w.n);
         w.nsplit = p.tail_split;
-        w.col0 = w.n * PAIR_BN + h * (PAIR_BN / p.tail_split);
+        w.col0 = w.n * pair_out_cols(OP) + h * (pair_out_cols(OP) / p.tail_split);
         return true;
     }
     return false;
 }
 
-template <bool B_MN, int WF, int STAGES>
+// First weight row (row of W, B and the codes) that CTA `rank` stages for an item.
+template <int OP>
+__device__ __forceinline__ int pair_b_row(const GemmArgs &p, const WorkItem &w, int rank) {
+    if (OP == OP_GLU) return w.col0 + rank * p.out_cols;
+    return w.col0 + rank * ((PAIR_BN / w.nsplit) / 2);
+}
+
+// ------------------------------------------------------------------ fused epilogues (OP_ACT, OP_GLU)
+// W consecutive fp32 columns of this thread's accumulator row.
+template <int W>
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&v)[W]) {
+    if constexpr (W == 32) tmem_ld_32x32b_x32(taddr, v);
+    else tmem_ld_32x32b_x16(taddr, v);
+}
+
+// W columns (a multiple of 8), starting at column c0 of the 64, of row `lane` of the
+// 32 x 64 staging box: fp32 to bf16, 16-byte chunks swizzled as stage_row64's.
+template <int W>
+__device__ __forceinline__ void stage_cols(uint8_t *sbuf, int lane, int c0, const float (&v)[W]) {
+    uint8_t *row_ptr = sbuf + lane * 128;
+#pragma unroll
+    for (int g = 0; g < W / 8; ++g) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * g + 2 * e], v[8 * g + 2 * e + 1]);
+            w[e] = *reinterpret_cast<uint32_t *>(&b2);
+        }
+        const int cc = c0 / 8 + g;
+        *reinterpret_cast<uint4 *>(row_ptr + ((cc ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// 8 bf16 of a 16-byte load to fp32.
+__device__ __forceinline__ void bf16x8_to_f32(const uint4 &u, float *f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+}
+
+// K-split last-wave tile of a fused epilogue (the hand-over of OP_STORE's, see the kernel):
+// the first half writes its fp32 accumulator to the workspace; the second adds it to its
+// own in tensor memory, so that the epilogue proper reads whole sums.  False after a wait
+// that ran out.
+__device__ __forceinline__ bool ksplit_exchange(const GemmArgs &p, const WorkItem &w, int rank, uint32_t t_row, int q,
+                                                int lane, int epi_tid, uint32_t tempty, volatile int *abort_flag,
+                                                volatile int *ks_ok) {
+    constexpr uint32_t KS_BYTES = 4 * 16 * 128 * 16;
+    const int slot = w.job * 2 + rank;
+    float4 *part = reinterpret_cast<float4 *>(p.ks_part) + static_cast<size_t>(slot) * (KS_BYTES / 16) + q * 32 + lane;
+    if (w.piece == 1) {
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(t_row + ch * 32, v);
+            tc_wait_ld();
+            if (ch == 7) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty);
+            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                __stcg(part + (ch * 8 + g) * 128,
+                       make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                   __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3])));
+        }
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (epi_tid == 0) st_release_gpu(p.ks_flag + slot, 1);
+        return true;
+    }
+    if (epi_tid == 0) {
+        const bool ok = wait_flag_bounded(p.ks_flag + slot, abort_flag, p.err, DERR_WAIT_PARTIAL);
+        if (ok) p.ks_flag[slot] = 0;  // zero again for the next call
+        *ks_ok = ok ? 1 : 0;
+    }
+    named_bar_sync(1, 128);
+    if (!*ks_ok) return false;
+#pragma unroll 1
+    for (int ch = 0; ch < 8; ++ch) {
+        float4 o[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) o[g] = __ldcg(part + (ch * 8 + g) * 128);
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(t_row + ch * 32, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + o[g].x);
+            v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + o[g].y);
+            v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + o[g].z);
+            v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + o[g].w);
+        }
+        tmem_st_32x32b_x32(t_row + ch * 32, v);
+    }
+    tc_wait_st();
+    return true;
+}
+
+// The epilogue of one item: this warp's 32 rows from `row0`, the item's columns from
+// w.col0, 64 at a time.  Each 64-column box of each output goes through one of the warp's
+// two staging buffers and a TMA store, which also clips rows and columns outside the
+// output.  The accumulator is read once per output (tensor memory is far faster than the
+// stores), W columns at a time: 32, or 16 where the dequant warps leave fewer registers.
+// The tile's TMEM is released right after the last read.
+template <int OP, bool DQ>
+__device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem &w, int row0, uint32_t t_row, int lane,
+                                               uint32_t tempty, uint8_t *stage_base) {
+    constexpr int W = DQ ? 16 : 32;
+    const int nch = (pair_out_cols(OP) / 64) / w.nsplit;
+    const int row = row0 + lane;
+    int n_out = 0;
+    // one 64-column box: fill(c, v, last) makes columns c .. c+W of the box
+    auto emit = [&](const CUtensorMap *tm, int col, auto &&fill) {
+        uint8_t *sbuf = stage_base + (n_out & 1) * (32 * 128);
+        ++n_out;
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 64; c += W) {
+            float v[W];
+            fill(c, v);
+            stage_cols<W>(sbuf, lane, c, v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tm, smem_u32(sbuf), col, row0);
+            bulk_commit_group();
+        }
+    };
+    auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty);
+    };
+    if constexpr (OP == OP_GLU) {
+        const int up0 = PAIR_BN / 2 / w.nsplit;  // TMEM column of the up half
+#pragma unroll 1
+        for (int ch = 0; ch < nch; ++ch) {
+            const int col = w.col0 + ch * 64;
+            if (p.save) {
+                for (int half = 0; half < 2; ++half)
+                    emit(half ? &p.tmS1 : &p.tmS0, col, [&](int c, float(&v)[W]) {
+                        uint32_t a[W];
+                        tmem_ld_row<W>(t_row + half * up0 + ch * 64 + c, a);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
+                    });
+            }
+            emit(&p.tmC, col, [&](int c, float(&v)[W]) {
+                uint32_t g[W], u[W];
+                tmem_ld_row<W>(t_row + ch * 64 + c, g);
+                tmem_ld_row<W>(t_row + up0 + ch * 64 + c, u);
+                tc_wait_ld();
+                if (ch == nch - 1 && c + W == 64) release();
+                act_dispatch(p.act, [&](auto A) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[e] = act_value<A.value>(__uint_as_float(g[e])) * __uint_as_float(u[e]);
+                });
+            });
+        }
+    } else {
+        // bias and residual, 8 columns a load; columns and rows outside the output read nothing
+        auto add8 = [&](const uint16_t *src, int col, float *v) {
+            if (col < p.out_cols) {
+                float f[8];
+                bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(src + col)), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += f[e];
+            }
+        };
+        const uint16_t *res_row = p.residual && row < p.out_rows
+                                      ? p.residual + static_cast<int64_t>(row) * p.out_cols : nullptr;
+#pragma unroll 1
+        for (int ch = 0; ch < nch; ++ch) {
+            const int col = w.col0 + ch * 64;
+            if (p.save)
+                emit(&p.tmS0, col, [&](int c, float(&v)[W]) {
+                    uint32_t a[W];
+                    tmem_ld_row<W>(t_row + ch * 64 + c, a);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
+                    if (p.bias)
+#pragma unroll
+                        for (int e = 0; e < W; e += 8) add8(p.bias, col + c + e, v + e);
+                });
+            emit(&p.tmC, col, [&](int c, float(&v)[W]) {
+                uint4 r[W / 8];
+#pragma unroll
+                for (int e = 0; e < W / 8; ++e)
+                    r[e] = res_row && col + c + 8 * e < p.out_cols
+                               ? __ldcg(reinterpret_cast<const uint4 *>(res_row + col + c + 8 * e))
+                               : make_uint4(0, 0, 0, 0);
+                __syncwarp();  // rows past the output took the other branch; the TMEM load is warp-wide
+                uint32_t a[W];
+                tmem_ld_row<W>(t_row + ch * 64 + c, a);
+                tc_wait_ld();
+                if (ch == nch - 1 && c + W == 64) release();
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
+                if (p.bias)
+#pragma unroll
+                    for (int e = 0; e < W; e += 8) add8(p.bias, col + c + e, v + e);
+                act_dispatch(p.act, [&](auto A) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[e] = act_value<A.value>(v[e]);
+                });
+#pragma unroll
+                for (int e = 0; e < W / 8; ++e) {
+                    float f[8];
+                    bf16x8_to_f32(r[e], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[8 * e + j] += f[j];
+                }
+            });
+        }
+    }
+}
+
+template <bool B_MN, int WF, int STAGES, int OP = OP_STORE>
 __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
     k_tc_gemm_pair(const __grid_constant__ GemmArgs p) {
     using Cfg = PairCfg<B_MN, WF, STAGES>;
@@ -329,6 +568,10 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             tma_prefetch_desc(&p.tmB1);
         }
         tma_prefetch_desc(&p.tmC);
+        if (OP != OP_STORE && p.save) {
+            tma_prefetch_desc(&p.tmS0);
+            if (OP == OP_GLU) tma_prefetch_desc(&p.tmS1);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(tmem_slot), Cfg::TMEM_COLS);
@@ -356,10 +599,10 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             uint64_t wait_empty_ns = 0;
             uint32_t flat = 0;  // K blocks of the CTA's sequence handled so far
             WorkItem w;
-            for (int i = 0; ok && get_pair_item(p, cluster, n_clusters, i, w); ++i) {
+            for (int i = 0; ok && get_pair_item<OP>(p, cluster, n_clusters, i, w); ++i) {
                 const int bn_cta = (PAIR_BN / w.nsplit) / 2;  // B rows this CTA stages
                 const int a_row = w.m * PAIR_BM + static_cast<int>(rank) * 128;
-                const int b_row = w.col0 + static_cast<int>(rank) * bn_cta;
+                const int b_row = pair_b_row<OP>(p, w, static_cast<int>(rank));
                 for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
                     // decoded weight: the weight segment's B tiles are written by the dequant warps, so the
                     // leader's full barrier then counts A only; rank-r tail B tiles come by TMA.
@@ -443,7 +686,7 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             long long wait_a_cyc = 0, wait_b_cyc = 0;
             uint32_t bready_phase = 0;  // decoded weight: bit s = parity of the next B-ready completion of stage s
             WorkItem w;
-            for (; ok && get_pair_item(p, cluster, n_clusters, it, w); ++it) {
+            for (; ok && get_pair_item<OP>(p, cluster, n_clusters, it, w); ++it) {
                 const int buf = it & 1;
                 const uint32_t aphase = (it >> 1) & 1;
                 const uint64_t tt = trace ? globaltimer_ns() : 0;
@@ -553,8 +796,8 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         };
         auto enter_item = [&](Cursor &c) {
             WorkItem wi;
-            c.valid = get_pair_item(p, cluster, n_clusters, c.item, wi);
-            c.b_row = c.valid ? wi.col0 + static_cast<int>(rank) * ((PAIR_BN / wi.nsplit) / 2) : 0;
+            c.valid = get_pair_item<OP>(p, cluster, n_clusters, c.item, wi);
+            c.b_row = c.valid ? pair_b_row<OP>(p, wi, static_cast<int>(rank)) : 0;
         };
         auto seek = [&](Cursor &c, int j) {
             const int wit = grp + j * DQ_GROUPS;
@@ -717,7 +960,7 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty_bar[1]), 0);
         int it = 0;
         WorkItem w;
-        for (; get_pair_item(p, cluster, n_clusters, it, w); ++it) {
+        for (; get_pair_item<OP>(p, cluster, n_clusters, it, w); ++it) {
             const int buf = it & 1;
             const uint32_t aphase = (it >> 1) & 1;
             if (epi_tid == 0)
@@ -726,6 +969,23 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             named_bar_sync(1, 128);
             if (!epi_ok[it & 1]) break;
             tc_fence_after();
+            if constexpr (OP != OP_STORE) {
+                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(buf * PAIR_BN);
+                const uint32_t tempty = buf ? tempty_leader1 : tempty_leader0;
+                if (!DQ && w.piece > 0) {
+                    if (!ksplit_exchange(p, w, static_cast<int>(rank), t_row, q, lane, epi_tid, tempty, abort_flag, ks_ok))
+                        break;
+                    if (w.piece == 1) {
+                        if (trace && epi_tid == 0 && it < 8) trace[TR_TILE_DONE0 + it] = globaltimer_ns();
+                        continue;
+                    }
+                }
+                fused_epilogue<OP, DQ>(p, w, w.m * PAIR_BM + static_cast<int>(rank) * 128 + q * 32, t_row, lane,
+                                       tempty, sEpi + (q * Cfg::EPI_BUFS) * (32 * 128));
+                if (trace && epi_tid == 0 && it < 8) trace[TR_TILE_DONE0 + it] = globaltimer_ns();
+                continue;
+            }
             if (!DQ && w.piece > 0) {
                 // Last-wave tile cut along K (both halves are their clusters' first items; the
                 // MMAs of the next tile run in the other TMEM accumulator meanwhile).  The first

@@ -42,6 +42,21 @@ inline bool tmap_2d(CUtensorMap *m, CUtensorMapDataType type, int esize, const v
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same of a column range of a wider row-major bf16 matrix: rows `ld` elements apart,
+// 128-byte swizzle.
+inline bool tmap_2d_bf16_ld(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t ld,
+                            uint32_t box_cols, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // MN-major bf16 operand [K rows][N cols] (N a multiple of 64) as the 3D tensor
 // {64 columns, K rows, N/64 column chunks}: one box {64, 64, 2} brings two 64-column chunks
 // of 64 K rows, chunk after chunk in shared memory (the layout of two 2D boxes {64, 64}),

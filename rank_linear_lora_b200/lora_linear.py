@@ -22,6 +22,9 @@ LORA_OK = 0
 STATUS = {0: "LORA_OK", 1: "LORA_ERR_INVALID_ARG", 2: "LORA_ERR_MISALIGNED", 3: "LORA_ERR_UNSUPPORTED",
           4: "LORA_ERR_WORKSPACE", 5: "LORA_ERR_CUDA", 6: "LORA_ERR_TIMEOUT"}
 OP_FWD, OP_BWD, OP_FWD_Q4, OP_BWD_Q4, OP_FWD_FP8, OP_BWD_FP8, OP_FWD_NF4, OP_BWD_NF4 = 0, 1, 2, 3, 4, 5, 6, 7
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # lora_act_t
+WEIGHT_FORMATS = {"bf16": 0, "q4": 1, "fp8": 2, "nf4": 3}                    # lora_weight_format_t
+HEAD_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}        # lora_dtype_t
 KERNEL_KINDS = ["xa", "fwd_main", "g", "dx_main", "dadb"]
 
 
@@ -55,6 +58,14 @@ def load_library():
     lib.lora_linear_bwd_fp8.argtypes = [P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, P, SZ, P]
     for f in ("lora_linear_fwd", "lora_linear_bwd", "lora_linear_fwd_q4", "lora_linear_bwd_q4", "lora_linear_fwd_fp8",
               "lora_linear_bwd_fp8", "lora_linear_fwd_nf4", "lora_linear_bwd_nf4"):
+        getattr(lib, f).restype = I
+    lib.lora_glu_fwd.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
+    lib.lora_glu_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
+    lib.lora_linear_act_fwd.argtypes = [P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
+    lib.lora_linear_act_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
+    lib.lora_linear_act_workspace_size.argtypes = [I, I64, I64, I64, I]
+    lib.lora_linear_act_workspace_size.restype = SZ
+    for f in ("lora_glu_fwd", "lora_glu_bwd", "lora_linear_act_fwd", "lora_linear_act_bwd"):
         getattr(lib, f).restype = I
     lib.lora_linear_check.argtypes = [P, P]
     lib.lora_linear_check.restype = I
@@ -499,3 +510,134 @@ def lora_linear_noalloc_selftest_timeout(limit_us: int = 1000, stream=None):
     fn.argtypes = [ctypes.c_uint32, ctypes.c_void_p]
     fn.restype = ctypes.c_int
     _check(fn(int(limit_us), _stream(stream)), "lora_linear_noalloc_selftest_timeout")
+
+
+# ---------------------------------------------------------------- operators around the layer
+class lora_weight_t(ctypes.Structure):
+    """A frozen weight in one of the storage formats (include/lora_linear.h)."""
+    _fields_ = [("format", ctypes.c_int32), ("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("codebook", ctypes.c_void_p)]
+
+
+def _weight(W):
+    """(lora_weight_t, d_out, d_in, what must outlive the call) of a bf16 tensor [d_out, d_in]
+    or of a weight with `kind`, `tensors` and `codebook` (autograd.FrozenWeight)."""
+    if isinstance(W, torch.Tensor):
+        if W.dim() != 2:
+            raise ValueError(f"W: expected a tensor [d_out, d_in], got shape {tuple(W.shape)}")
+        _bf16(W, "W", W.shape)
+        return lora_weight_t(0, W.data_ptr(), None, None), W.shape[0], W.shape[1], None
+    t = W.tensors
+    if W.kind == "bf16":
+        return _weight(t[0])
+    d_out, d_in = W.d_out, W.d_in
+    keep = cb = None
+    if W.kind == "fp8":
+        _fp8(t[0], t[1], d_out, d_in)
+    else:
+        _q4(t[0], t[1], d_out, d_in)
+        if W.kind == "nf4":
+            keep, cb = _codebook(W.codebook)
+    return lora_weight_t(WEIGHT_FORMATS[W.kind], t[0].data_ptr(), t[1].data_ptr(), cb), d_out, d_in, keep
+
+
+def _act(act) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act: one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def lora_linear_act_workspace_size(op: int, M: int, d_in: int, d_out: int, r: int) -> int:
+    return int(load_library().lora_linear_act_workspace_size(op, M, d_in, d_out, r))
+
+
+def act_workspace(op: int, M: int, d_in: int, d_out: int, r: int, device=None) -> torch.Tensor:
+    """A zeroed uint8 workspace for lora_linear_act_fwd / _bwd (torch allocates)."""
+    n = lora_linear_act_workspace_size(op, M, d_in, d_out, r)
+    if n == 0:
+        raise ValueError("invalid sizes for the workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def lora_glu_fwd(x, W, A, B, p, gu_save, xa_save, alpha, act, ws, stream=None):
+    """p = act(g) * u with [g | u] = x.W^T + s.(x.A^T).B^T; W: a bf16 tensor [2 d_ff, d_in]
+    or a FrozenWeight, the gate's rows first.  gu_save [M, 2 d_ff] and xa_save may be None."""
+    w, n, d_in, keep = _weight(W)
+    M, r = x.shape[0], A.shape[0]
+    for t, name, s in ((x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (p, "p", (M, n // 2))):
+        _bf16(t, name, s)
+    if n % 2:
+        raise ValueError(f"W: the gate's and the up projection's rows, got {n}")
+    if gu_save is not None:
+        _bf16(gu_save, "gu_save", (M, n))
+    if xa_save is not None:
+        _bf16(xa_save, "xa_save", (M, r))
+    st = load_library().lora_glu_fwd(_ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(p), _ptr(gu_save),
+                                     _ptr(xa_save), M, d_in, n // 2, r, float(alpha), _act(act), *_ws(ws),
+                                     _stream(stream))
+    del keep
+    _check(st, "lora_glu_fwd")
+
+
+def lora_glu_bwd(dP, gu, x, W, A, B, xa_save, dGU, dX, dA, dB, alpha, act, ws, stream=None):
+    """dGU = [dP * u * act'(g) | dP * act(g)] and the layer's dX (or None), dA, dB."""
+    w, n, d_in, keep = _weight(W)
+    M, r = x.shape[0], A.shape[0]
+    if n % 2:
+        raise ValueError(f"W: the gate's and the up projection's rows, got {n}")
+    for t, name, s in ((dP, "dP", (M, n // 2)), (gu, "gu", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)),
+                       (B, "B", (n, r)), (dGU, "dGU", (M, n))):
+        _bf16(t, name, s)
+    if xa_save is not None:
+        _bf16(xa_save, "xa_save", (M, r))
+    if dX is not None:
+        _bf16(dX, "dX", (M, d_in))
+    _f32(dA, "dA", (r, d_in))
+    _f32(dB, "dB", (n, r))
+    st = load_library().lora_glu_bwd(_ptr(dP), _ptr(gu), _ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(xa_save),
+                                     _ptr(dGU), _ptr(dX), _ptr(dA), _ptr(dB), M, d_in, n // 2, r, float(alpha),
+                                     _act(act), *_ws(ws), _stream(stream))
+    del keep
+    _check(st, "lora_glu_bwd")
+
+
+def lora_linear_act_fwd(x, W, A, B, bias, residual, out, pre_save, xa_save, alpha, act, ws, stream=None):
+    """out = act(x.W^T + s.(x.A^T).B^T + bias) + residual; W: a bf16 tensor or a FrozenWeight;
+    bias [d_out], residual, pre_save [M, d_out] and xa_save may each be None."""
+    w, n, d_in, keep = _weight(W)
+    M, r = x.shape[0], A.shape[0]
+    for t, name, s in ((x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (out, "out", (M, n))):
+        _bf16(t, name, s)
+    for t, name, s in ((bias, "bias", (n,)), (residual, "residual", (M, n)), (pre_save, "pre_save", (M, n)),
+                       (xa_save, "xa_save", (M, r))):
+        if t is not None:
+            _bf16(t, name, s)
+    st = load_library().lora_linear_act_fwd(_ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(bias), _ptr(residual),
+                                            _ptr(out), _ptr(pre_save), _ptr(xa_save), M, d_in, n, r, float(alpha),
+                                            _act(act), *_ws(ws), _stream(stream))
+    del keep
+    _check(st, "lora_linear_act_fwd")
+
+
+def lora_linear_act_bwd(dOut, pre, x, W, A, B, xa_save, dPre, dX, dA, dB, dbias, alpha, act, ws, stream=None):
+    """dPre = dOut * act'(pre), dbias = its sum over the tokens (or None), and the layer's dX
+    (or None), dA, dB.  pre and dPre may be None for act "none".  The workspace is
+    act_workspace's."""
+    w, n, d_in, keep = _weight(W)
+    M, r = x.shape[0], A.shape[0]
+    for t, name, s in ((dOut, "dOut", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r))):
+        _bf16(t, name, s)
+    for t, name, s in ((pre, "pre", (M, n)), (dPre, "dPre", (M, n)), (xa_save, "xa_save", (M, r)),
+                       (dX, "dX", (M, d_in))):
+        if t is not None:
+            _bf16(t, name, s)
+    _f32(dA, "dA", (r, d_in))
+    _f32(dB, "dB", (n, r))
+    if dbias is not None:
+        _f32(dbias, "dbias", (n,))
+    st = load_library().lora_linear_act_bwd(_ptr(dOut), _ptr(pre), _ptr(x), ctypes.byref(w), _ptr(A), _ptr(B),
+                                            _ptr(xa_save), _ptr(dPre), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(dbias), M,
+                                            d_in, n, r, float(alpha), _act(act), *_ws(ws), _stream(stream))
+    del keep
+    _check(st, "lora_linear_act_bwd")

@@ -1,0 +1,327 @@
+"""The gated projections and the projection with an epilogue on the GPU, against 64-bit
+references: every weight format, activation and optional part, odd and ragged sizes, one
+token, last waves cut along K and along N, and the gradients."""
+import pytest
+import torch
+
+from block_cases import ACT_ERR, BF, F32, LIPSCHITZ, Layer, act64, assert_within
+from rank_linear_lora_b200 import autograd as LA
+from rank_linear_lora_b200 import block
+from rank_linear_lora_b200 import lora_linear as L
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf(*shape):
+    return torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+
+
+def _f32(*shape):
+    return torch.full(shape, float("nan"), dtype=torch.float32, device="cuda")
+
+
+# M, d_in, d_ff, r, format, activation
+GLU = [
+    (1, 8, 8, 8, "bf16", "silu"),            # the smallest of everything
+    (1, 264, 136, 16, "bf16", "silu"),
+    (3, 1000, 520, 24, "bf16", "gelu"),
+    (16, 512, 264, 32, "bf16", "gelu_tanh"),
+    (17, 512, 264, 32, "bf16", "relu"),
+    (129, 200, 72, 72, "bf16", "silu"),      # a K tail of two 64-wide blocks
+    (300, 328, 392, 16, "bf16", "none"),
+    (257, 264, 1288, 8, "bf16", "gelu"),
+    (1, 512, 136, 16, "q4", "silu"),
+    (5, 448, 264, 16, "nf4", "silu"),
+    (2, 272, 136, 8, "fp8", "gelu_tanh"),
+    (300, 320, 264, 16, "q4", "silu"),
+    (300, 336, 264, 16, "fp8", "gelu"),
+    (300, 320, 392, 16, "nf4", "relu"),
+    (1280, 2056, 2048, 16, "bf16", "silu"),  # 80 tiles, 33 K blocks: the last wave cut along K
+    (1280, 264, 2048, 16, "bf16", "silu"),   # 5 K blocks: cut along N
+    (1280, 2112, 2048, 16, "q4", "silu"),    # several tiles per CTA pair on a coded weight
+]
+
+
+def _glu_reference(y, act):
+    h, err = y.h()
+    f = y.n // 2
+    g, u, eg, eu = h[:, :f], h[:, f:], err[:, :f], err[:, f:]
+    a, _ = act64(g, act)
+    ea = LIPSCHITZ * eg + ACT_ERR * g.abs()
+    p = a * u
+    ep = ea * (u.abs() + eu) + a.abs() * eu
+    return h, err, p, ep + (BF + 2 * F32) * (p.abs() + ep)
+
+
+@pytest.mark.parametrize("case", GLU, ids=["-".join(map(str, c)) for c in GLU])
+@pytest.mark.parametrize("save", [False, True], ids=["plain", "saved"])
+def test_glu_forward(case, save):
+    M, d, f, r, fmt, act = case
+    y = Layer(M, d, 2 * f, r, fmt, seed=11 + M)
+    ws = L.workspace(y.wt.ops()[0], M, d, 2 * f, r)
+    p, gu, xa = _bf(M, f), _bf(M, 2 * f) if save else None, _bf(M, r) if save else None
+    n0 = L.lora_linear_launch_count()
+    L.lora_glu_fwd(y.x, y.wt, y.A, y.B, p, gu, xa, y.alpha, act, ws)
+    L.lora_linear_check(ws)
+    assert L.lora_linear_launch_count() - n0 == 2
+    h, err, want, bound = _glu_reference(y, act)
+    assert_within("p", p, want, bound)
+    if save:
+        assert_within("gu", gu, h, err + BF * (h.abs() + err))
+    again = _bf(M, f)
+    L.lora_glu_fwd(y.x, y.wt, y.A, y.B, again, None, None, y.alpha, act, ws)
+    L.lora_linear_check(ws)
+    assert torch.equal(p, again)  # the same bits, and the workspace left ready for the next call
+
+
+GLU_BWD = [
+    (1, 264, 136, 16, "bf16", "silu"),
+    (129, 200, 72, 72, "bf16", "gelu"),
+    (300, 328, 392, 16, "bf16", "gelu_tanh"),
+    (64, 136, 2056, 32, "bf16", "relu"),
+    (200, 320, 264, 16, "q4", "silu"),
+    (200, 336, 264, 16, "fp8", "silu"),
+    (200, 320, 264, 16, "nf4", "none"),
+]
+
+
+@pytest.mark.parametrize("case", GLU_BWD, ids=["-".join(map(str, c)) for c in GLU_BWD])
+def test_glu_backward_from_saved_values(case):
+    """dGU and the layer's gradients from given pre-activations, xa saved or recomputed."""
+    M, d, f, r, fmt, act = case
+    y = Layer(M, d, 2 * f, r, fmt, seed=5 + M)
+    gu, dP = y.randn(M, 2 * f), y.randn(M, f)
+    gu[0, :8] = torch.tensor([0.0, -0.0, 30.0, -30.0, 64.0, -64.0, 1e-30, -1e-3], dtype=torch.bfloat16)
+    xa = (y.s * (y.x.double() @ y.A.double().t())).to(torch.bfloat16)
+    ws = L.workspace(y.wt.ops()[1], M, d, 2 * f, r)
+    a, da = act64(gu[:, :f].double(), act)
+    dh = torch.cat((dP.double() * gu[:, f:].double() * da, dP.double() * a), dim=1)
+    scale = torch.cat((dP.double() * gu[:, f:].double(), dP.double() * gu[:, :f].double()), dim=1).abs()
+    edh = BF * dh.abs() + 2 * ACT_ERR * LIPSCHITZ * (scale + dh.abs())
+    ref = y.backward(dh, edh)
+    for xa_save in (xa, None):
+        dGU, dX, dA, dB = _bf(M, 2 * f), _bf(M, d), _f32(r, d), _f32(2 * f, r)
+        L.lora_glu_bwd(dP, gu, y.x, y.wt, y.A, y.B, xa_save, dGU, dX, dA, dB, y.alpha, act, ws)
+        L.lora_linear_check(ws)
+        assert_within("dGU", dGU, dh, edh)
+        for name, got, k in (("dX", dX, 3), ("dA", dA, 3), ("dB", dB, 3)):
+            assert_within(name, got, *ref[name], roundings=k)
+
+
+# M, d_in, d_out, r, format, activation, bias, residual
+ACT = [
+    (1, 8, 8, 8, "bf16", "none", False, False),
+    (1, 264, 136, 16, "bf16", "none", False, True),
+    (7, 1000, 520, 24, "bf16", "gelu", True, True),
+    (16, 512, 264, 32, "bf16", "silu", True, False),
+    (17, 512, 264, 32, "bf16", "gelu_tanh", False, True),
+    (129, 200, 72, 72, "bf16", "relu", True, True),
+    (300, 328, 392, 16, "bf16", "none", True, False),
+    (1, 512, 136, 16, "q4", "none", True, True),
+    (5, 448, 264, 16, "nf4", "silu", False, True),
+    (2, 272, 136, 8, "fp8", "none", True, False),
+    (300, 320, 264, 16, "q4", "gelu", True, True),
+    (300, 336, 264, 16, "fp8", "none", False, True),
+    (300, 320, 392, 16, "nf4", "relu", True, False),
+    (1280, 2056, 4096, 16, "bf16", "gelu", True, True),  # 80 tiles: cut along K
+    (1280, 264, 4104, 16, "bf16", "none", True, True),   # 85 tiles: cut along N
+    (1280, 2112, 4096, 16, "fp8", "silu", True, True),
+]
+
+
+def _act_reference(y, act, bias, residual):
+    h, err = y.h()
+    if bias:
+        h, err = h + y.bias.double(), err + F32 * (h.abs() + y.bias.double().abs())
+    a, _ = act64(h, act)
+    ea = LIPSCHITZ * err + (0 if act == "none" else ACT_ERR * h.abs())
+    out = a + y.residual.double() if residual else a
+    return h, err, out, ea + (BF + 2 * F32) * (out.abs() + ea)
+
+
+@pytest.mark.parametrize("case", ACT, ids=["-".join(map(str, c)) for c in ACT])
+@pytest.mark.parametrize("save", [False, True], ids=["plain", "saved"])
+def test_linear_act_forward(case, save):
+    M, d, n, r, fmt, act, bias, residual = case
+    y = Layer(M, d, n, r, fmt, seed=21 + M)
+    ws = L.act_workspace(y.wt.ops()[0], M, d, n, r)
+    out, pre, xa = _bf(M, n), _bf(M, n) if save else None, _bf(M, r) if save else None
+    b, res = y.bias if bias else None, y.residual if residual else None
+    L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, b, res, out, pre, xa, y.alpha, act, ws)
+    L.lora_linear_check(ws)
+    h, err, want, bound = _act_reference(y, act, bias, residual)
+    assert_within("out", out, want, bound)
+    if save:
+        assert_within("pre", pre, h, err + BF * (h.abs() + err))
+    again = _bf(M, n)
+    L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, b, res, again, None, None, y.alpha, act, ws)
+    L.lora_linear_check(ws)
+    assert torch.equal(out, again)
+
+
+ACT_BWD = [
+    (1, 264, 136, 16, "bf16", "none", True),
+    (1, 264, 8, 16, "bf16", "gelu", True),
+    (33, 200, 1032, 72, "bf16", "gelu", True),
+    (129, 200, 72, 16, "bf16", "silu", False),
+    (700, 136, 264, 16, "bf16", "none", False),
+    (1500, 136, 328, 8, "bf16", "relu", True),
+    (200, 320, 264, 16, "q4", "gelu_tanh", True),
+    (200, 336, 264, 16, "fp8", "silu", True),
+    (200, 320, 264, 16, "nf4", "none", True),
+]
+
+
+@pytest.mark.parametrize("case", ACT_BWD, ids=["-".join(map(str, c)) for c in ACT_BWD])
+def test_linear_act_backward_from_saved_values(case):
+    M, d, n, r, fmt, act, bias = case
+    y = Layer(M, d, n, r, fmt, seed=31 + M)
+    pre, dOut = y.randn(M, n), y.randn(M, n)
+    xa = (y.s * (y.x.double() @ y.A.double().t())).to(torch.bfloat16)
+    ws = L.act_workspace(y.wt.ops()[1], M, d, n, r)
+    _, da = act64(pre.double(), act)
+    dh = dOut.double() * da
+    e32 = torch.zeros_like(dh) if act == "none" else 2 * ACT_ERR * LIPSCHITZ * (dOut.double() * pre.double()).abs() + \
+        2 * ACT_ERR * dOut.double().abs()
+    edh = e32 if act == "none" else e32 + BF * (dh.abs() + e32)
+    ref = y.backward(dh, edh)
+    bits = None
+    for _ in range(2):
+        dPre, dX, dA, dB = _bf(M, n), _bf(M, d), _f32(r, d), _f32(n, r)
+        db = _f32(n) if bias else None
+        has = act != "none"
+        L.lora_linear_act_bwd(dOut, pre if has else None, y.x, y.wt, y.A, y.B, xa, dPre if has else None, dX, dA, dB,
+                              db, y.alpha, act, ws)
+        L.lora_linear_check(ws)
+        if has:
+            assert_within("dPre", dPre, dh, edh)
+        for name, got, k in (("dX", dX, 3), ("dA", dA, 3), ("dB", dB, 3)):
+            assert_within(name, got, *ref[name], roundings=k)
+        if bias:
+            assert_within("dbias", db, dh.sum(0), e32.sum(0) + M * F32 * (dh.abs() + e32).sum(0))
+            assert bits is None or torch.equal(db, bits)  # a fixed order of summation
+            bits = db
+
+
+def _autograd_reference(y, kind, act, bias, residual, dout):
+    """Outputs and gradients by autograd in 64 bits."""
+    leaf = {k: getattr(y, k).double().requires_grad_(True) for k in ("x", "A", "B")}
+    if bias:
+        leaf["bias"] = y.bias.double().requires_grad_(True)
+    if residual:
+        leaf["residual"] = y.residual.double().requires_grad_(True)
+    h = leaf["x"] @ y.W.t() + y.s * (leaf["x"] @ leaf["A"].t()) @ leaf["B"].t()
+    f = block._TORCH_ACT[act]
+    if kind == "glu":
+        out = f(h[:, :y.n // 2]) * h[:, y.n // 2:]
+    else:
+        h = h + leaf["bias"] if bias else h
+        out = f(h) + leaf["residual"] if residual else f(h)
+    return out.detach(), dict(zip(leaf, torch.autograd.grad(out, list(leaf.values()), dout.double())))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4", "fp8", "nf4"])
+@pytest.mark.parametrize("kind", ["glu", "act"])
+def test_autograd_matches_the_formula(kind, fmt):
+    """Through the autograd functions: leading dimensions, an input that is a strided view,
+    gradients of every leaf.  Norm bounds: at most six independent roundings to bf16 lie
+    between the inputs and a gradient (h or pre, dh, s.xa, s.g, the result, and the coded
+    weight's own)."""
+    M, d, n, r = 2 * 150, 320, 528, 16
+    y = Layer(M, d, n, r, fmt, seed=3)
+    x = torch.stack((y.x, y.x), dim=1)[:, 0].reshape(2, 150, d)  # rows 2 d apart
+    x = x.detach().requires_grad_(True)
+    A, B = y.A.clone().requires_grad_(True), y.B.clone().requires_grad_(True)
+    f0, n0 = LA.fallback_calls, L.lora_linear_launch_count()
+    if kind == "glu":
+        out = block.lora_glu(x, y.wt, A, B, y.alpha, act="silu")
+        dout = y.randn(2, 150, n // 2)
+        leaves, names = (x, A, B), ("x", "A", "B")
+    else:
+        bias = y.bias.clone().requires_grad_(True)
+        res = y.residual.reshape(2, 150, n).clone().requires_grad_(True)
+        out = block.lora_linear_act(x, y.wt, A, B, y.alpha, bias=bias, residual=res, act="gelu")
+        dout = y.randn(2, 150, n)
+        leaves, names = (x, A, B, bias, res), ("x", "A", "B", "bias", "residual")
+    grads = torch.autograd.grad(out, leaves, dout)
+    torch.cuda.synchronize()
+    assert LA.fallback_calls == f0 and L.lora_linear_launch_count() - n0 == 6
+    want, gref = _autograd_reference(y, kind, "silu" if kind == "glu" else "gelu", kind == "act", kind == "act",
+                                     dout.reshape(M, -1))
+    lim = BF * (6 / 3) ** 0.5
+    rel = lambda a, b: ((a.double().reshape(b.shape) - b).norm() / b.norm()).item()  # noqa: E731
+    assert rel(out, want) <= lim
+    for name, got in zip(names, grads):
+        assert got.dtype == torch.bfloat16
+        assert rel(got, gref[name]) <= lim, name
+
+
+def test_no_grad_and_empty_batches():
+    y = Layer(40, 64, 128, 8, seed=9)
+    with torch.no_grad():
+        a = block.lora_glu(y.x.requires_grad_(True), y.wt, y.A, y.B, y.alpha)
+    b = block.lora_glu(y.x, y.wt, y.A, y.B, y.alpha)
+    assert not a.requires_grad and b.requires_grad and torch.equal(a, b)
+    x0 = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    A = y.A.clone().requires_grad_(True)
+    for out in (block.lora_glu(x0, y.wt, A, y.B, y.alpha), block.lora_linear_act(x0, y.wt, A, y.B, y.alpha)):
+        assert out.shape[0] == 0
+        gx, gA = torch.autograd.grad(out.float().sum(), (x0, A))
+        assert gx.shape == (0, 64) and not gA.any()
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    """A token with infinite or NaN inputs does not reach the other tokens' outputs."""
+    y = Layer(140, 128, 144, 8, seed=17)
+    ws = L.act_workspace(L.OP_FWD, 140, 128, 144, 8)
+    clean, got = _bf(140, 144), _bf(140, 144)
+    L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, y.residual, clean, None, None, y.alpha, "gelu", ws)
+    x = y.x.clone()
+    x[3], x[70] = float("nan"), float("inf")
+    L.lora_linear_act_fwd(x, y.wt, y.A, y.B, y.bias, y.residual, got, None, None, y.alpha, "gelu", ws)
+    L.lora_linear_check(ws)
+    rest = [i for i in range(140) if i not in (3, 70)]
+    assert torch.equal(got[rest], clean[rest])
+    assert got[3].isnan().all() and not got[70].isfinite().all()
+
+
+def test_two_streams_and_two_graphs():
+    """Calls on two streams, and two captured training steps replayed at the same time on
+    new inputs, give what the calls give alone."""
+    y = [Layer(300, 328, 1040, 16, seed=s) for s in (41, 42)]
+    dout = [t.randn(300, 520) for t in y]
+
+    def step(i, x):
+        x = x.detach().requires_grad_(True)
+        A, B = y[i].A.clone().requires_grad_(True), y[i].B.clone().requires_grad_(True)
+        p = block.lora_glu(x, y[i].wt, A, B, y[i].alpha)
+        return (p.detach(), *torch.autograd.grad(p, (x, A, B), dout[i]))
+
+    alone = [step(i, y[i].x) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got.append(step(i, y[i].x))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+    graphs, xs, outs = [], [], []
+    for i in (0, 1):
+        xs.append(torch.zeros_like(y[i].x))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            outs.append(step(i, xs[i]))
+        graphs.append(g)
+    for i in (0, 1):
+        xs[i].copy_(y[i].x)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(alone, outs):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
