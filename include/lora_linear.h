@@ -373,8 +373,9 @@ LORA_API lora_status_t lora_linear_selftest_timeout(void *workspace, size_t ws_b
                                                     void *stream);
 
 /* ---- operators around the layer ------------------------------------------------
- * What a transformer block computes right beside its projections: gated projections and
- * a projection with bias, activation and residual.  The conventions above hold for all of them.
+ * What a transformer block computes right beside its projections: gated projections,
+ * a projection with bias, activation and residual, and the norms of queries and keys
+ * with the rotation of their positions.  The conventions above hold for all of them.
  * The pages list these parts of a block's kernel fusion without formulas (page
  * "UnSloth加速库集成：编译级优化带来的性能飞跃", section 核心技术一); the formulas are
  * given at each entry point.
@@ -471,6 +472,65 @@ LORA_API lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t 
 /* Bytes of workspace of lora_linear_act_fwd / _bwd for `op`, a lora_op_t of the weight's
  * format (0 if the sizes are invalid).  Pure host function. */
 LORA_API size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r);
+
+/* Element types of the head operators' tensors. */
+typedef enum { LORA_T_BF16 = 0, LORA_T_FP16 = 1, LORA_T_FP32 = 2 } lora_dtype_t;
+
+/* A [M, heads, D] tensor: element (m, h, j) at data[m * token_stride + h * head_stride + j]
+ * (strides in elements, D contiguous), e.g. a column range of the stacked projection. */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+    int32_t heads;
+} lora_heads_t;
+
+/*
+ * Norms of queries and keys for each head, with the rotation of their positions:
+ *     n = v / sqrt(mean_j v_j^2 + eps) * weight        (weight NULL: 1; no norm if !norm)
+ *     y = n with its first `rot` dimensions rotated: for the pairs (a, b) of the layout,
+ *         y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin
+ * with cos, sin [n_pos, rot / 2] (fp32) read at row positions[m].  Pair i is (i, i + rot/2),
+ * or (2 i, 2 i + 1) if `interleaved`.  One pass: fp32 inside, one rounding at the end.
+ *   q, k           inputs; either may be NULL (nothing computed for it).
+ *   q_out, k_out   outputs of the same head counts; each may be its input, in place (same
+ *                  data and strides), and must not overlap inputs otherwise.
+ *   positions      int64 [M].  A position outside [0, n_pos) reads no table row; the
+ *                  rotated dimensions of that token become NaN.
+ *   rot            0 (no rotation; cos, sin and positions are then ignored) .. D.
+ * Requires 8 <= D <= 256, D % 8 == 0, rot % 8 == 0, 1 <= M <= 2^30, 1 <= heads <= 4096,
+ * eps >= 0 and finite; data, weights and tables 16-byte aligned; strides that are
+ * multiples of 16 bytes (of 8 for 16-bit types where rot / 2 is not a multiple of 8);
+ * strides that name no element twice (token_stride >= (heads - 1) head_stride + D, or
+ * head_stride >= (M - 1) token_stride + D; a stride over one token or head is not used).
+ * Reads and writes only the elements that the strides name.
+ */
+LORA_API lora_status_t lora_qk_norm_rope_fwd(int dtype, const lora_heads_t *q, const lora_heads_t *k,
+                                             const void *q_weight, const void *k_weight, const float *cos,
+                                             const float *sin, const int64_t *positions, int64_t n_pos,
+                                             const lora_heads_t *q_out, const lora_heads_t *k_out, int64_t M, int D,
+                                             int rot, int interleaved, int norm, float eps, void *stream);
+
+/*
+ * Backward, from the forward's inputs: with dn the gradient rotated back, i = 1 / sqrt(mean
+ * v^2 + eps) and e = v i:  dweight = sum over tokens and heads of dn * e,
+ * dv = i (dn weight - e mean_j(e dn weight)).
+ *   dq_out, dk_out  gradients of the outputs (NULL exactly where q, k are).
+ *   dq, dk          outputs; each may be its dq_out / dk_out, in place.
+ *   dq_weight, dk_weight  outputs [D] (fp32), or NULL.
+ * A token whose position is outside the table makes its dq, dk and the weights' gradients
+ * NaN.  Sums run in a fixed order for given sizes: the same call gives the same bits.
+ * Workspace: lora_qk_norm_rope_workspace_size(M, heads of q + heads of k, D) bytes, 256-byte aligned
+ * (it need not be zeroed); may be NULL when neither weight gradient is asked for.
+ */
+LORA_API lora_status_t lora_qk_norm_rope_bwd(int dtype, const lora_heads_t *dq_out, const lora_heads_t *dk_out,
+                                             const lora_heads_t *q, const lora_heads_t *k, const void *q_weight,
+                                             const void *k_weight, const float *cos, const float *sin,
+                                             const int64_t *positions, int64_t n_pos, const lora_heads_t *dq,
+                                             const lora_heads_t *dk, float *dq_weight, float *dk_weight, int64_t M,
+                                             int D, int rot, int interleaved, int norm, float eps, void *workspace,
+                                             size_t workspace_bytes, void *stream);
+
+LORA_API size_t lora_qk_norm_rope_workspace_size(int64_t M, int heads, int D);
 
 /* ---- measurement hooks (no effect on results) ---------------------------------
  * Kernel kinds, in the order a forward + backward launches them. */

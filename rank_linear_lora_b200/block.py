@@ -1,9 +1,12 @@
 """The operators around the LoRA linear layer of a transformer block, with autograd.
 
 * ``lora_glu``: gated projections of one x, act(gate) * up in the GEMM's epilogue;
-* ``lora_linear_act``: a projection with bias, activation and residual in its epilogue.
+* ``lora_linear_act``: a projection with bias, activation and residual in its epilogue;
+* ``qk_norm_rope``: the norms of queries and keys for each head with the rotation of their
+  positions (``rope_table`` makes its angles), and ``qkv_heads``, the same on the stacked
+  output of the q/k/v projections.
 
-Both take the frozen weight as a bf16 tensor or as a ``FrozenWeight`` of any format, and
+The projections take the frozen weight as a bf16 tensor or as a ``FrozenWeight`` of any format, and
 trainable adapters A, B of the (stacked) layer; gradients flow to x, A, B, the bias and the
 residual.  As ``autograd.lora_linear``: the library's kernels run, or torch's unfused
 composition where the library answers LORA_ERR_UNSUPPORTED or LORA_LINEAR_FUSED=0 asks for
@@ -219,3 +222,168 @@ def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str
 
     out = _fused_or(fused, unfused)
     return out if x.dim() == 2 else out.reshape(*x.shape[:-1], out.shape[-1])
+
+
+# ------------------------------------------------------------------ norms of q and k with the rotation
+def rope_table(n_pos: int, rot: int, theta: float = 10000.0, device=None):
+    """(cos, sin) [n_pos, rot / 2] in fp32 of the angles position * theta^(-2 i / rot), formed in
+    64 bits (an angle of tens of thousands of radians has no exact digits left in 32)."""
+    freq = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def _addressable(t):
+    """t [M, heads, D] if the library's strides can name it, else a contiguous copy."""
+    if t is None or (t.stride(2) == 1 and t.data_ptr() % 16 == 0 and all(
+            n == 1 or (s >= t.shape[2] and s * t.element_size() % 16 == 0) for n, s in zip(t.shape[:2], t.stride()))):
+        return t
+    return t.contiguous()
+
+
+def _heads_backward(grads, ins, weights, tables, outs, want_w, eps, interleaved, norm):
+    """The library's backward into `outs`; the fp32 weight gradients (None where not wanted)."""
+    one = next(t for t in ins if t is not None)
+    M, _, D = one.shape
+    dw = [torch.empty(D, dtype=torch.float32, device=one.device) if w else None for w in want_w]
+    ws = None
+    if any(want_w):
+        heads = sum(t.shape[1] for t in ins if t is not None)
+        ws = torch.empty(L.lora_qk_norm_rope_workspace_size(M, heads, D), dtype=torch.uint8, device=one.device)
+    L.lora_qk_norm_rope_bwd(*grads, *ins, *weights, *tables, *outs, *dw, ws, eps, interleaved, norm)
+    return dw
+
+
+class QkNormRopeFunction(torch.autograd.Function):
+    """The norms and the rotation of q [M, hq, D] and k [M, hk, D]."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
+        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        if q.shape[0] > 0:
+            L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.rest = eps, interleaved, norm
+        return q_out, k_out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        want = [w is not None and n for w, n in zip((wq, wk), ctx.needs_input_grad[2:4])]
+        if q.shape[0] == 0:
+            dw = [torch.zeros_like(w) if n else None for w, n in zip((wq, wk), want)]
+        else:
+            dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
+                                 (dq, dk), want, *ctx.rest)
+            dw = [None if t is None else t.to(q.dtype) for t in dw]
+        return dq, dk, *dw, None, None, None, None, None, None
+
+
+def _unfused_heads(v, w, cos, sin, positions, eps, interleaved, norm):
+    f = v.float()
+    if norm:
+        f = f * torch.rsqrt(f.square().mean(-1, keepdim=True) + eps)
+    if w is not None:
+        f = f * w.float()
+    if cos is not None:
+        rot = 2 * cos.shape[1]
+        c, s = cos[positions][:, None], sin[positions][:, None]
+        head = f[..., :rot]
+        a, b = (head[..., 0::2], head[..., 1::2]) if interleaved else head.chunk(2, dim=-1)
+        ra, rb = a * c - b * s, b * c + a * s
+        turned = torch.stack((ra, rb), -1).flatten(-2) if interleaved else torch.cat((ra, rb), -1)
+        f = torch.cat((turned, f[..., rot:]), dim=-1)
+    return f.to(v.dtype)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False, norm: bool = True):
+    """(q, k) with each head [D] over its root mean square (unless norm is False), times its
+    weight, the first 2 * cos.shape[1] dimensions rotated by the token's angles.
+
+    q [..., hq, D] and k [..., hk, D] (bf16, fp16 or fp32; column views of a stacked projection
+    are read in place), weights [D] of the same type, cos and sin [n_pos, rot / 2] fp32 (see
+    rope_table), positions [...] int64.  Pairs are (i, i + rot/2), or (2 i, 2 i + 1) if
+    interleaved.  New tensors; gradients flow to q, k and the weights."""
+    q3, k3 = (_addressable(t.reshape(-1, *t.shape[-2:])) for t in (q, k))
+    pos = None if positions is None else positions.reshape(-1).contiguous()
+
+    def fused():
+        if _grad_wanted(q, k, q_weight, k_weight):
+            return QkNormRopeFunction.apply(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
+        qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q3, k3))
+        if q3.shape[0] > 0:
+            L.lora_qk_norm_rope_fwd(q3, k3, q_weight, k_weight, cos, sin, pos, qo, ko, eps, interleaved, norm)
+        return qo, ko
+
+    def unfused():
+        return (_unfused_heads(q3, q_weight, cos, sin, pos, eps, interleaved, norm),
+                _unfused_heads(k3, k_weight, cos, sin, pos, eps, interleaved, norm))
+
+    qo, ko = _fused_or(fused, unfused)
+    return (qo, ko) if q.dim() == 3 else (qo.reshape(q.shape), ko.reshape(k.shape))
+
+
+class QkvHeadsFunction(torch.autograd.Function):
+    """q, k, v from the stacked projection h [M, (hq + 2 hk) D] = [q | k | v]: q and k with
+    norm and rotation, v a view.  The backward writes dq and dk straight into their columns
+    of one dh, the gradient the stacked projection's backward reads."""
+
+    @staticmethod
+    def forward(ctx, h, q_weight, k_weight, cos, sin, positions, hq, hk, D, eps, interleaved, norm):
+        q, k, v = QkvHeadsFunction.split(h, hq, hk, D)
+        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        if h.shape[0] > 0:
+            L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
+        ctx.save_for_backward(h, q_weight, k_weight, cos, sin, positions)
+        ctx.heads, ctx.rest = (hq, hk, D), (eps, interleaved, norm)
+        return q_out, k_out, v
+
+    @staticmethod
+    def split(h, hq, hk, D):
+        return (h[:, :hq * D].unflatten(1, (hq, D)), h[:, hq * D:(hq + hk) * D].unflatten(1, (hk, D)),
+                h[:, (hq + hk) * D:].unflatten(1, (hk, D)))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out, dv):
+        h, wq, wk, cos, sin, positions = ctx.saved_tensors
+        dh = torch.empty_like(h)
+        dq, dk, dv_part = QkvHeadsFunction.split(dh, *ctx.heads)
+        dv_part.copy_(dv)
+        q, k, _ = QkvHeadsFunction.split(h, *ctx.heads)
+        want = [w is not None and n for w, n in zip((wq, wk), ctx.needs_input_grad[1:3])]
+        if h.shape[0] == 0:
+            dw = [torch.zeros_like(w) if n else None for w, n in zip((wq, wk), want)]
+        else:
+            dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
+                                 (dq, dk), want, *ctx.rest)
+            dw = [None if t is None else t.to(h.dtype) for t in dw]
+        return dh, *dw, *(None,) * 9
+
+
+def qkv_heads(h, hq: int, hk: int, D: int, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+              eps: float = 1e-6, interleaved: bool = False, norm: bool = True):
+    """(q [..., hq, D], k [..., hk, D], v [..., hk, D]) from h [..., (hq + 2 hk) D] = [q | k | v],
+    the stacked output of the q/k/v projections (multi.SharedInputProjections): q and k as
+    qk_norm_rope gives them, v as it is."""
+    if h.shape[-1] != (hq + 2 * hk) * D:
+        raise ValueError(f"h: expected {(hq + 2 * hk) * D} columns for {hq} + 2 x {hk} heads of {D}, got {h.shape[-1]}")
+    h2 = h.reshape(-1, h.shape[-1]).contiguous()
+    pos = None if positions is None else positions.reshape(-1).contiguous()
+
+    def fused():
+        if _grad_wanted(h2, q_weight, k_weight):
+            return QkvHeadsFunction.apply(h2, q_weight, k_weight, cos, sin, pos, hq, hk, D, eps, interleaved, norm)
+        q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
+        return (*qk_norm_rope(q, k, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm), v)
+
+    def unfused():
+        q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
+        return (_unfused_heads(q, q_weight, cos, sin, pos, eps, interleaved, norm),
+                _unfused_heads(k, k_weight, cos, sin, pos, eps, interleaved, norm), v)
+
+    outs = _fused_or(fused, unfused)
+    return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)

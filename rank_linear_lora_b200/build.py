@@ -9,7 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_linear.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("lora_linear.cu", "noalloc.cu", "merge.cu", "block.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("lora_linear.cu", "noalloc.cu", "merge.cu", "block.cu",
+                                             "heads.cu")]
 
 
 def deps() -> list:

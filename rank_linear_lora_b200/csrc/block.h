@@ -12,6 +12,7 @@ namespace lora_host {
 
 void count_launch();          // one more kernel of this library launched
 bool programmatic_launch();   // programmatic dependent launch is on
+bool device_supported();      // the current device is one the kernels are built for
 
 // Launch with programmatic dependent launch: the kernel must call grid_dep_wait() before
 // it touches memory.

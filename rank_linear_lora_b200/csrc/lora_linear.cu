@@ -1277,6 +1277,11 @@ ActBwdLayout act_bwd_layout(size_t layer_bytes, int64_t M, int64_t d_out) {
 namespace lora_host {
 void count_launch() { g_launches.fetch_add(1); }
 bool programmatic_launch() { return pdl_enabled(); }
+bool device_supported() {
+    int dev = 0;
+    DevInfo *info = nullptr;
+    return device_info(&dev, &info) && info->supported;
+}
 }  // namespace lora_host
 
 // ====================================================================== C ABI

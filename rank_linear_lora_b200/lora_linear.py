@@ -65,7 +65,12 @@ def load_library():
     lib.lora_linear_act_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
     lib.lora_linear_act_workspace_size.argtypes = [I, I64, I64, I64, I]
     lib.lora_linear_act_workspace_size.restype = SZ
-    for f in ("lora_glu_fwd", "lora_glu_bwd", "lora_linear_act_fwd", "lora_linear_act_bwd"):
+    lib.lora_qk_norm_rope_fwd.argtypes = [I, P, P, P, P, P, P, P, I64, P, P, I64, I, I, I, I, F, P]
+    lib.lora_qk_norm_rope_bwd.argtypes = [I, P, P, P, P, P, P, P, P, P, I64, P, P, P, P, I64, I, I, I, I, F, P, SZ, P]
+    lib.lora_qk_norm_rope_workspace_size.argtypes = [I64, I, I]
+    lib.lora_qk_norm_rope_workspace_size.restype = SZ
+    for f in ("lora_glu_fwd", "lora_glu_bwd", "lora_linear_act_fwd", "lora_linear_act_bwd", "lora_qk_norm_rope_fwd",
+              "lora_qk_norm_rope_bwd"):
         getattr(lib, f).restype = I
     lib.lora_linear_check.argtypes = [P, P]
     lib.lora_linear_check.restype = I
@@ -641,3 +646,85 @@ def lora_linear_act_bwd(dOut, pre, x, W, A, B, xa_save, dPre, dX, dA, dB, dbias,
                                             d_in, n, r, float(alpha), _act(act), *_ws(ws), _stream(stream))
     del keep
     _check(st, "lora_linear_act_bwd")
+
+
+class lora_heads_t(ctypes.Structure):
+    """A [M, heads, D] tensor by strides (include/lora_linear.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+def _heads(t, name, M, D, dtype, heads=None):
+    """A tensor [M, heads, D] with its last dimension contiguous, by reference; None for None."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.dtype != dtype or t.shape[0] != M or t.shape[2] != D or t.stride(2) != 1 or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: expected a {dtype} tensor [{M}, {'heads' if heads is None else heads}, {D}], its last "
+                         f"dimension contiguous, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    _on_current_device(t, name)
+    return ctypes.byref(lora_heads_t(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]))
+
+
+def _head_args(q, k, q_weight, k_weight, cos, sin, positions):
+    """(M, D, dtype, rot, n_pos) of a call, its weights, tables and positions checked."""
+    one = q if q is not None else k
+    if one is None or one.dim() != 3:
+        raise ValueError("q, k: expected at least one tensor [M, heads, D]")
+    (M, _, D), dtype = one.shape, one.dtype
+    if dtype not in HEAD_DTYPES:
+        raise ValueError(f"q, k: one of {sorted(map(str, HEAD_DTYPES))}, got {dtype}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if w.dtype != dtype or tuple(w.shape) != (D,) or not w.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {(D,)}")
+            _on_current_device(w, name)
+    if cos is None:
+        return M, D, dtype, 0, 0
+    if sin is None or positions is None or cos.dim() != 2:
+        raise ValueError("cos, sin [n_pos, rot / 2] and positions go together")
+    n_pos, half = cos.shape
+    _f32(cos, "cos", (n_pos, half))
+    _f32(sin, "sin", (n_pos, half))
+    if positions.dtype != torch.int64 or tuple(positions.shape) != (M,) or not positions.is_contiguous():
+        raise ValueError(f"positions: expected a contiguous int64 tensor of shape {(M,)}")
+    _on_current_device(positions, "positions")
+    return M, D, dtype, 2 * half, n_pos
+
+
+def lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps=1e-6, interleaved=False,
+                          norm=True, stream=None):
+    """q_out, k_out = the heads of q and k [M, heads, D] over their root mean square, times the
+    weights, the first 2 * cos.shape[1] dimensions rotated by the angles of the tokens'
+    positions.  q or k, the weights, and cos with sin and positions may be None; q_out may be
+    q, and k_out k."""
+    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions)
+    hq, hk = (None if t is None else t.shape[1] for t in (q, k))
+    st = load_library().lora_qk_norm_rope_fwd(
+        HEAD_DTYPES[dtype], _heads(q, "q", M, D, dtype), _heads(k, "k", M, D, dtype), _ptr(q_weight), _ptr(k_weight),
+        _ptr(cos), _ptr(sin), _ptr(positions), n_pos, _heads(q_out, "q_out", M, D, dtype, hq),
+        _heads(k_out, "k_out", M, D, dtype, hk), M, D, rot, int(interleaved), int(norm), float(eps), _stream(stream))
+    _check(st, "lora_qk_norm_rope_fwd")
+
+
+def lora_qk_norm_rope_workspace_size(M: int, heads: int, D: int) -> int:
+    return int(load_library().lora_qk_norm_rope_workspace_size(M, heads, D))
+
+
+def lora_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, dq, dk, dq_weight, dk_weight,
+                          ws, eps=1e-6, interleaved=False, norm=True, stream=None):
+    """dq, dk (each may be its dq_out / dk_out, in place) and the fp32 weight gradients [D] (or
+    None) from the forward's inputs.  ws: lora_qk_norm_rope_workspace_size bytes, or None where
+    neither weight gradient is asked for."""
+    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions)
+    hq, hk = (None if t is None else t.shape[1] for t in (q, k))
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _f32(t, name, (D,))
+    wp, wn = (None, 0) if ws is None else _ws(ws)
+    st = load_library().lora_qk_norm_rope_bwd(
+        HEAD_DTYPES[dtype], _heads(dq_out, "dq_out", M, D, dtype, hq), _heads(dk_out, "dk_out", M, D, dtype, hk),
+        _heads(q, "q", M, D, dtype), _heads(k, "k", M, D, dtype), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+        _ptr(positions), n_pos, _heads(dq, "dq", M, D, dtype, hq), _heads(dk, "dk", M, D, dtype, hk), _ptr(dq_weight),
+        _ptr(dk_weight), M, D, rot, int(interleaved), int(norm), float(eps), wp, wn, _stream(stream))
+    _check(st, "lora_qk_norm_rope_bwd")

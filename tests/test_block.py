@@ -81,6 +81,76 @@ def test_linear_act_refusals(lib):
         assert bwd(**b) == 2, b
 
 
+def _h(data=0x1000, ts=1024, hs=128, heads=8):
+    return ctypes.byref(L.lora_heads_t(data, ts, hs, heads))
+
+
+def test_qk_norm_rope_refusals(lib):
+    def fwd(dtype=0, q=_h(), k=None, wq=None, cos=0x2000, sin=0x3000, pos=0x4000, n_pos=16, qo=_h(0x5000), ko=None, M=4,
+            D=128, rot=128, inter=0, eps=1e-6):
+        return lib.lora_qk_norm_rope_fwd(dtype, q, k, P(wq), None, P(cos), P(sin), P(pos), n_pos, qo, ko, M, D, rot, inter,
+                                         1, eps, None)
+
+    bad = [dict(dtype=3), dict(dtype=-1), dict(q=None), dict(q=None, qo=None), dict(qo=None), dict(ko=_h()), dict(M=0),
+           dict(M=(1 << 30) + 1), dict(D=0), dict(D=132), dict(D=264), dict(rot=132), dict(rot=136), dict(rot=-8),
+           dict(rot=12), dict(eps=-1.0), dict(eps=float("nan")), dict(cos=None), dict(sin=None), dict(pos=None),
+           dict(n_pos=0), dict(q=_h(None)), dict(q=_h(heads=0)), dict(q=_h(heads=5000)), dict(qo=_h(heads=7)),
+           dict(q=_h(ts=120)), dict(q=_h(hs=120)), dict(q=_h(hs=-128)), dict(qo=_h(ts=512)), dict(qo=_h(ts=0))]
+    for b in bad:
+        assert fwd(**b) == 1, b
+    for b in (dict(q=_h(0x1008)), dict(qo=_h(0x5002)), dict(q=_h(ts=1028)), dict(q=_h(hs=132, ts=2048)),
+              dict(wq=0x6004), dict(cos=0x2008), dict(sin=0x3004), dict(pos=0x4004)):
+        assert fwd(**b) == 2, b
+
+    def bwd(dy=_h(0x7000), q=_h(), dq=_h(0x5000), dwq=None, dwk=None, ws=None, nws=0):
+        return lib.lora_qk_norm_rope_bwd(0, dy, None, q, None, None, None, P(0x2000), P(0x3000), P(0x4000), 16, dq, None,
+                                         P(dwq), P(dwk), 4, 128, 128, 0, 1, 1e-6, P(ws), nws, None)
+
+    assert bwd(dy=None) == 1 and bwd(dq=None) == 1 and bwd(dwk=0x8000) == 1 and bwd(q=None) == 1
+    assert bwd(dwq=0x8000) == 4 and bwd(dwq=0x8000, ws=0x10000, nws=256) == 4
+    assert bwd(dwq=0x8000, ws=0x10010, nws=1 << 30) == 2 and bwd(dwq=0x8004, ws=0x10000, nws=1 << 30) == 2
+    assert L.lora_qk_norm_rope_workspace_size(4, 8, 128) > 0
+    for bad in ((0, 8, 128), (4, 0, 128), (4, 8, 12), (4, 8, 264)):
+        assert L.lora_qk_norm_rope_workspace_size(*bad) == 0
+
+
+def test_rope_table_far_positions():
+    """Angles of far positions keep their digits: against Python's own 64-bit arithmetic."""
+    import math
+    cos, sin = block.rope_table(40000, 16, theta=500.0)
+    assert cos.dtype == torch.float32 and cos.shape == (40000, 8)
+    for p, i in ((0, 0), (1, 7), (39999, 0), (39999, 5), (31234, 2)):
+        a = p * 500.0 ** (-2 * i / 16)
+        assert abs(cos[p, i].item() - math.cos(a)) < 1e-6 and abs(sin[p, i].item() - math.sin(a)) < 1e-6
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_unfused_heads(interleaved, monkeypatch):
+    """LORA_LINEAR_FUSED=0: torch's composition of the norms and the rotation, on q, k and on
+    the stacked projection, which gives the same q and k and v as it is."""
+    monkeypatch.setenv("LORA_LINEAR_FUSED", "0")
+    g = torch.Generator().manual_seed(2)
+    h = torch.randn(2, 6, (3 + 2 * 2) * 16, generator=g).requires_grad_(True)
+    wq, wk = torch.randn(16, generator=g), torch.randn(16, generator=g)
+    cos, sin = block.rope_table(32, 8)
+    pos = torch.randint(0, 32, (2, 6), generator=g)
+    q, k, v = block.qkv_heads(h, 3, 2, 16, wq, wk, cos, sin, pos, interleaved=interleaved)
+    q2, k2 = block.qk_norm_rope(h[..., :48].unflatten(-1, (3, 16)), h[..., 48:80].unflatten(-1, (2, 16)), wq, wk, cos,
+                                sin, pos, interleaved=interleaved)
+    assert torch.equal(q, q2) and torch.equal(k, k2) and torch.equal(v, h[..., 80:].unflatten(-1, (2, 16)))
+    n = h.detach()[1, 3, 16:32].double()
+    n = n / (n.square().mean() + 1e-6).sqrt() * wq.double()
+    i, j = (2, 3) if interleaved else (1, 5)
+    c, s = cos[pos[1, 3], 1].double(), sin[pos[1, 3], 1].double()
+    assert abs(q[1, 3, 1, i].item() - (n[i] * c - n[j] * s).item()) < 1e-5
+    assert abs(q[1, 3, 1, j].item() - (n[j] * c + n[i] * s).item()) < 1e-5
+    assert abs(q[1, 3, 1, 9].item() - n[9].item()) < 1e-5
+    (q.sum() + k.sum() + v.sum()).backward()
+    assert h.grad is not None
+    with pytest.raises(ValueError, match="columns"):
+        block.qkv_heads(h, 3, 3, 16)
+
+
 def test_workspace_sizes(lib):
     """The forward's workspace is the layer's; the backward's holds the bias partials too."""
     for op in range(8):
