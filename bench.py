@@ -90,7 +90,7 @@ def algorithmic_bytes(spec) -> float:
 
 # The sources the layer's kernels and their launches are built from: lora_linear.cu and
 # every header it includes (the merge and the workspace-free forward are other files).
-LAYER_SOURCES = ("lora_linear.cu", "side.cuh", "tc_gemm.cuh", "tc_gemm2.cuh", "act.cuh", "block.h", "ptx.cuh", "tmap.h")
+LAYER_SOURCES = ("lora_linear.cu", "side.cuh", "tc_gemm.cuh", "tc_gemm2.cuh", "act.cuh", "block.h", "decode.h", "ptx.cuh", "tmap.h")
 
 
 def kernel_source_hash() -> str:

@@ -42,7 +42,8 @@ def _workspace(size_fn, op: int, M: int, d_in: int, d_out: int, r: int, device) 
         raise ValueError(f"invalid sizes: {M} tokens, {d_in} -> {d_out}, rank {r}")
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(n, dtype=torch.uint8, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream, size_fn, op, M, d_in, d_out, r, n)
+    # the size depends on the plan of the shape, and so does the layout: a new plan, a new workspace
+    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index), op, M, d_in, d_out, r, n, L.plan_epoch)
     with _ws_lock:
         ws = _ws_cache.get(key)
         if ws is None:
@@ -60,21 +61,15 @@ def _frozen(W) -> LA.FrozenWeight:
     return W if isinstance(W, LA.FrozenWeight) else LA.FrozenWeight("bf16", (W,))
 
 
-def _fused_or(fused, unfused):
-    """fused(), or unfused() where the library declines (see the module docstring)."""
-    if LA.fused_enabled():
-        try:
-            return fused()
-        except L.LoraError as e:
-            if e.status != 3:  # only LORA_ERR_UNSUPPORTED falls back
-                raise
-            reason = str(e)
-    else:
-        reason = "LORA_LINEAR_FUSED=0"
+def _declined(e=None):
+    """Count (and warn once of) a call that takes the unfused composition; any error but
+    LORA_ERR_UNSUPPORTED is raised again."""
+    if e is not None and e.status != 3:
+        raise e
     LA.fallback_calls += 1
     if LA.fallback_calls == 1:
-        warnings.warn(f"fused LoRA operator not used ({reason}); computing the unfused composition", RuntimeWarning)
-    return unfused()
+        warnings.warn(f"fused LoRA operator not used ({e or 'LORA_LINEAR_FUSED=0'}); computing the unfused composition",
+                      RuntimeWarning)
 
 
 _TORCH_ACT = {
@@ -87,7 +82,32 @@ _TORCH_ACT = {
 
 
 def _grad_wanted(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+def _rows(x):
+    """x [..., d] as contiguous rows [M, d]."""
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    return x2 if x2.is_contiguous() else x2.contiguous()
+
+
+def _adapter_grads(A, B):
+    """fp32 (dA, dB) next to each other, and a function that gives them in A's and B's types:
+    one cast where those are the same."""
+    both = torch.empty(A.numel() + B.numel(), dtype=torch.float32, device=A.device)
+    na = A.numel()
+
+    def typed():
+        if A.dtype != B.dtype:
+            return both[:na].view(A.shape).to(A.dtype), both[na:].view(B.shape).to(B.dtype)
+        t = both.to(A.dtype)
+        return t[:na].view(A.shape), t[na:].view(B.shape)
+
+    return both[:na].view(A.shape), both[na:].view(B.shape), typed
 
 
 # ------------------------------------------------------------------ gated projections
@@ -121,12 +141,11 @@ class LoraGluFunction(torch.autograd.Function):
         dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
         if M == 0:
             return dX, torch.zeros_like(A), torch.zeros_like(B), None, None, None
-        dA = torch.empty(A.shape, dtype=torch.float32, device=x.device)
-        dB = torch.empty(B.shape, dtype=torch.float32, device=x.device)
+        dA, dB, typed = _adapter_grads(A, B)
         dGU = torch.empty_like(gu)
         ws = _workspace(L.lora_linear_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_glu_bwd(dP.contiguous(), gu, x, wt, A, B, xa, dGU, dX, dA, dB, ctx.alpha, ctx.act, ws)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None
+        return dX, *typed(), None, None, None
 
 
 def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
@@ -138,18 +157,21 @@ def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
     block-diagonal).  act: one of L.ACTIVATIONS."""
     wt = _frozen(W)
     L._act(act)
-    x2 = x.reshape(-1, x.shape[-1]).contiguous()
-
-    def fused():
-        if _grad_wanted(x2, A, B):
-            return LoraGluFunction.apply(x2, A, B, alpha, wt, act)
-        return _glu_forward(x2, A, B, alpha, wt, act, save=False)[0]
-
-    def unfused():
+    x2 = _rows(x)
+    p = None
+    if LA.fused_enabled():
+        try:
+            if _grad_wanted(x2, A, B):
+                p = LoraGluFunction.apply(x2, A, B, alpha, wt, act)
+            else:
+                p = _glu_forward(x2, A, B, alpha, wt, act, save=False)[0]
+        except L.LoraError as e:
+            _declined(e)
+    else:
+        _declined()
+    if p is None:
         g, u = LA._unfused(x2, wt, A, B, alpha).chunk(2, dim=-1)
-        return _TORCH_ACT[act](g) * u
-
-    p = _fused_or(fused, unfused)
+        p = _TORCH_ACT[act](g) * u
     return p if x.dim() == 2 else p.reshape(*x.shape[:-1], p.shape[-1])
 
 
@@ -189,14 +211,12 @@ class LoraLinearActFunction(torch.autograd.Function):
             dbias = torch.zeros(n, dtype=ctx.bias_dtype, device=x.device) if want_bias else None
             return dX, torch.zeros_like(A), torch.zeros_like(B), dbias, dres, None, None, None
         dOut = dOut.contiguous()
-        dA = torch.empty(A.shape, dtype=torch.float32, device=x.device)
-        dB = torch.empty(B.shape, dtype=torch.float32, device=x.device)
+        dA, dB, typed = _adapter_grads(A, B)
         dbias = torch.empty(n, dtype=torch.float32, device=x.device) if want_bias else None
         dPre = torch.empty_like(dOut) if ctx.act != "none" else None
         ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_linear_act_bwd(dOut, pre, x, wt, A, B, xa, dPre, dX, dA, dB, dbias, ctx.alpha, ctx.act, ws)
-        return (dX, dA.to(A.dtype), dB.to(B.dtype), dbias.to(ctx.bias_dtype) if want_bias else None, dres, None, None,
-                None)
+        return dX, *typed(), dbias.to(ctx.bias_dtype) if want_bias else None, dres, None, None, None
 
 
 def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str = "none"):
@@ -205,22 +225,26 @@ def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str
     FrozenWeight.  act: one of L.ACTIVATIONS."""
     wt = _frozen(W)
     L._act(act)
-    x2 = x.reshape(-1, x.shape[-1]).contiguous()
-    if residual is not None and residual.shape != (*x.shape[:-1], wt.d_out):
-        raise ValueError(f"residual: expected shape {(*x.shape[:-1], wt.d_out)}, got {tuple(residual.shape)}")
-    res2 = None if residual is None else residual.reshape(-1, wt.d_out).contiguous()
-
-    def fused():
-        if _grad_wanted(x2, A, B, bias, res2):
-            return LoraLinearActFunction.apply(x2, A, B, bias, res2, alpha, wt, act)
-        return _act_forward(x2, A, B, bias, res2, alpha, wt, act, save=False)[0]
-
-    def unfused():
+    x2, res2 = _rows(x), residual
+    if residual is not None:
+        if residual.shape != (*x.shape[:-1], wt.d_out):
+            raise ValueError(f"residual: expected shape {(*x.shape[:-1], wt.d_out)}, got {tuple(residual.shape)}")
+        res2 = _rows(residual)
+    out = None
+    if LA.fused_enabled():
+        try:
+            if _grad_wanted(x2, A, B, bias, res2):
+                out = LoraLinearActFunction.apply(x2, A, B, bias, res2, alpha, wt, act)
+            else:
+                out = _act_forward(x2, A, B, bias, res2, alpha, wt, act, save=False)[0]
+        except L.LoraError as e:
+            _declined(e)
+    else:
+        _declined()
+    if out is None:
         h = LA._unfused(x2, wt, A, B, alpha)
-        h = _TORCH_ACT[act](h if bias is None else h + bias)
-        return h if res2 is None else h + res2
-
-    out = _fused_or(fused, unfused)
+        out = _TORCH_ACT[act](h if bias is None else h + bias)
+        out = out if res2 is None else out + res2
     return out if x.dim() == 2 else out.reshape(*x.shape[:-1], out.shape[-1])
 
 
@@ -235,10 +259,24 @@ def rope_table(n_pos: int, rot: int, theta: float = 10000.0, device=None):
 
 def _addressable(t):
     """t [M, heads, D] if the library's strides can name it, else a contiguous copy."""
-    if t is None or (t.stride(2) == 1 and t.data_ptr() % 16 == 0 and all(
-            n == 1 or (s >= t.shape[2] and s * t.element_size() % 16 == 0) for n, s in zip(t.shape[:2], t.stride()))):
+    if t is None or t.dim() != 3:
+        return t
+    M, H, D = t.shape
+    ts, hs, one = t.stride()
+    unit = 16 // t.element_size()
+    if one == 1 and (M == 1 or (ts >= D and ts % unit == 0)) and (H == 1 or (hs >= D and hs % unit == 0)) \
+            and t.data_ptr() % 16 == 0:
         return t
     return t.contiguous()
+
+
+def _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
+    """New (q_out, k_out) from the library, contiguous."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if q.shape[0] > 0:
+        L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
+    return q_out, k_out
 
 
 def _heads_backward(grads, ins, weights, tables, outs, want_w, eps, interleaved, norm):
@@ -259,9 +297,7 @@ class QkNormRopeFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
-        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        if q.shape[0] > 0:
-            L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
+        q_out, k_out = _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm)
         ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
         ctx.rest = eps, interleaved, norm
         return q_out, k_out
@@ -307,23 +343,27 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     are read in place), weights [D] of the same type, cos and sin [n_pos, rot / 2] fp32 (see
     rope_table), positions [...] int64.  Pairs are (i, i + rot/2), or (2 i, 2 i + 1) if
     interleaved.  New tensors; gradients flow to q, k and the weights."""
-    q3, k3 = (_addressable(t.reshape(-1, *t.shape[-2:])) for t in (q, k))
-    pos = None if positions is None else positions.reshape(-1).contiguous()
-
-    def fused():
-        if _grad_wanted(q, k, q_weight, k_weight):
-            return QkNormRopeFunction.apply(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
-        qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q3, k3))
-        if q3.shape[0] > 0:
-            L.lora_qk_norm_rope_fwd(q3, k3, q_weight, k_weight, cos, sin, pos, qo, ko, eps, interleaved, norm)
-        return qo, ko
-
-    def unfused():
-        return (_unfused_heads(q3, q_weight, cos, sin, pos, eps, interleaved, norm),
+    if q.dim() == 3:
+        q3, k3, pos = q, k, positions
+    else:
+        q3, k3 = q.reshape(-1, *q.shape[-2:]), k.reshape(-1, *k.shape[-2:])
+        pos = None if positions is None else positions.reshape(-1).contiguous()
+    q3, k3 = _addressable(q3), _addressable(k3)
+    outs = None
+    if LA.fused_enabled():
+        try:
+            if _grad_wanted(q, k, q_weight, k_weight):
+                outs = QkNormRopeFunction.apply(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
+            else:
+                outs = _heads_forward(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
+        except L.LoraError as e:
+            _declined(e)
+    else:
+        _declined()
+    if outs is None:
+        outs = (_unfused_heads(q3, q_weight, cos, sin, pos, eps, interleaved, norm),
                 _unfused_heads(k3, k_weight, cos, sin, pos, eps, interleaved, norm))
-
-    qo, ko = _fused_or(fused, unfused)
-    return (qo, ko) if q.dim() == 3 else (qo.reshape(q.shape), ko.reshape(k.shape))
+    return outs if q.dim() == 3 else (outs[0].reshape(q.shape), outs[1].reshape(k.shape))
 
 
 class QkvHeadsFunction(torch.autograd.Function):
@@ -334,9 +374,7 @@ class QkvHeadsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, q_weight, k_weight, cos, sin, positions, hq, hk, D, eps, interleaved, norm):
         q, k, v = QkvHeadsFunction.split(h, hq, hk, D)
-        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        if h.shape[0] > 0:
-            L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
+        q_out, k_out = _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm)
         ctx.save_for_backward(h, q_weight, k_weight, cos, sin, positions)
         ctx.heads, ctx.rest = (hq, hk, D), (eps, interleaved, norm)
         return q_out, k_out, v
@@ -371,19 +409,15 @@ def qkv_heads(h, hq: int, hk: int, D: int, q_weight=None, k_weight=None, cos=Non
     qk_norm_rope gives them, v as it is."""
     if h.shape[-1] != (hq + 2 * hk) * D:
         raise ValueError(f"h: expected {(hq + 2 * hk) * D} columns for {hq} + 2 x {hk} heads of {D}, got {h.shape[-1]}")
-    h2 = h.reshape(-1, h.shape[-1]).contiguous()
+    h2 = _rows(h)
     pos = None if positions is None else positions.reshape(-1).contiguous()
-
-    def fused():
-        if _grad_wanted(h2, q_weight, k_weight):
-            return QkvHeadsFunction.apply(h2, q_weight, k_weight, cos, sin, pos, hq, hk, D, eps, interleaved, norm)
-        q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
-        return (*qk_norm_rope(q, k, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm), v)
-
-    def unfused():
-        q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
-        return (_unfused_heads(q, q_weight, cos, sin, pos, eps, interleaved, norm),
-                _unfused_heads(k, k_weight, cos, sin, pos, eps, interleaved, norm), v)
-
-    outs = _fused_or(fused, unfused)
+    if LA.fused_enabled() and _grad_wanted(h2, q_weight, k_weight):
+        try:
+            outs = QkvHeadsFunction.apply(h2, q_weight, k_weight, cos, sin, pos, hq, hk, D, eps, interleaved, norm)
+            return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)
+        except L.LoraError as e:
+            if e.status != 3:
+                raise
+    q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
+    outs = (*qk_norm_rope(q, k, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm), v)
     return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)

@@ -10,7 +10,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_linear.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("lora_linear.cu", "noalloc.cu", "merge.cu", "block.cu",
-                                             "heads.cu")]
+                                             "heads.cu", "decode.cu")]
 
 
 def deps() -> list:

@@ -30,6 +30,7 @@
 
 #include "../../include/lora_linear.h"
 #include "block.h"
+#include "decode.h"
 #include "side.cuh"
 #include "tc_gemm.cuh"
 #include "tc_gemm2.cuh"
@@ -1155,6 +1156,27 @@ lora_status_t fwd_impl(const uint16_t *x, const Weight &wt, const uint16_t *A, c
     LORA_TRY(prepare(wt.op_fwd(), M, d_in, d_out, r, ws, ws_bytes, stream, &c));
     const float s = alpha / static_cast<float>(r);
     uint16_t *sxa = xa_save ? xa_save : reinterpret_cast<uint16_t *>(c.ws + c.plan.xa);
+    if (fu.op != OP_STORE && M <= lora_host::DECODE_MAX_M) {
+        // a few tokens: the stream of W is spread over all SMs instead of a few tiles
+        lora_host::DecodeArgs d;
+        std::memset(&d, 0, sizeof(d));
+        d.x = x;
+        d.w = wt.coded() ? static_cast<const void *>(wt.Wq) : wt.W;
+        d.wscale = wt.Wscale;
+        if (wt.wf == WF_CB) std::copy(wt.codebook, wt.codebook + 16, d.cb);
+        d.B = B;
+        d.out = h;
+        d.save = fu.save;
+        d.bias = fu.bias;
+        d.residual = fu.residual;
+        d.M = static_cast<int>(M);
+        d.N = static_cast<int>(fu.op == OP_GLU ? d_out / 2 : d_out);
+        d.K = static_cast<int>(d_in);
+        d.r = r;
+        d.act = fu.act;
+        return lora_host::launch_decode(A, sxa, s, wt.wf, fu.op == OP_GLU, d, PLAN_SMS, c.st) == cudaSuccess
+                   ? LORA_OK : LORA_ERR_CUDA;
+    }
     LORA_TRY(c.plan.side ? side_xa(c, x, A, sxa, M, d_in, r, s) : step_xa(c, x, A, sxa, M, d_in, r, s));
     MainOperands o = main_operands(wt, x, sxa, B, h, d_out, d_in);
     o.op = fu.op;

@@ -292,8 +292,13 @@ class lora_plan_t(ctypes.Structure):
         return p
 
 
+plan_epoch = 0  # plans installed or removed so far: a workspace laid out by an earlier plan is not reused
+
+
 def lora_linear_set_plan(M: int, d_in: int, d_out: int, r: int, plan):
     """Install a plan (a lora_plan_t or a dict of its fields) for this shape; None removes it."""
+    global plan_epoch
+    plan_epoch += 1
     fn = load_library().lora_linear_set_plan
     fn.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p]
     fn.restype = ctypes.c_int
@@ -524,26 +529,48 @@ class lora_weight_t(ctypes.Structure):
                 ("codebook", ctypes.c_void_p)]
 
 
-def _weight(W):
+def _need(dev, dtype, *specs):
+    """Each (tensor, name, shape) contiguous, of this type, on the current device `dev`; a
+    tensor of None is left out.  (One pass of cheap comparisons: single tokens are served
+    through here.)"""
+    for t, name, shape in specs:
+        if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+                                  and t.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, the "
+                             f"current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """The stream's handle; None: the current stream of the current device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _weight(W, dev):
     """(lora_weight_t, d_out, d_in, what must outlive the call) of a bf16 tensor [d_out, d_in]
     or of a weight with `kind`, `tensors` and `codebook` (autograd.FrozenWeight)."""
     if isinstance(W, torch.Tensor):
         if W.dim() != 2:
             raise ValueError(f"W: expected a tensor [d_out, d_in], got shape {tuple(W.shape)}")
-        _bf16(W, "W", W.shape)
-        return lora_weight_t(0, W.data_ptr(), None, None), W.shape[0], W.shape[1], None
-    t = W.tensors
-    if W.kind == "bf16":
-        return _weight(t[0])
+        _need(dev, torch.bfloat16, (W, "W", W.shape))
+        return lora_weight_t(0, W.data_ptr()), W.shape[0], W.shape[1], None
+    t, kind = W.tensors, W.kind
+    if kind == "bf16":
+        return _weight(t[0], dev)
     d_out, d_in = W.d_out, W.d_in
     keep = cb = None
-    if W.kind == "fp8":
-        _fp8(t[0], t[1], d_out, d_in)
+    if kind == "fp8":
+        _need(dev, torch.uint8, (t[0], "W8", (d_out, d_in)))
+        _need(dev, torch.bfloat16, (t[1], "W8scale", (d_out,)))
     else:
-        _q4(t[0], t[1], d_out, d_in)
-        if W.kind == "nf4":
+        _need(dev, torch.uint8, (t[0], "Wq", (d_out, d_in // 2)))
+        _need(dev, torch.bfloat16, (t[1], "Wscale", (d_out, d_in // 64)))
+        if kind == "nf4":
             keep, cb = _codebook(W.codebook)
-    return lora_weight_t(WEIGHT_FORMATS[W.kind], t[0].data_ptr(), t[1].data_ptr(), cb), d_out, d_in, keep
+    return lora_weight_t(WEIGHT_FORMATS[kind], t[0].data_ptr(), t[1].data_ptr(), cb), d_out, d_in, keep
 
 
 def _act(act) -> int:
@@ -565,87 +592,78 @@ def act_workspace(op: int, M: int, d_in: int, d_out: int, r: int, device=None) -
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _two_halves(n):
+    if n % 2:
+        raise ValueError(f"W: the gate's and the up projection's rows, got {n}")
+    return n // 2
+
+
 def lora_glu_fwd(x, W, A, B, p, gu_save, xa_save, alpha, act, ws, stream=None):
     """p = act(g) * u with [g | u] = x.W^T + s.(x.A^T).B^T; W: a bf16 tensor [2 d_ff, d_in]
     or a FrozenWeight, the gate's rows first.  gu_save [M, 2 d_ff] and xa_save may be None."""
-    w, n, d_in, keep = _weight(W)
-    M, r = x.shape[0], A.shape[0]
-    for t, name, s in ((x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (p, "p", (M, n // 2))):
-        _bf16(t, name, s)
-    if n % 2:
-        raise ValueError(f"W: the gate's and the up projection's rows, got {n}")
-    if gu_save is not None:
-        _bf16(gu_save, "gu_save", (M, n))
-    if xa_save is not None:
-        _bf16(xa_save, "xa_save", (M, r))
-    st = load_library().lora_glu_fwd(_ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(p), _ptr(gu_save),
-                                     _ptr(xa_save), M, d_in, n // 2, r, float(alpha), _act(act), *_ws(ws),
-                                     _stream(stream))
-    del keep
-    _check(st, "lora_glu_fwd")
+    code, dev = _act(act), torch.cuda.current_device()
+    w, n, d_in, keep = _weight(W, dev)
+    M, r, f = x.shape[0], A.shape[0], _two_halves(n)
+    _need(dev, torch.bfloat16, (x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (p, "p", (M, f)),
+          (gu_save, "gu_save", (M, n)), (xa_save, "xa_save", (M, r)))
+    wp, wn = _ws(ws)
+    st = load_library().lora_glu_fwd(x.data_ptr(), ctypes.byref(w), A.data_ptr(), B.data_ptr(), p.data_ptr(),
+                                     _addr(gu_save), _addr(xa_save), M, d_in, f, r, float(alpha), code, wp, wn,
+                                     _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_glu_fwd")
 
 
 def lora_glu_bwd(dP, gu, x, W, A, B, xa_save, dGU, dX, dA, dB, alpha, act, ws, stream=None):
     """dGU = [dP * u * act'(g) | dP * act(g)] and the layer's dX (or None), dA, dB."""
-    w, n, d_in, keep = _weight(W)
-    M, r = x.shape[0], A.shape[0]
-    if n % 2:
-        raise ValueError(f"W: the gate's and the up projection's rows, got {n}")
-    for t, name, s in ((dP, "dP", (M, n // 2)), (gu, "gu", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)),
-                       (B, "B", (n, r)), (dGU, "dGU", (M, n))):
-        _bf16(t, name, s)
-    if xa_save is not None:
-        _bf16(xa_save, "xa_save", (M, r))
-    if dX is not None:
-        _bf16(dX, "dX", (M, d_in))
-    _f32(dA, "dA", (r, d_in))
-    _f32(dB, "dB", (n, r))
-    st = load_library().lora_glu_bwd(_ptr(dP), _ptr(gu), _ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(xa_save),
-                                     _ptr(dGU), _ptr(dX), _ptr(dA), _ptr(dB), M, d_in, n // 2, r, float(alpha),
-                                     _act(act), *_ws(ws), _stream(stream))
-    del keep
-    _check(st, "lora_glu_bwd")
+    code, dev = _act(act), torch.cuda.current_device()
+    w, n, d_in, keep = _weight(W, dev)
+    M, r, f = x.shape[0], A.shape[0], _two_halves(n)
+    _need(dev, torch.bfloat16, (dP, "dP", (M, f)), (gu, "gu", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)),
+          (B, "B", (n, r)), (dGU, "dGU", (M, n)), (xa_save, "xa_save", (M, r)), (dX, "dX", (M, d_in)))
+    _need(dev, torch.float32, (dA, "dA", (r, d_in)), (dB, "dB", (n, r)))
+    wp, wn = _ws(ws)
+    st = load_library().lora_glu_bwd(dP.data_ptr(), gu.data_ptr(), x.data_ptr(), ctypes.byref(w), A.data_ptr(),
+                                     B.data_ptr(), _addr(xa_save), dGU.data_ptr(), _addr(dX), dA.data_ptr(),
+                                     dB.data_ptr(), M, d_in, f, r, float(alpha), code, wp, wn, _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_glu_bwd")
 
 
 def lora_linear_act_fwd(x, W, A, B, bias, residual, out, pre_save, xa_save, alpha, act, ws, stream=None):
     """out = act(x.W^T + s.(x.A^T).B^T + bias) + residual; W: a bf16 tensor or a FrozenWeight;
     bias [d_out], residual, pre_save [M, d_out] and xa_save may each be None."""
-    w, n, d_in, keep = _weight(W)
+    code, dev = _act(act), torch.cuda.current_device()
+    w, n, d_in, keep = _weight(W, dev)
     M, r = x.shape[0], A.shape[0]
-    for t, name, s in ((x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (out, "out", (M, n))):
-        _bf16(t, name, s)
-    for t, name, s in ((bias, "bias", (n,)), (residual, "residual", (M, n)), (pre_save, "pre_save", (M, n)),
-                       (xa_save, "xa_save", (M, r))):
-        if t is not None:
-            _bf16(t, name, s)
-    st = load_library().lora_linear_act_fwd(_ptr(x), ctypes.byref(w), _ptr(A), _ptr(B), _ptr(bias), _ptr(residual),
-                                            _ptr(out), _ptr(pre_save), _ptr(xa_save), M, d_in, n, r, float(alpha),
-                                            _act(act), *_ws(ws), _stream(stream))
-    del keep
-    _check(st, "lora_linear_act_fwd")
+    _need(dev, torch.bfloat16, (x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)), (out, "out", (M, n)),
+          (bias, "bias", (n,)), (residual, "residual", (M, n)), (pre_save, "pre_save", (M, n)),
+          (xa_save, "xa_save", (M, r)))
+    wp, wn = _ws(ws)
+    st = load_library().lora_linear_act_fwd(x.data_ptr(), ctypes.byref(w), A.data_ptr(), B.data_ptr(), _addr(bias),
+                                            _addr(residual), out.data_ptr(), _addr(pre_save), _addr(xa_save), M, d_in,
+                                            n, r, float(alpha), code, wp, wn, _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_linear_act_fwd")
 
 
 def lora_linear_act_bwd(dOut, pre, x, W, A, B, xa_save, dPre, dX, dA, dB, dbias, alpha, act, ws, stream=None):
     """dPre = dOut * act'(pre), dbias = its sum over the tokens (or None), and the layer's dX
     (or None), dA, dB.  pre and dPre may be None for act "none".  The workspace is
     act_workspace's."""
-    w, n, d_in, keep = _weight(W)
+    code, dev = _act(act), torch.cuda.current_device()
+    w, n, d_in, keep = _weight(W, dev)
     M, r = x.shape[0], A.shape[0]
-    for t, name, s in ((dOut, "dOut", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r))):
-        _bf16(t, name, s)
-    for t, name, s in ((pre, "pre", (M, n)), (dPre, "dPre", (M, n)), (xa_save, "xa_save", (M, r)),
-                       (dX, "dX", (M, d_in))):
-        if t is not None:
-            _bf16(t, name, s)
-    _f32(dA, "dA", (r, d_in))
-    _f32(dB, "dB", (n, r))
-    if dbias is not None:
-        _f32(dbias, "dbias", (n,))
-    st = load_library().lora_linear_act_bwd(_ptr(dOut), _ptr(pre), _ptr(x), ctypes.byref(w), _ptr(A), _ptr(B),
-                                            _ptr(xa_save), _ptr(dPre), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(dbias), M,
-                                            d_in, n, r, float(alpha), _act(act), *_ws(ws), _stream(stream))
-    del keep
-    _check(st, "lora_linear_act_bwd")
+    _need(dev, torch.bfloat16, (dOut, "dOut", (M, n)), (x, "x", (M, d_in)), (A, "A", (r, d_in)), (B, "B", (n, r)),
+          (pre, "pre", (M, n)), (dPre, "dPre", (M, n)), (xa_save, "xa_save", (M, r)), (dX, "dX", (M, d_in)))
+    _need(dev, torch.float32, (dA, "dA", (r, d_in)), (dB, "dB", (n, r)), (dbias, "dbias", (n,)))
+    wp, wn = _ws(ws)
+    st = load_library().lora_linear_act_bwd(dOut.data_ptr(), _addr(pre), x.data_ptr(), ctypes.byref(w), A.data_ptr(),
+                                            B.data_ptr(), _addr(xa_save), _addr(dPre), _addr(dX), dA.data_ptr(),
+                                            dB.data_ptr(), _addr(dbias), M, d_in, n, r, float(alpha), code, wp, wn,
+                                            _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_linear_act_bwd")
 
 
 class lora_heads_t(ctypes.Structure):
@@ -654,19 +672,19 @@ class lora_heads_t(ctypes.Structure):
                 ("heads", ctypes.c_int32)]
 
 
-def _heads(t, name, M, D, dtype, heads=None):
-    """A tensor [M, heads, D] with its last dimension contiguous, by reference; None for None."""
+def _heads(t, name, shape, dtype, dev):
+    """A tensor of `shape` = [M, heads, D] with its last dimension contiguous, by reference; None
+    for None."""
     if t is None:
         return None
-    if t.dim() != 3 or t.dtype != dtype or t.shape[0] != M or t.shape[2] != D or t.stride(2) != 1 or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: expected a {dtype} tensor [{M}, {'heads' if heads is None else heads}, {D}], its last "
-                         f"dimension contiguous, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    _on_current_device(t, name)
-    return ctypes.byref(lora_heads_t(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]))
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or st[2] != 1 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} on cuda:{dev}, the current device, its last "
+                         f"dimension contiguous, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return ctypes.byref(lora_heads_t(t.data_ptr(), st[0], st[1], shape[1]))
 
 
-def _head_args(q, k, q_weight, k_weight, cos, sin, positions):
+def _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev):
     """(M, D, dtype, rot, n_pos) of a call, its weights, tables and positions checked."""
     one = q if q is not None else k
     if one is None or one.dim() != 3:
@@ -674,22 +692,16 @@ def _head_args(q, k, q_weight, k_weight, cos, sin, positions):
     (M, _, D), dtype = one.shape, one.dtype
     if dtype not in HEAD_DTYPES:
         raise ValueError(f"q, k: one of {sorted(map(str, HEAD_DTYPES))}, got {dtype}")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if w.dtype != dtype or tuple(w.shape) != (D,) or not w.is_contiguous():
-                raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {(D,)}")
-            _on_current_device(w, name)
+    if q is not None and k is not None and (k.dim() != 3 or k.shape[0] != M or k.shape[2] != D):
+        raise ValueError(f"k: expected [{M}, heads, {D}] as q, got {tuple(k.shape)}")
+    _need(dev, dtype, (q_weight, "q_weight", (D,)), (k_weight, "k_weight", (D,)))
     if cos is None:
         return M, D, dtype, 0, 0
     if sin is None or positions is None or cos.dim() != 2:
         raise ValueError("cos, sin [n_pos, rot / 2] and positions go together")
-    n_pos, half = cos.shape
-    _f32(cos, "cos", (n_pos, half))
-    _f32(sin, "sin", (n_pos, half))
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (M,) or not positions.is_contiguous():
-        raise ValueError(f"positions: expected a contiguous int64 tensor of shape {(M,)}")
-    _on_current_device(positions, "positions")
-    return M, D, dtype, 2 * half, n_pos
+    _need(dev, torch.float32, (cos, "cos", cos.shape), (sin, "sin", cos.shape))
+    _need(dev, torch.int64, (positions, "positions", (M,)))
+    return M, D, dtype, 2 * cos.shape[1], cos.shape[0]
 
 
 def lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps=1e-6, interleaved=False,
@@ -698,13 +710,15 @@ def lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, 
     weights, the first 2 * cos.shape[1] dimensions rotated by the angles of the tokens'
     positions.  q or k, the weights, and cos with sin and positions may be None; q_out may be
     q, and k_out k."""
-    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions)
-    hq, hk = (None if t is None else t.shape[1] for t in (q, k))
+    dev = torch.cuda.current_device()
+    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev)
+    qs, ks = None if q is None else q.shape, None if k is None else k.shape
     st = load_library().lora_qk_norm_rope_fwd(
-        HEAD_DTYPES[dtype], _heads(q, "q", M, D, dtype), _heads(k, "k", M, D, dtype), _ptr(q_weight), _ptr(k_weight),
-        _ptr(cos), _ptr(sin), _ptr(positions), n_pos, _heads(q_out, "q_out", M, D, dtype, hq),
-        _heads(k_out, "k_out", M, D, dtype, hk), M, D, rot, int(interleaved), int(norm), float(eps), _stream(stream))
-    _check(st, "lora_qk_norm_rope_fwd")
+        HEAD_DTYPES[dtype], _heads(q, "q", qs, dtype, dev), _heads(k, "k", ks, dtype, dev), _addr(q_weight),
+        _addr(k_weight), _addr(cos), _addr(sin), _addr(positions), n_pos, _heads(q_out, "q_out", qs, dtype, dev),
+        _heads(k_out, "k_out", ks, dtype, dev), M, D, rot, interleaved, norm, float(eps), _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_qk_norm_rope_fwd")
 
 
 def lora_qk_norm_rope_workspace_size(M: int, heads: int, D: int) -> int:
@@ -716,15 +730,15 @@ def lora_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
     """dq, dk (each may be its dq_out / dk_out, in place) and the fp32 weight gradients [D] (or
     None) from the forward's inputs.  ws: lora_qk_norm_rope_workspace_size bytes, or None where
     neither weight gradient is asked for."""
-    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions)
-    hq, hk = (None if t is None else t.shape[1] for t in (q, k))
-    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-        if t is not None:
-            _f32(t, name, (D,))
+    dev = torch.cuda.current_device()
+    M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev)
+    qs, ks = None if q is None else q.shape, None if k is None else k.shape
+    _need(dev, torch.float32, (dq_weight, "dq_weight", (D,)), (dk_weight, "dk_weight", (D,)))
     wp, wn = (None, 0) if ws is None else _ws(ws)
     st = load_library().lora_qk_norm_rope_bwd(
-        HEAD_DTYPES[dtype], _heads(dq_out, "dq_out", M, D, dtype, hq), _heads(dk_out, "dk_out", M, D, dtype, hk),
-        _heads(q, "q", M, D, dtype), _heads(k, "k", M, D, dtype), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-        _ptr(positions), n_pos, _heads(dq, "dq", M, D, dtype, hq), _heads(dk, "dk", M, D, dtype, hk), _ptr(dq_weight),
-        _ptr(dk_weight), M, D, rot, int(interleaved), int(norm), float(eps), wp, wn, _stream(stream))
-    _check(st, "lora_qk_norm_rope_bwd")
+        HEAD_DTYPES[dtype], _heads(dq_out, "dq_out", qs, dtype, dev), _heads(dk_out, "dk_out", ks, dtype, dev),
+        _heads(q, "q", qs, dtype, dev), _heads(k, "k", ks, dtype, dev), _addr(q_weight), _addr(k_weight), _addr(cos),
+        _addr(sin), _addr(positions), n_pos, _heads(dq, "dq", qs, dtype, dev), _heads(dk, "dk", ks, dtype, dev),
+        _addr(dq_weight), _addr(dk_weight), M, D, rot, interleaved, norm, float(eps), wp, wn, _raw_stream(stream, dev))
+    if st:
+        raise LoraError(st, "lora_qk_norm_rope_bwd")
