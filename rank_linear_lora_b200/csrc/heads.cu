@@ -33,8 +33,13 @@ namespace {
 using namespace lora;
 
 constexpr int WARPS = 8;
-constexpr int FWD_HEADS = 4;  // heads per group in flight, forward
-constexpr int BWD_HEADS = 2;  // backward (two inputs)
+// Heads of a group in flight.  Forward: two, at three CTAs an SM (16384 tokens of 40 heads of
+// 128 in bf16: 61 us; three heads at three CTAs 69, two at four 68, four at two 72, registers
+// spilling or loads too few).  Backward, two inputs: one where a vector holds 8 elements (8192
+// tokens: 60 us; two 61, spilling), two where it holds 4 (1999 tokens of 10 fp32 heads: 11.4 us
+// against 14.0).
+constexpr int FWD_HEADS = 2;
+__host__ __device__ constexpr int bwd_heads(int V) { return V == 4 ? 2 : 1; }
 constexpr int SMS = 148;
 
 // One of q and k.
@@ -62,66 +67,126 @@ struct HeadArgs {
     float *partials;  // backward: [CTAs][D], or null
 };
 
+// ------------------------------------------------------------------ pairs of fp32
+// Arithmetic runs on pairs of neighbouring elements (the packed fp32 instructions), which
+// halves the instructions of a kernel that issue would bound otherwise.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 swap2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack2(hi, lo);
+}
+__device__ __forceinline__ float hsum2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return lo + hi;
+}
+
 // ------------------------------------------------------------------ element types
+// A 32-bit word of two 16-bit elements to a pair and back (one rounding).
 template <class T>
 struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
-    static __device__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
-    static __device__ __nv_bfloat16 put(float f) { return __float2bfloat16_rn(f); }
+    static __device__ f2 get(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    static __device__ uint32_t put(f2 v) {
+        float lo, hi;
+        unpack2(v, lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
 };
 template <>
 struct Elem<__half> {
-    static __device__ float get(__half v) { return __half2float(v); }
-    static __device__ __half put(float f) { return __float2half_rn(f); }
-};
-template <>
-struct Elem<float> {
-    static __device__ float get(float v) { return v; }
-    static __device__ float put(float f) { return f; }
-};
-
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-    using type = uint4;
-};
-template <>
-struct Raw<8> {
-    using type = uint2;
+    static __device__ f2 get(uint32_t w) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        return pack2(f.x, f.y);
+    }
+    static __device__ uint32_t put(f2 v) {
+        float lo, hi;
+        unpack2(v, lo, hi);
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
 };
 
-// A vector of V elements as loaded.
+// A vector of V elements as loaded: V * sizeof(T) is 16 or 8 bytes.
 template <class T, int V>
 struct Vec {
-    typename Raw<V * sizeof(T)>::type raw;
-    __device__ void load(const T *p) { raw = __ldcs(reinterpret_cast<const decltype(raw) *>(p)); }
-    __device__ void load_kept(const T *p) { raw = __ldg(reinterpret_cast<const decltype(raw) *>(p)); }
-    __device__ void clear() { raw = decltype(raw)(); }
-    __device__ void get(float (&f)[V]) const {
-        const T *e = reinterpret_cast<const T *>(&raw);
+    static constexpr int W = V * sizeof(T) / 4;  // 32-bit words
+    uint32_t w[W];
+    __device__ void clear() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = Elem<T>::get(e[i]);
+        for (int i = 0; i < W; ++i) w[i] = 0;
     }
-    __device__ void put(const float (&f)[V]) {
-        T *e = reinterpret_cast<T *>(&raw);
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = Elem<T>::put(f[i]);
+    __device__ void load(const T *p) {  // read once: past L1
+        if constexpr (W == 4)
+            asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "l"(p));
+        else
+            asm volatile("ld.global.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     }
-    __device__ void store(T *p) const { *reinterpret_cast<decltype(raw) *>(p) = raw; }
+    __device__ void load_kept(const T *p) {
+        if constexpr (W == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = v.x, w[1] = v.y;
+        }
+    }
+    __device__ void store(T *p) const {
+        // written once: streaming stores keep them from evicting what is still to be read
+        // (16384 tokens of 40 heads of 128 in bf16: 65.7 -> 62.5 us)
+        if constexpr (W == 4) __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+        else __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0], w[1]));
+    }
+    __device__ f2 get(int i) const {  // elements 2 i, 2 i + 1
+        if constexpr (sizeof(T) == 4) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return Elem<T>::get(w[i]);
+    }
+    __device__ void put(int i, f2 v) {
+        if constexpr (sizeof(T) == 4) {
+            float lo, hi;
+            unpack2(v, lo, hi);
+            w[2 * i] = __float_as_uint(lo);
+            w[2 * i + 1] = __float_as_uint(hi);
+        } else {
+            w[i] = Elem<T>::put(v);
+        }
+    }
 };
 
 // ------------------------------------------------------------------ a lane's share of a head
 // Slots of V elements.  Halves: slot 0 is vector p of the first rot/2 dimensions, slot 1
 // its partner, slots 2.. (NS of them) the dimensions behind the rotation.  INTER: two slots
-// over all of D, pairs inside a vector.
+// over all of D, partners next to each other.  So in either layout a rotated pair of
+// elements is  own * c + partner * (+-s)  with the partner in the other slot, or swapped.
 template <int V, bool INTER, int NS>
 struct Lane {
     static constexpr int SLOTS = INTER ? 2 : 2 + NS;
+    static constexpr int P = V / 2;  // pairs of a slot
     int off[SLOTS];   // first dimension
     bool has[SLOTS];
-    float c[V], s[V];  // halves: of the vector's dimensions; INTER: V/2 pairs per slot
 
     __device__ void place(int D, int rot, int p, int L) {
         if constexpr (INTER) {
@@ -141,92 +206,118 @@ struct Lane {
             }
         }
     }
-    // cos and sin of a token; a position outside the table makes the rotated dimensions NaN
-    __device__ void angles(const HeadArgs &a, int64_t token) {
+
+    // cos and sin of a token's position: halves, of the vector's dimensions (they serve slots 0
+    // and 1); INTER, of each slot's pairs, an angle twice.  Without a rotation 1 and 0; a
+    // position outside the table reads nothing and gives NaN.
+    static constexpr int TURNS = INTER ? 2 : 1;
+    __device__ void angles(const HeadArgs &a, int64_t pos, f2 (&c)[TURNS][P], f2 (&s)[TURNS][P]) const {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            c[e] = 1.0f;
-            s[e] = 0.0f;
-        }
-        if (a.rot == 0) return;
-        const int64_t pos = __ldg(a.pos + token);
-        const bool ok = pos >= 0 && pos < a.n_pos;
-        const int64_t row = ok ? pos * (a.rot / 2) : 0;
-        constexpr int N = INTER ? V / 2 : V;  // table entries of a slot
+        for (int i = 0; i < TURNS; ++i)
 #pragma unroll
-        for (int i = 0; i < (INTER ? 2 : 1); ++i) {
-            if (!has[i] || (INTER && off[i] >= a.rot)) continue;
-            const int64_t at = row + (INTER ? off[i] / 2 : off[i]);
-#pragma unroll
-            for (int e = 0; e < N; e += (N < 4 ? 2 : 4)) {
-                if constexpr (N < 4) {
-                    const float2 fc = __ldg(reinterpret_cast<const float2 *>(a.cos + at + e));
-                    const float2 fs = __ldg(reinterpret_cast<const float2 *>(a.sin + at + e));
-                    c[i * N + e] = fc.x, c[i * N + e + 1] = fc.y;
-                    s[i * N + e] = fs.x, s[i * N + e + 1] = fs.y;
-                } else {
-                    const float4 fc = __ldg(reinterpret_cast<const float4 *>(a.cos + at + e));
-                    const float4 fs = __ldg(reinterpret_cast<const float4 *>(a.sin + at + e));
-                    c[i * N + e] = fc.x, c[i * N + e + 1] = fc.y, c[i * N + e + 2] = fc.z, c[i * N + e + 3] = fc.w;
-                    s[i * N + e] = fs.x, s[i * N + e + 1] = fs.y, s[i * N + e + 2] = fs.z, s[i * N + e + 3] = fs.w;
-                }
+            for (int e = 0; e < P; ++e) {
+                c[i][e] = pack2(1.0f, 1.0f);
+                s[i][e] = 0;
             }
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (!ok) c[i * N + e] = s[i * N + e] = __int_as_float(0x7fc00000);
-        }
-    }
-    // rotate by the angles (sign 1) or back (sign -1)
-    template <int SIGN>
-    __device__ void rotate(float (&v)[SLOTS][V]) const {
+        if (a.rot == 0) return;
+        const bool ok = pos >= 0 && pos < a.n_pos;
+        const float bad = ok ? 0.0f : __int_as_float(0x7fc00000);
+        const float *cr = a.cos + (ok ? pos * (a.rot / 2) : 0), *sr = a.sin + (ok ? pos * (a.rot / 2) : 0);
         if constexpr (INTER) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                if (!has[i] || off[i] >= a.rot) continue;
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) {
-                    const float x = v[i][2 * e], y = v[i][2 * e + 1];
-                    const float cc = c[i * (V / 2) + e], ss = SIGN * s[i * (V / 2) + e];
-                    v[i][2 * e] = x * cc - y * ss;
-                    v[i][2 * e + 1] = y * cc + x * ss;
+                for (int e = 0; e < P; e += 2) {  // entry e belongs to the elements 2 e, 2 e + 1
+                    const float2 fc = __ldg(reinterpret_cast<const float2 *>(cr + off[i] / 2 + e));
+                    const float2 fs = __ldg(reinterpret_cast<const float2 *>(sr + off[i] / 2 + e));
+                    c[i][e] = pack2(fc.x + bad, fc.x + bad);
+                    c[i][e + 1] = pack2(fc.y + bad, fc.y + bad);
+                    s[i][e] = pack2(fs.x, fs.x);
+                    s[i][e + 1] = pack2(fs.y, fs.y);
                 }
+            }
         } else {
+            if (!has[0]) return;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float x = v[0][e], y = v[1][e], ss = SIGN * s[e];
-                v[0][e] = x * c[e] - y * ss;
-                v[1][e] = y * c[e] + x * ss;
+            for (int e = 0; e < P; e += 2) {
+                const float4 fc = __ldg(reinterpret_cast<const float4 *>(cr + off[0] + 2 * e));
+                const float4 fs = __ldg(reinterpret_cast<const float4 *>(sr + off[0] + 2 * e));
+                c[0][e] = pack2(fc.x + bad, fc.y + bad);
+                c[0][e + 1] = pack2(fc.z + bad, fc.w + bad);
+                s[0][e] = pack2(fs.x, fs.y);
+                s[0][e + 1] = pack2(fs.z, fs.w);
             }
         }
     }
+    static __device__ f2 partner(const f2 (&v)[SLOTS][P], int i, int e) { return INTER ? swap2(v[i][e]) : v[1 - i][e]; }
 };
 
-// Sum over the L lanes of a head (all 32 lanes take part).
-__device__ __forceinline__ float sum_head(float v, int log_l) {
-    for (int i = 0; i < log_l; ++i) v += __shfl_xor_sync(0xffffffffu, v, 1 << i);
-    return v;
+// v rotated back by the angles, in place:  v_a c + v_b s,  v_b c - v_a s.
+template <int V, bool INTER, int NS>
+__device__ __forceinline__ void rotate_back(f2 (&v)[Lane<V, INTER, NS>::SLOTS][V / 2],
+                                            const f2 (&c)[INTER ? 2 : 1][V / 2], const f2 (&s)[INTER ? 2 : 1][V / 2]) {
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+        if constexpr (INTER) {
+            const f2 sign = pack2(1.0f, -1.0f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) v[i][e] = fma2(swap2(v[i][e]), mul2(s[i][e], sign), mul2(v[i][e], c[i][e]));
+        } else {
+            const f2 a = v[0][e], b = v[1][e];
+            v[0][e] = fma2(b, s[0][e], mul2(a, c[0][e]));
+            v[1][e] = fma2(mul2(a, s[0][e]), pack2(-1.0f, -1.0f), mul2(b, c[0][e]));
+        }
+    }
 }
 
-// The weight of a lane's slots, as loaded (ones without a weight).
+// Each of N values summed over the L lanes of a head (all 32 lanes take part); together, so
+// that their shuffles overlap.
+template <int N>
+__device__ __forceinline__ void sum_head(float (&v)[N], int log_l) {
+#pragma unroll 1
+    for (int m = 1; m < (1 << log_l); m <<= 1) {
+        float o[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[n] = __shfl_xor_sync(0xffffffffu, v[n], m);
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += o[n];
+    }
+}
+
+// The weight of a lane's slots as loaded (ones without a weight).
 template <class T, int V, class LaneT>
 __device__ __forceinline__ void load_weight(const HeadTensor &t, const LaneT &ln, Vec<T, V> (&w)[LaneT::SLOTS]) {
 #pragma unroll
     for (int i = 0; i < LaneT::SLOTS; ++i) {
-        if (t.weight && ln.has[i]) {
-            w[i].load_kept(static_cast<const T *>(t.weight) + ln.off[i]);
-        } else {
-            float one[V];
+        w[i].clear();
+        if (t.weight && ln.has[i]) w[i].load_kept(static_cast<const T *>(t.weight) + ln.off[i]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) one[e] = 1.0f;
-            w[i].put(one);
-        }
+        for (int e = 0; e < V / 2; ++e)
+            if (!t.weight) w[i].put(e, pack2(1.0f, 1.0f));
     }
 }
 
+// Unit u of a tensor: its token and the first of its heads.
+__device__ __forceinline__ int64_t unit_token(const HeadTensor &t, int64_t u, int &h_lo) {
+    if (t.splits == 1) {
+        h_lo = 0;
+        return u;
+    }
+    const int64_t token = u / t.splits;
+    h_lo = static_cast<int>(u - token * t.splits) * t.per_unit;
+    return token;
+}
+
+__device__ __forceinline__ int64_t position(const HeadArgs &a, int64_t token) { return a.rot ? __ldg(a.pos + token) : 0; }
+
 // ------------------------------------------------------------------ forward
+// The weight goes into the rotation's coefficients once a token:
+//   y = i (own * (w c) + partner * (w_partner q))
 template <class T, int V, bool INTER, int NS>
-__global__ void __launch_bounds__(WARPS * 32) k_heads_fwd(const __grid_constant__ HeadArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, NS ? 2 : 3) k_heads_fwd(const __grid_constant__ HeadArgs a) {
     using LaneT = Lane<V, INTER, NS>;
-    constexpr int SL = LaneT::SLOTS;
+    constexpr int SL = LaneT::SLOTS, P = V / 2;
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -235,65 +326,92 @@ __global__ void __launch_bounds__(WARPS * 32) k_heads_fwd(const __grid_constant_
     if (which) u -= a.t[0].units;
     const HeadTensor &t = a.t[which];
     if (u >= t.units) return;
-    const int64_t token = u / t.splits;
-    const int h_lo = static_cast<int>(u - token * t.splits) * t.per_unit;
+    int h_lo;
+    const int64_t token = unit_token(t, u, h_lo);
+    const int64_t pos = position(a, token);
     const int h_hi = min(t.heads, h_lo + t.per_unit);
     const int L = 1 << a.log_l, G = 32 >> a.log_l, g = lane >> a.log_l;
     LaneT ln;
     ln.place(a.D, a.rot, lane & (L - 1), L);
-    const T *in = static_cast<const T *>(t.in) + token * t.in_ts;
-    T *out = static_cast<T *>(t.out) + token * t.out_ts;
-    Vec<T, V> w[SL];
-    for (int h0 = h_lo + g; h0 - g < h_hi; h0 += G * FWD_HEADS) {
+    const T *in = static_cast<const T *>(t.in) + token * t.in_ts + (h_lo + g) * t.in_hs;
+    T *out = static_cast<T *>(t.out) + token * t.out_ts + (h_lo + g) * t.out_hs;
+    const int64_t in_step = G * t.in_hs, out_step = G * t.out_hs;
+    f2 c[2][P], q[2][P], w[SL][P];
+    for (int h0 = h_lo; h0 < h_hi; h0 += G * FWD_HEADS) {
         Vec<T, V> x[FWD_HEADS][SL];
 #pragma unroll
-        for (int j = 0; j < FWD_HEADS; ++j)
+        for (int j = 0; j < FWD_HEADS; ++j) {
+            const bool mine = h0 + g + j * G < h_hi;
 #pragma unroll
             for (int i = 0; i < SL; ++i) {
                 x[j][i].clear();
-                if (h0 + j * G < h_hi && ln.has[i]) x[j][i].load(in + (h0 + j * G) * t.in_hs + ln.off[i]);
+                if (mine && ln.has[i]) x[j][i].load(in + ln.off[i]);
             }
-        if (h0 - g == h_lo) {  // behind the first heads' loads
-            ln.angles(a, token);
-            load_weight<T, V>(t, ln, w);
+            in += in_step;
         }
+        if (h0 == h_lo) {  // behind the first heads' loads
+            f2 co[LaneT::TURNS][P], si[LaneT::TURNS][P];
+            ln.angles(a, pos, co, si);
+            Vec<T, V> raw[SL];
+            load_weight<T, V>(t, ln, raw);
+#pragma unroll
+            for (int i = 0; i < SL; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) w[i][e] = raw[i].get(e);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const f2 sign = INTER ? pack2(-1.0f, 1.0f) : i ? pack2(1.0f, 1.0f) : pack2(-1.0f, -1.0f);
+                    c[i][e] = mul2(co[INTER ? i : 0][e], w[i][e]);
+                    q[i][e] = mul2(mul2(si[INTER ? i : 0][e], sign), LaneT::partner(w, i, e));
+                }
+        }
+        float ss[FWD_HEADS];
 #pragma unroll
         for (int j = 0; j < FWD_HEADS; ++j) {
-            float v[SL][V], ss = 0.0f;
+            f2 sq = 0;
+#pragma unroll
+            for (int i = 0; i < SL; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const f2 v = x[j][i].get(e);
+                    sq = fma2(v, v, sq);
+                }
+            ss[j] = hsum2(sq);
+        }
+        sum_head(ss, a.log_l);
+#pragma unroll
+        for (int j = 0; j < FWD_HEADS; ++j) {
+            f2 v[SL][P];
+#pragma unroll
+            for (int i = 0; i < SL; ++i)
+#pragma unroll
+                for (int e = 0; e < P; ++e) v[i][e] = x[j][i].get(e);
+            const float inv = a.norm ? rsqrtf(ss[j] * a.inv_d + a.eps) : 1.0f;
+            const f2 inv2 = pack2(inv, inv);
+            const bool mine = h0 + g + j * G < h_hi;
 #pragma unroll
             for (int i = 0; i < SL; ++i) {
-                x[j][i].get(v[i]);
+                Vec<T, V> y;
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss += v[i][e] * v[i][e];
+                for (int e = 0; e < P; ++e) {
+                    const f2 r = i < 2 ? fma2(LaneT::partner(v, i, e), q[i < 2 ? i : 0][e], mul2(v[i][e], c[i < 2 ? i : 0][e]))
+                                       : mul2(v[i][e], w[i][e]);
+                    y.put(e, mul2(r, inv2));
+                }
+                if (mine && ln.has[i]) y.store(out + ln.off[i]);
             }
-            ss = sum_head(ss, a.log_l);
-            const float inv = a.norm ? rsqrtf(ss * a.inv_d + a.eps) : 1.0f;
-#pragma unroll
-            for (int i = 0; i < SL; ++i) {
-                float f[V];
-                w[i].get(f);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[i][e] = v[i][e] * inv * f[e];
-            }
-            ln.template rotate<1>(v);
-            if (h0 + j * G < h_hi) {
-#pragma unroll
-                for (int i = 0; i < SL; ++i)
-                    if (ln.has[i]) {
-                        Vec<T, V> y;
-                        y.put(v[i]);
-                        y.store(out + (h0 + j * G) * t.out_hs + ln.off[i]);
-                    }
-            }
+            out += out_step;
         }
     }
 }
 
 // ------------------------------------------------------------------ backward
 template <class T, int V, bool INTER, int NS>
-__global__ void __launch_bounds__(WARPS * 32) k_heads_bwd(const __grid_constant__ HeadArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __grid_constant__ HeadArgs a) {
     using LaneT = Lane<V, INTER, NS>;
-    constexpr int SL = LaneT::SLOTS;
+    constexpr int SL = LaneT::SLOTS, P = V / 2, BWD_HEADS = bwd_heads(V);
     __shared__ float red[WARPS][256];
     grid_dep_wait();
     grid_dep_launch_dependents();
@@ -304,80 +422,112 @@ __global__ void __launch_bounds__(WARPS * 32) k_heads_bwd(const __grid_constant_
     const int L = 1 << a.log_l, G = 32 >> a.log_l, g = lane >> a.log_l;
     LaneT ln;
     ln.place(a.D, a.rot, lane & (L - 1), L);
-    Vec<T, V> w[SL];
+    const int64_t in_step = G * t.in_hs, dy_step = G * t.dy_hs, out_step = G * t.out_hs;
+    Vec<T, V> w[SL];  // as loaded: half the registers
+    f2 dw[SL][P];
     load_weight<T, V>(t, ln, w);
-    float dw[SL][V] = {};
-    for (int64_t u = static_cast<int64_t>(cta) * WARPS + warp; u < t.units; u += static_cast<int64_t>(t.ctas) * WARPS) {
-        const int64_t token = u / t.splits;
-        const int h_lo = static_cast<int>(u - token * t.splits) * t.per_unit;
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+#pragma unroll
+        for (int e = 0; e < P; ++e) dw[i][e] = 0;
+    const int64_t stride = static_cast<int64_t>(t.ctas) * WARPS;
+    int64_t u = static_cast<int64_t>(cta) * WARPS + warp;
+    int h_lo = 0;
+    int64_t token = u < t.units ? unit_token(t, u, h_lo) : 0;
+    int64_t pos = u < t.units ? position(a, token) : 0;  // one unit ahead of its use
+    while (u < t.units) {
         const int h_hi = min(t.heads, h_lo + t.per_unit);
-        const T *in = static_cast<const T *>(t.in) + token * t.in_ts;
-        const T *dy = static_cast<const T *>(t.dy) + token * t.dy_ts;
-        T *out = static_cast<T *>(t.out) + token * t.out_ts;
-        for (int h0 = h_lo + g; h0 - g < h_hi; h0 += G * BWD_HEADS) {
+        const T *in = static_cast<const T *>(t.in) + token * t.in_ts + (h_lo + g) * t.in_hs;
+        const T *dy = static_cast<const T *>(t.dy) + token * t.dy_ts + (h_lo + g) * t.dy_hs;
+        T *out = static_cast<T *>(t.out) + token * t.out_ts + (h_lo + g) * t.out_hs;
+        int next_lo = 0;
+        int64_t next_token = 0;
+        f2 c[LaneT::TURNS][P], s[LaneT::TURNS][P];
+        for (int h0 = h_lo; h0 < h_hi; h0 += G * BWD_HEADS) {
             Vec<T, V> x[BWD_HEADS][SL], d[BWD_HEADS][SL];
 #pragma unroll
-            for (int j = 0; j < BWD_HEADS; ++j)
+            for (int j = 0; j < BWD_HEADS; ++j) {
+                const bool mine = h0 + g + j * G < h_hi;
 #pragma unroll
                 for (int i = 0; i < SL; ++i) {
                     x[j][i].clear();
                     d[j][i].clear();
-                    if (h0 + j * G < h_hi && ln.has[i]) {
-                        x[j][i].load(in + (h0 + j * G) * t.in_hs + ln.off[i]);
-                        d[j][i].load(dy + (h0 + j * G) * t.dy_hs + ln.off[i]);
+                    if (mine && ln.has[i]) {
+                        x[j][i].load(in + ln.off[i]);
+                        d[j][i].load(dy + ln.off[i]);
                     }
                 }
-            if (h0 - g == h_lo) ln.angles(a, token);
-#pragma unroll
-            for (int j = 0; j < BWD_HEADS; ++j) {
-                float v[SL][V], dn[SL][V], ss = 0.0f, st = 0.0f;
-#pragma unroll
-                for (int i = 0; i < SL; ++i) {
-                    x[j][i].get(v[i]);
-                    d[j][i].get(dn[i]);
-                }
-                ln.template rotate<-1>(dn);
-#pragma unroll
-                for (int i = 0; i < SL; ++i) {
-                    float f[V];
-                    w[i].get(f);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        ss += v[i][e] * v[i][e];
-                        st += v[i][e] * dn[i][e] * f[e];
-                    }
-                }
-                ss = sum_head(ss, a.log_l);
-                st = sum_head(st, a.log_l);
-                const float inv = a.norm ? rsqrtf(ss * a.inv_d + a.eps) : 1.0f;
-                const float m = a.norm ? inv * inv * st * a.inv_d : 0.0f;  // v m = e mean(e dn w)
-                const bool mine = h0 + j * G < h_hi;
-#pragma unroll
-                for (int i = 0; i < SL; ++i) {
-                    if (!mine || !ln.has[i]) continue;
-                    float f[V];
-                    w[i].get(f);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        dw[i][e] += dn[i][e] * (v[i][e] * inv);
-                        f[e] = inv * (dn[i][e] * f[e] - v[i][e] * m);
-                    }
-                    Vec<T, V> y;
-                    y.put(f);
-                    y.store(out + (h0 + j * G) * t.out_hs + ln.off[i]);
+                in += in_step;
+                dy += dy_step;
+            }
+            if (h0 == h_lo) {
+                ln.angles(a, pos, c, s);
+                u += stride;
+                if (u < t.units) {
+                    next_token = unit_token(t, u, next_lo);
+                    pos = position(a, next_token);
                 }
             }
+            f2 dn[BWD_HEADS][SL][P];         // the gradient rotated back
+            float sums[2 * BWD_HEADS];       // of v^2 and of v dn w
+#pragma unroll
+            for (int j = 0; j < BWD_HEADS; ++j) {
+                f2 sq = 0, st = 0;
+#pragma unroll
+                for (int i = 0; i < SL; ++i)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) dn[j][i][e] = d[j][i].get(e);
+                rotate_back<V, INTER, NS>(dn[j], c, s);
+#pragma unroll
+                for (int i = 0; i < SL; ++i)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const f2 v = x[j][i].get(e);
+                        sq = fma2(v, v, sq);
+                        st = fma2(v, mul2(dn[j][i][e], w[i].get(e)), st);
+                    }
+                sums[2 * j] = hsum2(sq);
+                sums[2 * j + 1] = hsum2(st);
+            }
+            sum_head(sums, a.log_l);
+#pragma unroll
+            for (int j = 0; j < BWD_HEADS; ++j) {
+                const float inv = a.norm ? rsqrtf(sums[2 * j] * a.inv_d + a.eps) : 1.0f;
+                // i (dn w - v i^2 mean(v dn w)) = i dn w + v k
+                const float k = a.norm ? -(inv * inv) * (sums[2 * j + 1] * a.inv_d) * inv : 0.0f;
+                const f2 inv2 = pack2(inv, inv), k2 = pack2(k, k);
+                const bool mine = h0 + g + j * G < h_hi;
+#pragma unroll
+                for (int i = 0; i < SL; ++i) {
+                    Vec<T, V> y;
+                    if (!mine || !ln.has[i]) continue;
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        const f2 v = x[j][i].get(e), di = mul2(dn[j][i][e], inv2);
+                        dw[i][e] = fma2(di, v, dw[i][e]);
+                        y.put(e, fma2(v, k2, mul2(di, w[i].get(e))));
+                    }
+                    y.store(out + ln.off[i]);
+                }
+                out += out_step;
+            }
         }
+        token = next_token;
+        h_lo = next_lo;
     }
     if (!a.partials) return;
     // over the warp's groups, then over the CTA's warps
 #pragma unroll
     for (int i = 0; i < SL; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float v = dw[i][e];
-            for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (g == 0 && ln.has[i]) red[warp][ln.off[i] + e] = v;
+        for (int e = 0; e < P; ++e) {
+            float v[2];
+            unpack2(dw[i][e], v[0], v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                for (int o = L; o < 32; o <<= 1) v[h] += __shfl_xor_sync(0xffffffffu, v[h], o);
+                if (g == 0 && ln.has[i]) red[warp][ln.off[i] + 2 * e + h] = v[h];
+            }
         }
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < a.D) {
@@ -465,11 +615,14 @@ lora_status_t check_heads(const lora_heads_t *t, int heads, int esize, int vec_b
     return LORA_OK;
 }
 
-// Heads a warp takes of one token: all of them, halved while the warps are too few to fill
-// the device (eight an SM), down to one round of the warp's groups.
-void fill_units(HeadTensor &t, int64_t M, int group_heads, int all_heads) {
+// Heads a warp takes of one token: all of them, halved while the tensor has fewer than `want`
+// units, down to one batch of the warp's groups; then, while the units are too few to fill
+// the device (eight an SM), down to one head a group.
+void fill_units(HeadTensor &t, int64_t M, int group_heads, int batch, int64_t want) {
     int per = t.heads;
-    while (per > group_heads && M * ((all_heads + per - 1) / per) < int64_t(SMS) * 8) per = (per + 1) / 2;
+    auto units = [&] { return M * ((t.heads + per - 1) / per); };
+    while (per > group_heads * batch && units() < want) per = (per + 1) / 2;
+    while (per > group_heads && units() < int64_t(SMS) * 8) per = (per + 1) / 2;
     per = std::min(t.heads, (per + group_heads - 1) / group_heads * group_heads);
     t.per_unit = per;
     t.splits = (t.heads + per - 1) / per;
@@ -543,7 +696,6 @@ lora_status_t run(int dtype, const lora_heads_t *const in[2], const lora_heads_t
     a.inv_d = 1.0f / static_cast<float>(D);
     a.partials = want_dw ? static_cast<float *>(ws) : nullptr;
     const int group_heads = 32 >> shape.log_l;
-    const int all = (in[0] ? in[0]->heads : 0) + (in[1] ? in[1]->heads : 0);
     split_ctas(in[0] ? in[0]->heads : 0, in[1] ? in[1]->heads : 0, &a.t[0].ctas, &a.t[1].ctas);
     for (int i = 0; i < 2; ++i) {
         if (!in[i]) continue;
@@ -561,7 +713,10 @@ lora_status_t run(int dtype, const lora_heads_t *const in[2], const lora_heads_t
         }
         t.weight = weight[i];
         t.heads = in[i]->heads;
-        fill_units(t, M, group_heads, all);
+        // backward: eight units or more for each of the tensor's resident warps, so that the last
+        // round, which not all of them have, is a small part
+        if (bwd) fill_units(t, M, group_heads, bwd_heads(shape.V), int64_t(t.ctas) * WARPS * 8);
+        else fill_units(t, M, group_heads, FWD_HEADS, int64_t(SMS) * 8);
         t.ctas = static_cast<int>(std::min<int64_t>(t.ctas, (t.units + WARPS - 1) / WARPS));
     }
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
