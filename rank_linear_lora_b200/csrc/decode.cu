@@ -3,403 +3,781 @@
 //   acc[n, m] = sum_k W[n, k] x[m, k] + sum_j B[n, j] (s.xa)[m, j],   then the epilogue
 //
 // Bound by reading W once.  A 256 x 256 tensor-core tile per CTA pair would put only
-// d_out / 256 pairs of SMs on that stream, so here a cluster of CTAs takes 16 weight rows (the
-// gate's and the up projection's 16, when gated), its warps split K, and each lane loads the
-// weight straight from memory into the registers of mma.sync m16n8k16: weight rows are the
-// 16-row side, tokens the 8-column side (M <= 8 NT).  A lane's 16-byte load holds 8
-// consecutive k of one row; since both operands may order k in any one way, those are the k of
-// the lane's fragment registers of two products, and x is loaded by the same rule: no shared
-// memory, no shuffles, no layout of W other than its own.
+// d_out / 256 pairs of SMs on that stream, so here one persistent CTA an SM takes groups of 16
+// weight rows (the gate's and the up projection's 16, when gated), every CTA the same number:
 //
-// Codes are widened in registers.  4-bit codes enter the products as the exact integers q - 8,
-// E4M3 codes as their exact values; the scale (one a row, or one a row and 64 k) multiplies
-// the fp32 sums, so no decoded weight is rounded.  Codebook values are rounded once to bf16
-// and looked up two codes at a time in a shared table of a byte's 256 pairs, one copy for
-// each lane's bank.
+//   product warps    a group's rows are cut along K into stages of two 2 KB boxes (128 bytes of
+//                    16 rows: both projections' when gated, else two in a row); the warps take
+//                    the CTA's stages in turn.  Each streams its own by TMA into a private ring
+//                    in shared memory, several ahead and on into the next groups, and at a
+//                    group's end leaves its sums in one of two buffers.
+//   finishing warps  finish a group while the others go on: the warps' sums in a fixed order,
+//                    the low-rank term (products on B's rows and s.xa), the epilogue.
 //
-// The sums of the CTA's warps, then of the cluster's CTAs, are added in a fixed order; the
-// low-rank term is one warp's extra products on the rows of B.  s.xa comes from the same
-// kernel run on A's rows just before; this kernel starts its stream of W beside it and waits
-// for it only before the low-rank term (programmatic dependent launch: the s.xa kernel lets
-// it start only once all its own CTAs have seen their predecessor complete, so x is final).
+// The products run on mma.sync m16n8k16: weight rows are its 16-row side, tokens its 8-column
+// side (M <= 8 NT).  tcgen05 would want its weight operand decoded back into shared memory;
+// here a tile goes from shared memory into fragment registers once, and at a few tokens the
+// tensor pipe has nothing to do either way.  Both operands may order k in any one way, so a
+// lane's fragment registers are 8 or 16 consecutive weights of one row, and x is laid out to
+// match, in shared memory where it fits there.  TMA's 128-byte swizzle and the order in which
+// fragment rows take tile rows keep those reads free of bank conflicts.
+//
+// Codes are widened in registers, and no decoded weight is rounded.  A 4-bit code under the
+// exponent of 128 is 128 + q; the products take that, and 136 times the block's sum of x
+// comes off afterwards, since the code stands for q - 8.  E4M3
+// codes enter with their exact values.  The scale (one a row, or one a row and 64 k, fetched
+// a tile ahead) multiplies the fp32 sums.  Codebook values are rounded once to bf16 and looked
+// up two codes at a time in a table of a byte's 256 pairs, a copy in every bank.
+//
+// s.xa comes from k_decode_xa just before; this kernel starts its stream beside it and waits
+// for it only before the low-rank term (programmatic dependent launch: that kernel lets this
+// one start only once all its own CTAs have seen their predecessor complete, so x is final).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "act.cuh"
 #include "decode.h"
 #include "ptx.cuh"
+#include "tc_gemm.cuh"
+#include "tmap.h"
 
 namespace {
 
 using namespace lora;
 using lora_host::DecodeArgs;
 
-constexpr int WARPS = 8;
-constexpr int ROWS = 16;  // weight rows per m-tile
-enum DecodeOp { D_XA = 0, D_ACT = 1, D_GLU = 2 };
+constexpr int ROWS = 16;        // weight rows per m-tile
+constexpr int TILE_BYTES = 128;  // of a row per tile
+constexpr int BOX = ROWS * TILE_BYTES;
+constexpr int TILE = 128;       // values of an m-tile x n-tile
+constexpr int FIN_WARPS = 4;     // finishing warps: a thread for each value of an n-tile
+constexpr int STAGE = 2 * BOX;
+enum DecodeOp { D_ACT = 1, D_GLU = 2 };
 enum DecodeFmt { F_BF16 = LORA_W_BF16, F_Q4 = LORA_W_Q4, F_FP8 = LORA_W_FP8, F_CB = LORA_W_NF4 };
+
+template <int FMT, int OP, int NT>
+struct Cfg {
+    static constexpr bool NIBBLE = FMT == F_Q4 || FMT == F_CB;
+    static constexpr int MT = OP == D_GLU ? 2 : 1;
+    // Widening 4-bit codes is bound by instructions, not by memory: more warps, and the ring they
+    // leave room for (8192 -> 2 x 28672, four tokens: 66 us; 8 warps x 4 stages 78, 16 x 2, which
+    // spill, 94).  The other formats stream at 8 x 4 (4096 -> 2 x 11008 in bf16, one token: 30 us).
+    static constexpr int WARPS = NIBBLE ? 12 : 8;
+    static constexpr int STAGES = NIBBLE ? 2 : 4;
+    static constexpr int THREADS = (WARPS + FIN_WARPS) * 32;
+    static constexpr int BOX_K = FMT == F_BF16 ? 64 : FMT == F_FP8 ? 128 : 256;  // k of a box
+    static constexpr int STAGE_K = MT == 2 ? BOX_K : 2 * BOX_K;
+    static constexpr int BLOCKS = STAGE_K / 64;                // 64-wide blocks of k
+    static constexpr int BOX_BLOCKS = BOX_K / 64;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int OUT = MT * NT * TILE;                 // fp32 sums of a group
+    static constexpr int RED = 2 * WARPS * OUT * 4;
+    static constexpr int TABLE = FMT == F_CB ? 256 * 32 * 4 : 0;
+    static constexpr int BARS = (WARPS * STAGES + 4) * 8;
+    static constexpr int FIXED = 1024 + RING + RED + OUT * 4 + TABLE + BARS + 16 + 128;
+    static constexpr int X_MAX = (232448 - FIXED) / 64 * 64;   // room for x
+};
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Weights are read once: past L1, and 256 bytes at a time into L2.
-__device__ __forceinline__ uint4 ld_stream16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 ld_stream8(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+// The same from C = 0.
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
 }
+// Shared-memory loads by 32-bit address, in program order with the waits and the copies.
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ uint16_t f32_bf16(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// One row's 64-wide step as loaded by a lane (16 weights), and its scale.
-template <int FMT>
-struct RowLoad {
-    uint4 v[FMT == F_BF16 ? 2 : 1];
-    uint16_t sc;
-};
-
-// Lane's weights of one row in a 64-wide step: bf16, k0 + 8 j and k0 + 32 + 8 j (8 each);
-// codes, the 16 from k0 + 16 j.  Nothing is read at or behind K.
-template <int FMT>
-__device__ __forceinline__ void load_row(RowLoad<FMT> &r, const DecodeArgs &a, int64_t row, int k0, int j) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    if constexpr (FMT == F_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(a.w) + row * a.K + k0 + 8 * j;
-        r.v[0] = k0 + 8 * j < a.K ? ld_stream16(p) : zero;
-        r.v[1] = k0 + 32 + 8 * j < a.K ? ld_stream16(p + 32) : zero;
-    } else if constexpr (FMT == F_FP8) {
-        r.v[0] = k0 + 16 * j < a.K ? ld_stream16(static_cast<const uint8_t *>(a.w) + row * a.K + k0 + 16 * j) : zero;
-    } else {  // K % 64 == 0
-        const uint2 q = ld_stream8(static_cast<const uint8_t *>(a.w) + row * (a.K / 2) + k0 / 2 + 8 * j);
-        r.v[0] = make_uint4(q.x, q.y, 0, 0);
-        r.sc = __ldg(a.wscale + row * (a.K / 64) + k0 / 64);
-    }
+// Tile row (0..7) of fragment row g: 8 lanes (16-byte reads) or 16 (8-byte reads) that are
+// served together then read all 32 banks of the swizzled rows.
+template <bool NIBBLE>
+__device__ __forceinline__ int tile_row(int g) {
+    return NIBBLE ? ((g & 3) << 1) | (g >> 2) : (g >> 1) | ((g & 1) << 2);
 }
 
-// The lane's 16 weights as 8 bf16 pairs, in the order of the x pairs that load_x gives.
-template <int FMT>
-__device__ __forceinline__ void decode_row(const RowLoad<FMT> &r, const uint32_t *table, int lane, uint32_t (&w)[8]) {
-    if constexpr (FMT == F_BF16) {
-        w[0] = r.v[0].x, w[1] = r.v[0].y, w[2] = r.v[0].z, w[3] = r.v[0].w;
-        w[4] = r.v[1].x, w[5] = r.v[1].y, w[6] = r.v[1].z, w[7] = r.v[1].w;
-    } else if constexpr (FMT == F_FP8) {
-        const uint32_t q[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm("{\n\t.reg .b16 c0, c1, a0, a1, a2, a3;\n\t.reg .b32 h0, h1;\n\t.reg .f32 f0, f1, f2, f3;\n\t"
-                "mov.b32 {c0, c1}, %2;\n\t"
-                "cvt.rn.f16x2.e4m3x2 h0, c0;\n\t"
-                "cvt.rn.f16x2.e4m3x2 h1, c1;\n\t"
-                "mov.b32 {a0, a1}, h0;\n\t"
-                "mov.b32 {a2, a3}, h1;\n\t"
-                "cvt.f32.f16 f0, a0;\n\tcvt.f32.f16 f1, a1;\n\tcvt.f32.f16 f2, a2;\n\tcvt.f32.f16 f3, a3;\n\t"
-                "cvt.rn.bf16x2.f32 %0, f1, f0;\n\t"
-                "cvt.rn.bf16x2.f32 %1, f3, f2;\n\t}"
-                : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
-                : "r"(q[i]));
-    } else if constexpr (FMT == F_Q4) {
-        // pairs (e, e + 4) of each word's 8 codes: a nibble under the exponent of 128 is
-        // 128 + q, less 136 it is q - 8, both exact
-        const uint32_t q[2] = {r.v[0].x, r.v[0].y};
-        const __nv_bfloat162 off = __floats2bfloat162_rn(136.0f, 136.0f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t u = ((q[i] >> (4 * e)) & 0x000F000Fu) | 0x43004300u;
-                const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&u), off);
-                w[4 * i + e] = *reinterpret_cast<const uint32_t *>(&d);
-            }
-    } else {
-        const uint32_t q[2] = {r.v[0].x, r.v[0].y};
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) w[4 * i + b] = table[((q[i] >> (8 * b)) & 0xFFu) * 32 + lane];
-    }
+// Four E4M3 codes to two pairs of bf16, exactly.
+__device__ __forceinline__ void widen_fp8(uint32_t q, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 c0, c1, a0, a1, a2, a3;\n\t.reg .b32 h0, h1;\n\t.reg .f32 f0, f1, f2, f3;\n\t"
+        "mov.b32 {c0, c1}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h0, c0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h1, c1;\n\t"
+        "mov.b32 {a0, a1}, h0;\n\t"
+        "mov.b32 {a2, a3}, h1;\n\t"
+        "cvt.f32.f16 f0, a0;\n\tcvt.f32.f16 f1, a1;\n\tcvt.f32.f16 f2, a2;\n\tcvt.f32.f16 f3, a3;\n\t"
+        "cvt.rn.bf16x2.f32 %0, f1, f0;\n\t"
+        "cvt.rn.bf16x2.f32 %1, f3, f2;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(q));
+}
+// 128 + q of the codes (e, e + 4) of a word's 8 is and_or(word >> 4 e, 0x000F000F, 0x43004300), a
+// pair of bf16.  The masks come in registers: one LOP3 then ands and ors (immediates take two).
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+    return d;
+}
+// The table's pair of a byte of codes.
+__device__ __forceinline__ uint32_t cb_pair(uint32_t table_lane, uint32_t v, int byte) {
+    uint32_t w;
+    asm("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(table_lane + ((v >> (8 * byte)) & 0xFFu) * 128u));
+    return w;
 }
 
-// The x pairs of token n that belong to the lane's weights of a step (zero behind M and K).
-template <int FMT>
-__device__ __forceinline__ void load_x(uint32_t (&v)[8], const DecodeArgs &a, int n, int k0, int j) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const int ka = FMT == F_BF16 ? k0 + 8 * j : k0 + 16 * j, kb = FMT == F_BF16 ? ka + 32 : ka + 8;
-    const uint16_t *p = a.x + static_cast<int64_t>(n) * a.K;
-    const uint4 u = n < a.M && ka < a.K ? __ldcg(reinterpret_cast<const uint4 *>(p + ka)) : zero;
-    const uint4 w = n < a.M && kb < a.K ? __ldcg(reinterpret_cast<const uint4 *>(p + kb)) : zero;
-    if constexpr (FMT == F_Q4) {
-        v[0] = prmt(u.x, u.z, 0x5410), v[1] = prmt(u.x, u.z, 0x7632);
-        v[2] = prmt(u.y, u.w, 0x5410), v[3] = prmt(u.y, u.w, 0x7632);
-        v[4] = prmt(w.x, w.z, 0x5410), v[5] = prmt(w.x, w.z, 0x7632);
-        v[6] = prmt(w.y, w.w, 0x5410), v[7] = prmt(w.y, w.w, 0x7632);
-    } else {
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-        v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
-    }
+// Barrier of the finishing warps; true where any of their threads brings true.
+__device__ __forceinline__ bool fin_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(v)), "n"(FIN_WARPS * 32) : "memory");
+    return r != 0;
 }
 
-template <int FMT, int OP, int NT>
-__global__ void __launch_bounds__(WARPS * 32) k_decode(const __grid_constant__ DecodeArgs a) {
-    constexpr int MT = OP == D_GLU ? 2 : 1;
-    constexpr int TILE = 128;                 // values of an m-tile x n-tile
-    constexpr int PER_STEP = MT == 2 ? 1 : 2;  // steps in flight together
-    extern __shared__ uint32_t table[];        // F_CB: [256][32]
-    __shared__ float red[WARPS][MT * NT * TILE];
-    __shared__ float sums[MT * NT * TILE];
+// XS: x is in shared memory (else its fragments come from memory stage by stage).
+template <int FMT, int OP, int NT, bool XS>
+__global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const __grid_constant__ DecodeArgs a) {
+    using C_ = Cfg<FMT, OP, NT>;
+    constexpr int MT = C_::MT, WARPS = C_::WARPS, STAGES = C_::STAGES, OUT = C_::OUT, BLOCKS = C_::BLOCKS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *red = reinterpret_cast<float *>(smem + C_::RING);  // [2][WARPS][OUT]
+    float *tail = red + 2 * WARPS * OUT;                      // [OUT] the low-rank term
+    uint32_t *table = reinterpret_cast<uint32_t *>(tail + OUT);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(table) + C_::TABLE);  // [WARPS][STAGES]
+    uint64_t *red_full = bars + WARPS * STAGES, *red_empty = red_full + 2;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(red_empty + 2);
+    uint8_t *zero = reinterpret_cast<uint8_t *>(red_empty + 2) + 16;  // 128 bytes: a block of a token behind M
+    uint8_t *xs = zero + 128;                                         // x, rows x_stride bytes
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, j = lane & 3;
-    const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int row0 = static_cast<int>(blockIdx.x) / C * ROWS;
-    if (OP == D_XA) grid_dep_wait();
+    const int S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;      // stages of a group
+    const int groups = (a.N + ROWS - 1) / ROWS;
+    const int u0 = blockIdx.x, u_step = gridDim.x;
+    const int row_in = tile_row<C_::NIBBLE>(g);  // tile rows of the lane: row_in, row_in + 8
+
+    if (warp < WARPS && lane == 0)
+        for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[warp * STAGES + s]), 1);
+    if (threadIdx.x == WARPS * 32) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&red_full[b]), WARPS);
+            mbar_init(smem_u32(&red_empty[b]), FIN_WARPS);
+        }
+        *abort_flag = 0;
+    }
+    fence_mbar_init();
+    __syncwarp();
     grid_dep_launch_dependents();
+
+    // x: 64-wide blocks laid out as the fragments take them, zero behind K.  Its loads go out
+    // before the stream's, which would hold them up by the whole ring.
+    const int x_cols = S * C_::STAGE_K, x_stride = x_cols * 2 + 64;  // 64 bytes apart mod 128: no two tokens' reads share a bank
+    const int x_chunks = XS ? a.M * (x_cols / 8) : 0;
+    constexpr int X_AHEAD = 8;
+    uint4 xv[X_AHEAD];
+    auto x_load = [&](int c) {
+        const int m = c / (x_cols / 8), k = (c - m * (x_cols / 8)) * 8;
+        return k < a.K ? __ldcg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * a.K + k)) : make_uint4(0, 0, 0, 0);
+    };
+    auto x_store = [&](int c, uint4 v) {
+        const int m = c / (x_cols / 8), k = (c - m * (x_cols / 8)) * 8;
+        int at = k;
+        if (FMT != F_BF16) at = (k & ~63) + ((k >> 3) & 1) * 32 + ((k >> 4) & 3) * 8;  // 16 in a row per lane
+        if (FMT == F_Q4)
+            v = make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+        *reinterpret_cast<uint4 *>(xs + m * x_stride + at * 2) = v;
+    };
+#pragma unroll
+    for (int i = 0; i < X_AHEAD; ++i)
+        if (static_cast<int>(threadIdx.x) + i * C_::THREADS < x_chunks) xv[i] = x_load(threadIdx.x + i * C_::THREADS);
+
+    // Requests of a product warp, whose stages are the CTA's warp, warp + WARPS, ...: the cursor
+    // (group req_u, stage req_s of it) runs STAGES ahead of the stage in use.
+    uint8_t *ring = smem + warp * (STAGES * STAGE);  // (product warps only)
+    int req_u = u0 + warp / S * u_step, req_s = warp % S, requested = 0;
+    auto advance = [&]() {
+        if (req_u >= groups) return;
+        if (lane == 0) {
+            const int s = requested & (STAGES - 1);
+            const uint32_t bar = smem_u32(&bars[warp * STAGES + s]), dst = smem_u32(ring + s * STAGE);
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(STAGE));
+            const int byte = req_s * (MT == 2 ? 1 : 2) * TILE_BYTES, row = req_u * ROWS;
+            tma_load_2d(dst, &a.tmW, bar, byte, row);
+            tma_load_2d(dst + BOX, &a.tmW, bar, MT == 2 ? byte : byte + TILE_BYTES, MT == 2 ? a.N + row : row);
+        }
+        ++requested;
+        req_s += WARPS;
+        while (req_s >= S) {
+            req_s -= S;
+            req_u += u_step;
+        }
+    };
+    static_assert((STAGES & (STAGES - 1)) == 0, "stages are counted by masks");
+    if (warp < WARPS)
+        for (int s = 0; s < STAGES; ++s) advance();
+
+#pragma unroll
+    for (int i = 0; i < X_AHEAD; ++i)
+        if (static_cast<int>(threadIdx.x) + i * C_::THREADS < x_chunks) x_store(threadIdx.x + i * C_::THREADS, xv[i]);
+    for (int c = threadIdx.x + X_AHEAD * C_::THREADS; c < x_chunks; c += C_::THREADS) x_store(c, x_load(c));
+    if (threadIdx.x < 32) reinterpret_cast<uint32_t *>(zero)[threadIdx.x] = 0;
+    // 4-bit codes: -136 times each block's sum of x, [block][token] (zero behind M)
+    float *xsum = reinterpret_cast<float *>(xs + (XS ? a.M * x_stride : 0));
+    if constexpr (XS && FMT == F_Q4) {
+        __syncthreads();
+        const int nb = x_cols / 64;
+        for (int c = threadIdx.x; c < nb * 8 * NT; c += C_::THREADS) {
+            const int b = c / (8 * NT), m = c % (8 * NT);
+            float v = 0.0f;
+            if (m < a.M) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(xs + m * x_stride + b * 128);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 q = p[i];
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
+                }
+            }
+            xsum[c] = -136.0f * v;
+        }
+    }
     if constexpr (FMT == F_CB) {
-        for (int i = threadIdx.x; i < 256 * 32; i += WARPS * 32) {
-            const int b = i >> 5;
-            const __nv_bfloat162 v = __floats2bfloat162_rn(a.cb[b & 15], a.cb[b >> 4]);
+        for (int i = threadIdx.x; i < 256 * 32; i += C_::THREADS) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a.cb[(i >> 5) & 15], a.cb[i >> 9]);
             table[i] = *reinterpret_cast<const uint32_t *>(&v);
         }
-        __syncthreads();
     }
-    // the lane's rows (those behind the output repeat the last one and are not stored)
-    int64_t row[MT][2];
+    __syncthreads();
+
+    if (warp < WARPS) {
+        // ------------------------------------------------------------------ products
+        const uint32_t table_lane = smem_u32(table) + lane * 4;
+        const uint32_t ring0 = smem_u32(ring) + row_in * TILE_BYTES;
+        uint32_t q4_mask = 0x000F000Fu, q4_bits = 0x43004300u;  // kept in registers
+        asm volatile("" : "+r"(q4_mask), "+r"(q4_bits));
+        uint32_t chunk[4];  // byte of the lane's weights of block b of a box in its (swizzled) row
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int b = 0; b < 4; ++b)
+            chunk[b] = C_::NIBBLE ? (((2 * b + (j >> 1)) ^ row_in) << 4) + (j & 1) * 8 : ((4 * (b & 1) + j) ^ row_in) << 4;
+        // the fragments of a 64-wide block of x, token n*8 + g; tokens behind M read zeros
+        const uint32_t xsum0 = smem_u32(xsum) + j * 8;
+        uint32_t xp[NT], x_step[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) row[m][h] = static_cast<int64_t>(m) * a.N + min(row0 + g + 8 * h, a.N - 1);
-    float acc[MT][NT][4] = {};
-    const int steps = (a.K + 63) / 64;
-    const int s_lo = steps * rank / C, s_hi = steps * (rank + 1) / C;
-    for (int s = s_lo + warp; s < s_hi; s += WARPS * PER_STEP) {
-        RowLoad<FMT> ld[PER_STEP][MT][2];
-        uint32_t xv[PER_STEP][NT][8];
-#pragma unroll
-        for (int u = 0; u < PER_STEP; ++u) {
-            const int k0 = (s + u * WARPS) * 64;
-            if (u > 0 && s + u * WARPS >= s_hi) break;
+        for (int n = 0; n < NT; ++n) {
+            const bool in = n * 8 + g < a.M;
+            xp[n] = smem_u32(in ? xs + (n * 8 + g) * x_stride : zero) + j * 16;
+            x_step[n] = in ? 128u : 0u;
+        }
+        auto load_x = [&](int n, int block, uint32_t (&v)[8]) {
+            uint4 u, w;
+            if constexpr (XS) {
+                const uint32_t p = xp[n] + block * x_step[n];
+                u = lds16(p);
+                w = lds16(p + 64);
+            } else {
+                u = w = make_uint4(0, 0, 0, 0);
+                const int ka = block * 64 + (FMT == F_BF16 ? 8 * j : 16 * j), kb = ka + (FMT == F_BF16 ? 32 : 8);
+                const uint16_t *p = a.x + static_cast<int64_t>(n * 8 + g) * a.K;
+                if (n * 8 + g < a.M) {
+                    if (ka < a.K) u = __ldcg(reinterpret_cast<const uint4 *>(p + ka));
+                    if (kb < a.K) w = __ldcg(reinterpret_cast<const uint4 *>(p + kb));
+                }
+                __syncwarp();
+                if (FMT == F_Q4) {
+                    u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
+                    w = make_uint4(prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632), prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
+                }
+            }
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w, v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
+        };
+        // 4-bit scales of a stage, as loaded: 4 blocks of k of each of the lane's rows of a box.  The
+        // rows' pointers are the group's.
+        const int n_kb = a.K / 64;
+        const uint16_t *sc_row[MT][2];
+        auto scale_rows = [&](int u) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) load_row<FMT>(ld[u][m][h], a, row[m][h], k0, j);
+                for (int h = 0; h < 2; ++h)
+                    sc_row[m][h] = a.wscale + static_cast<int64_t>(min(u * ROWS + row_in + 8 * h, a.N - 1) + m * a.N) * n_kb;
+        };
+        const bool sc_aligned = n_kb % 4 == 0;  // four scales are 8 aligned bytes
+        auto load_scales = [&](int s, uint2 (&sc)[2][2]) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) load_x<FMT>(xv[u][t], a, t * 8 + g, k0, j);
+            for (int x = 0; x < 2; ++x) {  // box
+                const int kb = MT == 2 ? s * 4 : s * 8 + x * 4;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint16_t *p = sc_row[MT == 2 ? x : 0][h] + kb;
+                    if (sc_aligned) {
+                        sc[x][h] = kb < n_kb ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
+                    } else {
+                        uint32_t q[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) q[b] = kb + b < n_kb ? __ldg(p + b) : 0;
+                        sc[x][h] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+                    }
+                }
+            }
+        };
+        bool ok = true;
+        int used = 0, part = 0;
+        int u = u0 + warp / S * u_step, st = warp % S;  // the warp's next stage
+        uint2 sc[2][2], sc_next[2][2];
+        int sc_u = u;  // the group of sc_row
+        if constexpr (C_::NIBBLE)
+            if (u < groups) {
+                scale_rows(u);
+                load_scales(st, sc_next);
+            }
+        for (int gu = u0; gu < groups; gu += u_step, ++part) {
+            float acc[MT][NT][4] = {};
+            float row_scale[MT][2];
+            if constexpr (FMT == F_FP8) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        row_scale[m][h] = bf16_f32(__ldg(a.wscale + m * a.N + min(gu * ROWS + row_in + 8 * h, a.N - 1)));
+            }
+            while (u == gu) {
+                const int slot = used & (STAGES - 1), s = st;
+                st += WARPS;
+                while (st >= S) {
+                    st -= S;
+                    u += u_step;
+                }
+                if constexpr (C_::NIBBLE) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) sc[x][0] = sc_next[x][0], sc[x][1] = sc_next[x][1];
+                    if (u < groups) {
+                        if (u != sc_u) scale_rows(sc_u = u);
+                        load_scales(st, sc_next);
+                    }
+                }
+                uint32_t x[XS ? 1 : 2][NT][8];
+                if constexpr (!XS)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) load_x(n, s * BLOCKS, x[0][n]);
+                if (ok) ok = wait_bounded(smem_u32(&bars[warp * STAGES + slot]), static_cast<uint32_t>(used / STAGES) & 1u,
+                                          abort_flag, a.err, DERR_WAIT_FULL);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t box0 = ring0 + slot * STAGE;
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    if (XS || b + 1 < BLOCKS) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) load_x(n, s * BLOCKS + (XS ? b : b + 1), x[XS ? 0 : (b + 1) & 1][n]);
+                    }
+                    const uint32_t(&xb)[NT][8] = x[XS ? 0 : b & 1];
+                    const int bb = b % C_::BOX_BLOCKS;  // block of its box
+                    // the lane's weights of the block, as loaded: two rows of each m-tile
+                    uint4 q[MT][2][FMT == F_BF16 ? 2 : 1];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t p = box0 + (MT == 2 ? m : b / C_::BOX_BLOCKS) * BOX + h * 1024 + chunk[bb];
+                            if constexpr (C_::NIBBLE) {
+                                const uint2 c = lds8(p);
+                                q[m][h][0] = make_uint4(c.x, c.y, 0, 0);
+                            } else {
+                                q[m][h][0] = lds16(p);
+                                if constexpr (FMT == F_BF16) q[m][h][1] = lds16(box0 + (MT == 2 ? m : b / C_::BOX_BLOCKS) * BOX + h * 1024 + chunk[1]);
+                            }
+                        }
+                    // pairs 2 i, 2 i + 1 of a row: its operand of the i-th product
+                    auto pairs = [&](const uint4 (&c)[FMT == F_BF16 ? 2 : 1], int i, uint32_t &lo, uint32_t &hi) {
+                        if constexpr (FMT == F_BF16) {
+                            const uint4 &v = c[i >> 1];
+                            lo = i & 1 ? v.z : v.x;
+                            hi = i & 1 ? v.w : v.y;
+                        } else if constexpr (FMT == F_FP8) {
+                            widen_fp8(i == 0 ? c[0].x : i == 1 ? c[0].y : i == 2 ? c[0].z : c[0].w, lo, hi);
+                        } else if constexpr (FMT == F_Q4) {
+                            const uint32_t v = i < 2 ? c[0].x : c[0].y;
+                            lo = and_or(v >> (i & 1 ? 8 : 0), q4_mask, q4_bits);
+                            hi = and_or(v >> (i & 1 ? 12 : 4), q4_mask, q4_bits);
+                        } else {
+                            const uint32_t v = i < 2 ? c[0].x : c[0].y;
+                            lo = cb_pair(table_lane, v, (i & 1) * 2);
+                            hi = cb_pair(table_lane, v, (i & 1) * 2 + 1);
+                        }
+                    };
+                    // Widening alternates with the products of the m-tiles, so that a product's latency is spent
+                    // on the next one's operands.
+                    float p4[MT][NT][4], xo[NT][4];  // xo: -136 times the sum of x, of the lane's tokens
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            uint32_t a0, a1, a2, a3;
+                            pairs(q[m][0], i, a0, a2);
+                            pairs(q[m][1], i, a1, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                if constexpr (C_::NIBBLE) {
+                                    if (i == 0) mma_bf16_zero(p4[m][n], a0, a1, a2, a3, xb[n][0], xb[n][1]);
+                                    else mma_bf16(p4[m][n], a0, a1, a2, a3, xb[n][2 * i], xb[n][2 * i + 1]);
+                                } else {
+                                    mma_bf16(acc[m][n], a0, a1, a2, a3, xb[n][2 * i], xb[n][2 * i + 1]);
+                                }
+                            }
+                        }
+                        if constexpr (FMT == F_Q4 && !XS) {  // one more product, with -136 for the weights
+                            constexpr uint32_t off = 0xC308C308u;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                if (i == 0) mma_bf16_zero(xo[n], off, off, off, off, xb[n][0], xb[n][1]);
+                                else mma_bf16(xo[n], off, off, off, off, xb[n][2 * i], xb[n][2 * i + 1]);
+                            }
+                        }
+                    }
+                    if constexpr (FMT == F_Q4 && XS) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 v = lds8(xsum0 + ((s * BLOCKS + b) * 8 * NT + n * 8) * 4);
+                            xo[n][0] = __uint_as_float(v.x), xo[n][1] = __uint_as_float(v.y);
+                        }
+                    }
+                    if constexpr (C_::NIBBLE) {
+                        // the block's sums times the scale of each of the lane's rows; a 4-bit code stands for
+                        // q - 8 = (128 + q) - 136
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int x_ = MT == 2 ? m : b / C_::BOX_BLOCKS;
+                            const uint32_t q0 = bb < 2 ? sc[x_][0].x : sc[x_][0].y, q1 = bb < 2 ? sc[x_][1].x : sc[x_][1].y;
+                            const float s0 = __uint_as_float(bb & 1 ? q0 & 0xFFFF0000u : q0 << 16);
+                            const float s1 = __uint_as_float(bb & 1 ? q1 & 0xFFFF0000u : q1 << 16);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float v = FMT == F_Q4 ? p4[m][n][e] + xo[n][e & 1] : p4[m][n][e];
+                                    acc[m][n][e] = fmaf(e < 2 ? s0 : s1, v, acc[m][n][e]);
+                                }
+                        }
+                    }
+                }
+                __syncwarp();  // every lane has read the stage
+                ++used;
+                advance();
+            }
+            // the group's sums of this warp, once the buffer's last group is finished
+            const int buf = part & 1;
+            if (ok) ok = wait_bounded(smem_u32(&red_empty[buf]), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, abort_flag,
+                                      a.err, DERR_WAIT_TMEM_EMPTY);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = acc[m][n][e];
+                        if constexpr (FMT == F_FP8) v[e] *= row_scale[m][e >> 1];
+                        if constexpr (FMT == F_Q4) v[e] *= 1.0f / 7.0f;
+                    }
+                    *reinterpret_cast<float4 *>(&red[(buf * WARPS + warp) * OUT + (m * NT + n) * TILE + lane * 4]) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&red_full[buf]));
         }
+        // After a wait that ran out: copies still in flight land before the CTA leaves.
+        if (!ok && lane == 0)
+            for (int q = used; q < requested; ++q) {
+                volatile int never = 0;
+                wait_bounded(smem_u32(&bars[warp * STAGES + (q & (STAGES - 1))]), static_cast<uint32_t>(q / STAGES) & 1u, &never,
+                             a.err, DERR_WAIT_DRAIN);
+            }
+        return;
+    }
+
+    // ---------------------------------------------------------------------- finish
+    const int fw = warp - WARPS, o = threadIdx.x - WARPS * 32;  // a thread: value o of each n-tile
+    const int l = o >> 2, oi = o & 3;
+    grid_dep_wait();  // s.xa is there, and no earlier kernel still reads what is stored here
+    // s.xa and the fragments of B run through the same products; warp fw takes tile fw of MT x NT
+    auto low_rank = [&](int u) {
+        if (fw < MT * NT) {
+            const int m = fw / NT, n = fw % NT;
+            const int64_t r0 = static_cast<int64_t>(m) * a.N + min(u * ROWS + row_in, a.N - 1);
+            const int64_t r1 = static_cast<int64_t>(m) * a.N + min(u * ROWS + row_in + 8, a.N - 1);
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            float c[4] = {};
+#pragma unroll 2
+            for (int k = 8 * j; k < (a.r + 31) / 32 * 32; k += 32) {
+                const bool in = k < a.r;
+                const uint4 b0 = in ? __ldcg(reinterpret_cast<const uint4 *>(a.B + r0 * a.r + k)) : zero;
+                const uint4 b1 = in ? __ldcg(reinterpret_cast<const uint4 *>(a.B + r1 * a.r + k)) : zero;
+                const uint4 v = in && n * 8 + g < a.M
+                                    ? __ldcg(reinterpret_cast<const uint4 *>(a.xa + static_cast<int64_t>(n * 8 + g) * a.r + k)) : zero;
+                __syncwarp();
+                mma_bf16(c, b0.x, b1.x, b0.y, b1.y, v.x, v.y);
+                mma_bf16(c, b0.z, b1.z, b0.w, b1.w, v.z, v.w);
+            }
+            *reinterpret_cast<float4 *>(&tail[fw * TILE + lane * 4]) = make_float4(c[0], c[1], c[2], c[3]);
+        }
+    };
+    auto epilogue = [&](int u, int n, const float (&v)[MT]) {
+        const int col = u * ROWS + tile_row<C_::NIBBLE>(l >> 2) + 8 * (oi >> 1);
+        const int token = n * 8 + 2 * (l & 3) + (oi & 1);
+        if (col >= a.N || token >= a.M) return;
+        const int64_t at = static_cast<int64_t>(token) * a.N + col;
+        if constexpr (OP == D_GLU) {
+            if (a.save) {
+                const int64_t s = static_cast<int64_t>(token) * 2 * a.N + col;
+                a.save[s] = f32_bf16(v[0]);
+                a.save[s + a.N] = f32_bf16(v[1]);
+            }
+            float y = 0.0f;
+            act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(v[0]); });
+            a.out[at] = f32_bf16(y * v[1]);
+        } else {
+            float y = v[0];
+            if (a.bias) y += bf16_f32(__ldcg(a.bias + col));
+            if (a.save) a.save[at] = f32_bf16(y);
+            act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(y); });
+            if (a.residual) y += bf16_f32(__ldcg(a.residual + at));
+            a.out[at] = f32_bf16(y);
+        }
+    };
+    int part = 0;
+    for (int u = u0; u < groups; u += u_step, ++part) {
+        const int buf = part & 1;
+        low_rank(u);
+        // the low-rank term of all four warps is there, and all four agree on how the wait ended
+        if (fin_any(!wait_bounded(smem_u32(&red_full[buf]), static_cast<uint32_t>(part >> 1) & 1u, abort_flag, a.err,
+                                  DERR_WAIT_TMEM_FULL)))
+            break;
+        float v[NT][MT];
 #pragma unroll
-        for (int u = 0; u < PER_STEP; ++u) {
-            if (u > 0 && s + u * WARPS >= s_hi) break;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                uint32_t w0[8], w1[8];
-                decode_row<FMT>(ld[u][m][0], table, lane, w0);
-                decode_row<FMT>(ld[u][m][1], table, lane, w1);
-                if constexpr (FMT == F_Q4 || FMT == F_CB) {
-                    // the step is one scale block: its sums times the scale
-                    const float f = FMT == F_Q4 ? 1.0f / 7.0f : 1.0f;
-                    const float s0 = __uint_as_float(static_cast<uint32_t>(ld[u][m][0].sc) << 16) * f;
-                    const float s1 = __uint_as_float(static_cast<uint32_t>(ld[u][m][1].sc) << 16) * f;
+                v[n][m] = 0.0f;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        float part[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16(part, w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1], xv[u][t][2 * i],
-                                     xv[u][t][2 * i + 1]);
-                        acc[m][t][0] += s0 * part[0];
-                        acc[m][t][1] += s0 * part[1];
-                        acc[m][t][2] += s1 * part[2];
-                        acc[m][t][3] += s1 * part[3];
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16(acc[m][t], w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1], xv[u][t][2 * i],
-                                     xv[u][t][2 * i + 1]);
-                }
+                for (int w = 0; w < WARPS; ++w) v[n][m] += red[(buf * WARPS + w) * OUT + (m * NT + n) * TILE + o];
+                v[n][m] += tail[(m * NT + n) * TILE + o];
             }
+        named_bar_sync(1, FIN_WARPS * 32);  // read by all before the next group's low-rank term
+        if (lane == 0) mbar_arrive(smem_u32(&red_empty[buf]));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) epilogue(u, n, v[n]);
+    }
+}
+
+// ------------------------------------------------------------------ s.xa = bf16(s . x.A^T)
+// The same products on A's rows, few and short: no ring, each lane loads its weights straight
+// from memory, the CTAs of a cluster split K.
+constexpr int XA_WARPS = 8;
+
+template <int NT>
+__global__ void __launch_bounds__(XA_WARPS * 32) k_decode_xa(const uint16_t *x, const uint16_t *A, uint16_t *xa, int M,
+                                                             int K, int r, float scale, int C) {
+    __shared__ float red[XA_WARPS][NT * TILE];
+    __shared__ float sums[NT * TILE];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, j = lane & 3;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int row0 = static_cast<int>(blockIdx.x) / C * ROWS;
+    grid_dep_wait();
+    grid_dep_launch_dependents();  // only now: k_decode reads x without waiting for this kernel
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto at = [&](const uint16_t *p, int64_t row, int k) {
+        return k < K ? __ldcg(reinterpret_cast<const uint4 *>(p + row * K + k)) : zero;
+    };
+    const int64_t a0 = min(row0 + g, r - 1), a1 = min(row0 + g + 8, r - 1);  // rows behind r are not stored
+    float acc[NT][4] = {};
+    const int steps = (K + 31) / 32;
+    const int s_lo = steps * rank / C, s_hi = steps * (rank + 1) / C;
+#pragma unroll 2
+    for (int s = s_lo + warp; s < s_hi; s += XA_WARPS) {
+        const int k = s * 32 + 8 * j;
+        const uint4 w0 = at(A, a0, k), w1 = at(A, a1, k);
+        uint4 v[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) v[t] = t * 8 + g < M ? at(x, t * 8 + g, k) : zero;
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            mma_bf16(acc[t], w0.x, w1.x, w0.y, w1.y, v[t].x, v[t].y);
+            mma_bf16(acc[t], w0.z, w1.z, w0.w, w1.w, v[t].z, v[t].w);
         }
     }
-    if constexpr (FMT == F_FP8) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float s0 = __uint_as_float(static_cast<uint32_t>(__ldg(a.wscale + row[m][0])) << 16);
-            const float s1 = __uint_as_float(static_cast<uint32_t>(__ldg(a.wscale + row[m][1])) << 16);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                acc[m][t][0] *= s0;
-                acc[m][t][1] *= s0;
-                acc[m][t][2] *= s1;
-                acc[m][t][3] *= s1;
-            }
-        }
-    }
-    if (OP != D_XA && rank == 0) {
-        // every thread of the storing CTA waits: what it stores may still be read by an earlier
-        // kernel, and s.xa is the predecessor's
-        grid_dep_wait();
-        if (warp == WARPS - 1)
-            for (int k0 = 0; k0 < a.r; k0 += 32) {
-                const bool in = k0 + 8 * j < a.r;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                uint4 xa[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    xa[t] = in && t * 8 + g < a.M
-                                ? __ldcg(reinterpret_cast<const uint4 *>(a.xa + static_cast<int64_t>(t * 8 + g) * a.r + k0 + 8 * j))
-                                : zero;
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint4 b0 = in ? __ldcg(reinterpret_cast<const uint4 *>(a.B + row[m][0] * a.r + k0 + 8 * j)) : zero;
-                    const uint4 b1 = in ? __ldcg(reinterpret_cast<const uint4 *>(a.B + row[m][1] * a.r + k0 + 8 * j)) : zero;
-                    __syncwarp();
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma_bf16(acc[m][t], b0.x, b1.x, b0.y, b1.y, xa[t].x, xa[t].y);
-                        mma_bf16(acc[m][t], b0.z, b1.z, b0.w, b1.w, xa[t].z, xa[t].w);
-                    }
-                }
-            }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            *reinterpret_cast<float4 *>(&red[warp][(m * NT + t) * TILE + lane * 4]) =
-                make_float4(acc[m][t][0], acc[m][t][1], acc[m][t][2], acc[m][t][3]);
+    for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<float4 *>(&red[warp][t * TILE + lane * 4]) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    for (int o = threadIdx.x; o < MT * NT * TILE; o += WARPS * 32) {
+    for (int o = threadIdx.x; o < NT * TILE; o += XA_WARPS * 32) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v += red[w][o];
+        for (int w = 0; w < XA_WARPS; ++w) v += red[w][o];
         sums[o] = v;
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
-    if (rank == 0) {
-        for (int o = threadIdx.x; o < NT * TILE; o += WARPS * 32) {
-            float v[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int at = m * NT * TILE + o;
-                v[m] = sums[at];
-                for (int c = 1; c < C; ++c) {
-                    float f;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(f)
-                                 : "r"(mapa_shared(smem_u32(&sums[at]), static_cast<uint32_t>(c))));
-                    v[m] += f;
-                }
+    if (rank == 0)
+        for (int o = threadIdx.x; o < NT * TILE; o += XA_WARPS * 32) {
+            float v = sums[o];
+            for (int c = 1; c < C; ++c) {
+                float f;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(f) : "r"(mapa_shared(smem_u32(&sums[o]), static_cast<uint32_t>(c))) : "memory");
+                v += f;
             }
             const int l = (o & (TILE - 1)) >> 2, i = o & 3;
             const int n = row0 + (l >> 2) + 8 * (i >> 1), token = o / TILE * 8 + 2 * (l & 3) + (i & 1);
-            if (n >= a.N || token >= a.M) continue;
-            const int64_t at = static_cast<int64_t>(token) * a.N + n;
-            if constexpr (OP == D_XA) {
-                a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * a.scale));
-            } else if constexpr (OP == D_GLU) {
-                if (a.save) {
-                    const int64_t s = static_cast<int64_t>(token) * 2 * a.N + n;
-                    a.save[s] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-                    a.save[s + a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(v[1]));
-                }
-                float y = 0.0f;
-                act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(v[0]); });
-                a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y * v[1]));
-            } else {
-                float y = v[0];
-                if (a.bias) y += __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + n)) << 16);
-                if (a.save) a.save[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-                act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(y); });
-                if (a.residual) y += __uint_as_float(static_cast<uint32_t>(__ldcg(a.residual + at)) << 16);
-                a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-            }
+            if (n < r && token < M) xa[static_cast<int64_t>(token) * r + n] = f32_bf16(v * scale);
         }
-    }
     if (C > 1) cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
-template <int FMT, int OP, int NT>
-cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
-    auto kern = k_decode<FMT, OP, NT>;
-    constexpr size_t smem = FMT == F_CB ? 256 * 32 * sizeof(uint32_t) : 0;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>((a.N + ROWS - 1) / ROWS * a.cluster));
-    cfg.blockDim = dim3(WARPS * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+// ------------------------------------------------------------------ host
+void launch_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute (&attr)[2], int grid, int threads, size_t smem, int cluster,
+                   cudaStream_t st) {
+    std::memset(cfg, 0, sizeof(*cfg));
+    cfg->gridDim = dim3(static_cast<unsigned>(grid));
+    cfg->blockDim = dim3(static_cast<unsigned>(threads));
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = lora_host::programmatic_launch() ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    cfg->attrs = attr;
+    cfg->numAttrs = lora_host::programmatic_launch() ? 2 : 1;
+}
+
+std::mutex g_mu;
+
+// Raise an instantiation's shared-memory limit, once a device.
+template <int FMT, int OP, int NT, bool XS>
+cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t st) {
+    using C_ = Cfg<FMT, OP, NT>;
+    static bool done[64] = {};  // shared-memory limit raised, once a device
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!done[d]) {
+            e = cudaFuncSetAttribute(k_decode<FMT, OP, NT, XS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C_::FIXED + C_::X_MAX);
+            if (e != cudaSuccess) return e;
+            done[d] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    launch_config(&cfg, attr, grid, C_::THREADS, C_::FIXED + (XS ? static_cast<size_t>(x_bytes) : 0), 1, st);
+    e = cudaLaunchKernelEx(&cfg, k_decode<FMT, OP, NT, XS>, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     lora_host::count_launch();
     return e;
 }
 
+template <int FMT, int OP, int NT>
+cudaError_t launch_x(const DecodeArgs &a, int sms, cudaStream_t st) {
+    using C_ = Cfg<FMT, OP, NT>;
+    // One CTA an SM, each with as many groups as the fullest has to have: fewer SMs than all of
+    // them still draw the whole bandwidth, and none waits for a last one.
+    const int groups = (a.N + ROWS - 1) / ROWS, rounds = (groups + sms - 1) / sms;
+    const int grid = (groups + rounds - 1) / rounds;
+    const int64_t S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;
+    int64_t x_bytes = a.M * (S * C_::STAGE_K * 2 + 64);
+    if (FMT == F_Q4) x_bytes += S * C_::BLOCKS * 8 * NT * 4;  // and its blocks' sums
+    return x_bytes <= C_::X_MAX ? launch<FMT, OP, NT, true>(a, grid, x_bytes, st)
+                                : launch<FMT, OP, NT, false>(a, grid, 0, st);
+}
+
+// The s.xa kernel asks for the shared-memory split that k_decode needs, so that an SM it runs on
+// does not have to empty before a CTA of k_decode can join it; once a device.
+cudaError_t prepare_xa() {
+    static bool done[64] = {};
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[d]) {
+        for (auto kern : {k_decode_xa<1>, k_decode_xa<2>}) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            if (e != cudaSuccess) return e;
+        }
+        done[d] = true;
+    }
+    return cudaSuccess;
+}
+
 template <int FMT, int OP>
-cudaError_t launch_nt(const DecodeArgs &a, cudaStream_t st) {
-    if (a.M <= 8) return launch<FMT, OP, 1>(a, st);
-    return launch<FMT, OP, 2>(a, st);
+cudaError_t launch_nt(const DecodeArgs &a, int sms, cudaStream_t st) {
+    return a.M <= 8 ? launch_x<FMT, OP, 1>(a, sms, st) : launch_x<FMT, OP, 2>(a, sms, st);
 }
 
 template <int OP>
-cudaError_t launch_fmt(int fmt, const DecodeArgs &a, cudaStream_t st) {
+cudaError_t launch_fmt(int fmt, const DecodeArgs &a, int sms, cudaStream_t st) {
     switch (fmt) {
-        case F_Q4: return launch_nt<F_Q4, OP>(a, st);
-        case F_FP8: return launch_nt<F_FP8, OP>(a, st);
-        case F_CB: return launch_nt<F_CB, OP>(a, st);
-        default: return launch_nt<F_BF16, OP>(a, st);
+        case F_Q4: return launch_nt<F_Q4, OP>(a, sms, st);
+        case F_FP8: return launch_nt<F_FP8, OP>(a, sms, st);
+        case F_CB: return launch_nt<F_CB, OP>(a, sms, st);
+        default: return launch_nt<F_BF16, OP>(a, sms, st);
     }
-}
-
-// CTAs that share 16 rows, splitting K: enough for four CTAs an SM, while each warp keeps two
-// steps of 64 (a quarter of that for s.xa, whose whole stream is short: latency counts there).
-int choose_cluster(int64_t units, int K, int sms, int steps_per_warp) {
-    int c = 1;
-    while (c < 8 && units * c < 4 * sms && (K + 63) / 64 >= 2 * c * WARPS * steps_per_warp) c *= 2;
-    return c;
 }
 
 }  // namespace
 
 namespace lora_host {
 
-cudaError_t launch_decode(const uint16_t *A, uint16_t *xa, float s, int format, bool glu, DecodeArgs a, int sms,
-                          cudaStream_t st) {
-    DecodeArgs p = a;
-    p.w = A;
-    p.N = a.r;
-    p.out = xa;
-    p.scale = s;
-    p.cluster = choose_cluster((a.r + ROWS - 1) / ROWS, a.K, sms, 1);
-    cudaError_t e = launch_nt<F_BF16, D_XA>(p, st);
+cudaError_t launch_decode(const uint16_t *A, uint16_t *xa, float s, int format, bool glu, DecodeArgs a, const void *w,
+                          int sms, cudaStream_t st) {
+    const uint64_t rows = static_cast<uint64_t>(a.N) * (glu ? 2 : 1);
+    const uint64_t row_bytes = format == F_BF16 ? uint64_t(a.K) * 2 : format == F_FP8 ? uint64_t(a.K) : uint64_t(a.K) / 2;
+    if (!tmap_2d(&a.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, row_bytes, rows, TILE_BYTES, ROWS, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    // s.xa: clusters of up to 8 CTAs, as long as each warp keeps a 32-wide step
+    int C = 1;
+    while (C < 8 && (a.K + 31) / 32 >= 2 * C * XA_WARPS) C *= 2;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    launch_config(&cfg, attr, (a.r + ROWS - 1) / ROWS * C, XA_WARPS * 32, 0, C, st);
+    cudaError_t e = prepare_xa();
+    if (e != cudaSuccess) return e;
+    e = cudaLaunchKernelEx(&cfg, a.M <= 8 ? k_decode_xa<1> : k_decode_xa<2>, a.x, A, xa, a.M, a.K, a.r, s, C);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    count_launch();
     if (e != cudaSuccess) return e;
     a.xa = xa;
-    a.cluster = choose_cluster((a.N + ROWS - 1) / ROWS, a.K, sms, 2);
-    return glu ? launch_fmt<D_GLU>(format, a, st) : launch_fmt<D_ACT>(format, a, st);
+    return glu ? launch_fmt<D_GLU>(format, a, sms, st) : launch_fmt<D_ACT>(format, a, sms, st);
 }
 
 }  // namespace lora_host

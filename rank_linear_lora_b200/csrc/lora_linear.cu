@@ -1161,20 +1161,21 @@ lora_status_t fwd_impl(const uint16_t *x, const Weight &wt, const uint16_t *A, c
         lora_host::DecodeArgs d;
         std::memset(&d, 0, sizeof(d));
         d.x = x;
-        d.w = wt.coded() ? static_cast<const void *>(wt.Wq) : wt.W;
         d.wscale = wt.Wscale;
         if (wt.wf == WF_CB) std::copy(wt.codebook, wt.codebook + 16, d.cb);
-        d.B = B;
         d.out = h;
         d.save = fu.save;
         d.bias = fu.bias;
         d.residual = fu.residual;
+        d.err = reinterpret_cast<int *>(c.ws + c.plan.err);
         d.M = static_cast<int>(M);
         d.N = static_cast<int>(fu.op == OP_GLU ? d_out / 2 : d_out);
         d.K = static_cast<int>(d_in);
         d.r = r;
         d.act = fu.act;
-        return lora_host::launch_decode(A, sxa, s, wt.wf, fu.op == OP_GLU, d, PLAN_SMS, c.st) == cudaSuccess
+        d.B = B;
+        const void *w = wt.coded() ? static_cast<const void *>(wt.Wq) : wt.W;
+        return lora_host::launch_decode(A, sxa, s, wt.wf, fu.op == OP_GLU, d, w, PLAN_SMS, c.st) == cudaSuccess
                    ? LORA_OK : LORA_ERR_CUDA;
     }
     LORA_TRY(c.plan.side ? side_xa(c, x, A, sxa, M, d_in, r, s) : step_xa(c, x, A, sxa, M, d_in, r, s));
