@@ -414,8 +414,8 @@ typedef struct {
  *   xa_save  as lora_linear_fwd.
  *   act      a lora_act_t; LORA_ACT_NONE gives p = g * u.
  * d_ff % 8 == 0 (W's sizes as in the layer with d_out = 2 d_ff); the workspace is
- * lora_linear_workspace_size(the format's forward op, M, d_in, 2 d_ff, r).  Needs CTA pairs
- * (LORA_ERR_UNSUPPORTED without them).
+ * lora_linear_act_workspace_size(the format's forward op, M, d_in, 2 d_ff, r).  Needs CTA
+ * pairs for more than 16 tokens (LORA_ERR_UNSUPPORTED without them).
  */
 LORA_API lora_status_t lora_glu_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A, const uint16_t *B,
                                     uint16_t *p, uint16_t *gu_save, uint16_t *xa_save, int64_t M, int64_t d_in,
@@ -444,7 +444,8 @@ LORA_API lora_status_t lora_glu_bwd(const uint16_t *dP, const uint16_t *gu, cons
  *   out       output [M, d_out] (bf16), rounded once from fp32.
  *   pre_save  optional output [M, d_out] (bf16): pre, for the backward of an activation.
  * Everything else as lora_linear_fwd; the workspace is that of
- * lora_linear_workspace_size(the format's forward op, ...).  Needs CTA pairs.
+ * lora_linear_act_workspace_size(the format's forward op, ...).  Needs CTA pairs for more
+ * than 16 tokens.
  */
 LORA_API lora_status_t lora_linear_act_fwd(const uint16_t *x, const lora_weight_t *W, const uint16_t *A,
                                            const uint16_t *B, const uint16_t *bias, const uint16_t *residual,
@@ -469,8 +470,10 @@ LORA_API lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t 
                                            float *dbias, int64_t M, int64_t d_in, int64_t d_out, int r, float alpha,
                                            int act, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace of lora_linear_act_fwd / _bwd for `op`, a lora_op_t of the weight's
- * format (0 if the sizes are invalid).  Pure host function. */
+/* Bytes of workspace of lora_linear_act_fwd / _bwd, and of lora_glu_fwd with d_out = 2 d_ff, for
+ * `op`, a lora_op_t of the weight's format (0 if the sizes are invalid).  The forwards also run
+ * in less, down to lora_linear_workspace_size without its own hand-over buffer, with no tile cut
+ * along K.  Pure host function. */
 LORA_API size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r);
 
 /* Element types of the head operators' tensors. */

@@ -117,7 +117,7 @@ def _glu_forward(x, A, B, alpha, wt, act, save):
     gu = torch.empty(M, n, dtype=torch.bfloat16, device=x.device) if save else None
     xa = torch.empty(M, r, dtype=torch.bfloat16, device=x.device) if save else None
     if M > 0:
-        ws = _workspace(L.lora_linear_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
+        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
         L.lora_glu_fwd(x, wt, A, B, p, gu, xa, alpha, act, ws)
     return p, gu, xa
 

@@ -207,7 +207,7 @@ constexpr int pair_stages() {
 template <bool B_MN, int WF, int OP = OP_STORE>
 cudaError_t launch_pair(const GemmArgs &args, int grid, cudaStream_t st, DevInfo *dev, int attr_bit, int kind) {
     constexpr int S = pair_stages<WF>();
-    using Cfg = PairCfg<B_MN, WF, S>;
+    using Cfg = PairCfg<B_MN, WF, S, OP>;
     auto kern = k_tc_gemm_pair<B_MN, WF, S, OP>;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -557,6 +557,7 @@ struct Plan {
     bool dx_ksplit = false;     // bf16 backward: the dX GEMM's last wave cut along K, dA + dB after it
     size_t ks_part = 0, ks_flag = 0;  // K-split hand-over buffers (the end of the workspace)
     int ks_tiles = 0;           // tail tiles they hold
+    int fused_slots = 0;        // or accumulators, of a fused forward's cut
     size_t total_min = 0;       // the workspace without them (the forward then cuts along N)
     int dx_mode = 0;            // 0: dA beside the dX GEMM's last wave unless that wave can be cut
                                 // along N (then dA follows); 1: always beside; 2: always after
@@ -592,7 +593,33 @@ Split forced_split(int64_t kb, int splits) {
     return sp;
 }
 
-bool make_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r, int sms, Plan *pl) {
+// How a fused forward's tiles on C clusters are cut along K: `pieces` per cut tile (1: none), of
+// `cut` tiles.  With fewer tiles than clusters, as many pieces as put a cluster on each, of 8 K
+// blocks or more (4096 x 4096, 256 tokens: 16 tiles of 65 blocks; a piece costs the hand-over of
+// its accumulator); else the last wave's tiles in two, as the forward's.
+struct FusedCut {
+    int pieces = 1, cut = 0;
+    int slots() const { return cut * (pieces - 1); }
+};
+FusedCut fused_cut(int64_t M, int64_t d_out, int64_t K, int r, int64_t C) {
+    FusedCut f;
+    const int64_t T = cdiv(M, 256) * cdiv(d_out, 256), kb = cdiv(K, BK) + cdiv(r, BK);
+    if (C < 1) return f;
+    if (T < C) {
+        const int64_t P = std::min<int64_t>({C / T, kb / 8, 8});
+        if (P >= 2) {
+            f.pieces = static_cast<int>(P);
+            f.cut = static_cast<int>(T);
+        }
+    } else if (T % C > 0 && 2 * (T % C) <= C && kb >= KSPLIT_MIN_KB) {
+        f.pieces = 2;
+        f.cut = static_cast<int>(T % C);
+    }
+    return f;
+}
+
+// `fused`: a forward with a fused epilogue (its own K cut; d_out counts W's rows).
+bool make_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r, int sms, Plan *pl, bool fused = false) {
     const bool bwd = (op == LORA_OP_BWD || op == LORA_OP_BWD_Q4 || op == LORA_OP_BWD_FP8 || op == LORA_OP_BWD_NF4);
     const int64_t mt_tok = cdiv(M, BM), mt_in = cdiv(d_in, BM), mt_out = cdiv(d_out, BM);
     lora_plan_t ov;
@@ -645,7 +672,17 @@ bool make_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r, int sms, P
     }
     pl->total_min = off;
     pl->dx_ksplit = op == LORA_OP_BWD && ov.dx_overlap == 3;
-    if (pl->fwd_ksplit || pl->dx_ksplit) {
+    if (fused) {
+        pl->fwd_ksplit = false;
+        const int slots = M <= lora_host::DECODE_MAX_M ? 0 : fused_cut(M, d_out, d_in, r, PLAN_SMS / 2).slots();
+        if (slots > 0) {
+            pl->fused_slots = slots;
+            pl->ks_flag = off;
+            off = align256(off + static_cast<size_t>(slots) * 2 * sizeof(int));
+            pl->ks_part = off;
+            off = align256(off + static_cast<size_t>(slots) * 256 * 256 * 4);
+        }
+    } else if (pl->fwd_ksplit || pl->dx_ksplit) {
         // the last wave of the CTA-pair GEMM (256 x 256 tiles on PLAN_SMS / 2 clusters; the
         // forward's N = d_out, K = d_in, dX's N = d_in, K = d_out): K-split when it holds at
         // most half as many tiles as there are clusters and K + r is at least KSPLIT_MIN_KB
@@ -706,14 +743,17 @@ struct Ctx {
 };
 
 lora_status_t prepare(int op, int64_t M, int64_t d_in, int64_t d_out, int r, void *ws, size_t ws_bytes,
-                      void *stream, Ctx *c) {
+                      void *stream, Ctx *c, bool fused = false) {
     if (!device_info(&c->dev, &c->info)) return LORA_ERR_CUDA;
     if (!c->info->supported) return LORA_ERR_UNSUPPORTED;
-    make_plan(op, M, d_in, d_out, r, PLAN_SMS, &c->plan);
+    make_plan(op, M, d_in, d_out, r, PLAN_SMS, &c->plan, fused);
     if (!ws) return LORA_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return LORA_ERR_MISALIGNED;
     if (ws_bytes < c->plan.total_min) return LORA_ERR_WORKSPACE;
-    if (ws_bytes < c->plan.total) c->plan.fwd_ksplit = c->plan.dx_ksplit = false;  // no room for the hand-over
+    if (ws_bytes < c->plan.total) {  // no room for the hand-over
+        c->plan.fwd_ksplit = c->plan.dx_ksplit = false;
+        c->plan.fused_slots = 0;
+    }
     c->ws = static_cast<uint8_t *>(ws);
     c->st = static_cast<cudaStream_t>(stream);
     return LORA_OK;
@@ -999,14 +1039,25 @@ lora_status_t step_main(const Ctx &c, const MainOperands &o, int64_t M, int64_t 
         a.num_tiles = static_cast<int>(T);
         a.group_m = std::min(a.m_tiles, 8);
         const int64_t W = T / pair_C, R = T % pair_C;
+        const FusedCut fc = o.op != OP_STORE ? fused_cut(M, b_rows, K0, r, pair_C) : FusedCut();
+        const bool fcut = fc.slots() > 0 && fc.slots() <= c.plan.fused_slots;
         const bool kcut = ksplit && !q4 && W >= 1 && R > 0 && 2 * R <= pair_C && R <= c.plan.ks_tiles;
-        const bool split = !kcut && allow_tail_split && W >= 1 && R > 0 && 2 * R <= pair_C;
+        const bool split = !fcut && !kcut && allow_tail_split && W >= 1 && R > 0 && 2 * R <= pair_C;
         a.dp_tiles = static_cast<int>(split || kcut ? W * pair_C : T);
         a.dp_waves = static_cast<int>(split || kcut ? W : cdiv(T, pair_C));
         a.tail_tiles = static_cast<int>(split || kcut ? R : 0);
         a.tail_split = split ? 2 : 1;
         if (kcut) {
             a.tail_ksplit = 1;
+            a.ks_part = reinterpret_cast<float *>(c.ws + c.plan.ks_part);
+            a.ks_flag = reinterpret_cast<int *>(c.ws + c.plan.ks_flag);
+        }
+        if (fcut) {
+            a.tail_ksplit = 1;
+            a.ks_pieces = fc.pieces;
+            a.tail_tiles = fc.cut;
+            a.dp_tiles = static_cast<int>(T - fc.cut);
+            a.dp_waves = static_cast<int>(W);  // 0 where every tile is cut
             a.ks_part = reinterpret_cast<float *>(c.ws + c.plan.ks_part);
             a.ks_flag = reinterpret_cast<int *>(c.ws + c.plan.ks_flag);
         }
@@ -1030,7 +1081,8 @@ lora_status_t step_main(const Ctx &c, const MainOperands &o, int64_t M, int64_t 
                 if (!tmap_bf16(&a.tmB1n, o.B1, r, b_rows, 64, CTA_BN / 2)) return LORA_ERR_CUDA;
             }
         }
-        const int clusters = split || kcut ? pair_C : static_cast<int>(std::min<int64_t>(T, pair_C));
+        const int clusters = fcut && W == 0 ? fc.cut * fc.pieces
+                             : split || kcut || fcut ? pair_C : static_cast<int>(std::min<int64_t>(T, pair_C));
         if (idle_sms) *idle_sms = (!split && R > 0 && W >= 1) ? c.info->sms - static_cast<int>(2 * R) : 0;
         cudaError_t e;
         if (o.op == OP_ACT)
@@ -1153,7 +1205,7 @@ lora_status_t fwd_impl(const uint16_t *x, const Weight &wt, const uint16_t *A, c
         (xa_save && !aligned16(xa_save)))
         return LORA_ERR_MISALIGNED;
     Ctx c;
-    LORA_TRY(prepare(wt.op_fwd(), M, d_in, d_out, r, ws, ws_bytes, stream, &c));
+    LORA_TRY(prepare(wt.op_fwd(), M, d_in, d_out, r, ws, ws_bytes, stream, &c, fu.op != OP_STORE));
     const float s = alpha / static_cast<float>(r);
     uint16_t *sxa = xa_save ? xa_save : reinterpret_cast<uint16_t *>(c.ws + c.plan.xa);
     if (fu.op != OP_STORE && M <= lora_host::DECODE_MAX_M) {
@@ -1573,7 +1625,10 @@ size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d
     const size_t layer = lora_linear_workspace_size(op, M, d_in, d_out, r);
     if (layer == 0) return 0;
     const bool bwd = op == LORA_OP_BWD || op == LORA_OP_BWD_Q4 || op == LORA_OP_BWD_FP8 || op == LORA_OP_BWD_NF4;
-    return bwd ? act_bwd_layout(layer, M, d_out).total : layer;
+    if (bwd) return act_bwd_layout(layer, M, d_out).total;
+    Plan pl;
+    make_plan(op, M, d_in, d_out, r, PLAN_SMS, &pl, true);
+    return pl.total;
 }
 
 lora_status_t lora_linear_check(void *workspace, void *stream) {

@@ -113,6 +113,7 @@ struct GemmArgs {
     // two clusters; the first hands its fp32 accumulator over through ks_part and raises
     // its flag in ks_flag (zero on entry, cleared by the reader), the second adds it.
     int tail_ksplit;
+    // A fused epilogue's slots have the layout of ksplit_exchange instead.
     float *ks_part;          // [tail tile][CTA rank][chunk (4)][16-byte column group (16)][row (128)] float4
     int *ks_flag;            // [tail tile][CTA rank]
     // CTA-pair GEMM, MN-major bf16 weight: 1 when tmB0 is the 3D column-chunk map, so a
@@ -126,6 +127,7 @@ struct GemmArgs {
     int act;
     int out_cols, out_rows;
     int save;
+    int ks_pieces;           // with tail_ksplit: K pieces per cut tile (OP_STORE: always two)
     const uint16_t *bias;
     const uint16_t *residual;
     CUtensorMap tmS0, tmS1;

@@ -85,18 +85,24 @@ __host__ __device__ constexpr int dq_index(int w) {
 enum PairOp { OP_STORE = 0, OP_ACT = 1, OP_GLU = 2 };
 __host__ __device__ constexpr int pair_out_cols(int op) { return op == OP_GLU ? 128 : 256; }
 
-template <bool B_MN, int WF, int STAGES>
+template <bool B_MN, int WF, int STAGES, int OP = OP_STORE>
 struct PairCfg {
     static constexpr bool DQ = WF != WF_BF16;         // the weight's B tiles are decoded in shared memory
     static constexpr int A_BYTES = 128 * BK * 2;      // 16 KB: this CTA's 128 rows of A
     static constexpr int B_BYTES = CTA_BN * BK * 2;   // 16 KB: this CTA's 128 rows of B
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int Q_BYTES = DQ ? DQ_WARPS * DQ_QDEPTH * dq_qslot(WF) : 0;  // per-warp packed-code rings
-    static constexpr int EPI_BUFS = 2;  // output staging per epilogue warp: 32 rows x 64 columns, double-buffered
-    static constexpr int EPI_BYTES = 4 * EPI_BUFS * 32 * 128;
+    // A fused epilogue has more to do per value than OP_STORE's, so it gets eight warps, two to a
+    // TMEM quarter, where no dequant warps need the threads.  Against four, at d_in = d_out =
+    // 4096: 4096 tokens with gelu, bias and residual take 128 us, not 134; 17 tokens 27.6, not
+    // 33.1, and 256 tokens 35.5, not 41.1 (tiles cut along K, whose sums the epilogue joins).
+    static constexpr int EPI_WARPS = OP != OP_STORE && !DQ ? 8 : 4;
+    static constexpr int EPI_BUFS = 8 / EPI_WARPS;  // output staging per epilogue warp: 32 rows x 64 columns each
+    static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * 32 * 128;
     static constexpr int TMEM_COLS = 2 * PAIR_BN;     // two 256-column accumulators
     static constexpr int BAR_BYTES = DQ ? 1024 : 512;
-    static constexpr int THREADS = DQ ? NUM_THREADS + 32 * dq_warp_span(DQ_WARPS) : NUM_THREADS;  // + dequant warps
+    static constexpr int THREADS =
+        DQ ? NUM_THREADS + 32 * dq_warp_span(DQ_WARPS) : NUM_THREADS + 32 * (EPI_WARPS - 4);  // + dequant warps
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + Q_BYTES + EPI_BYTES + BAR_BYTES;
     static_assert(STAGES <= 32, "per-stage phase bits are kept in one 32-bit mask");
     static_assert(SMEM_BYTES <= 232448, "at most 227 KB of shared memory per CTA");
@@ -231,15 +237,18 @@ __device__ __forceinline__ bool get_pair_item(const GemmArgs &p, int cluster, in
         // 2tt + 1: the first half hands its fp32 partial over, the second (with the rank-r
         // tail) adds it; both hand-overs overlap the clusters' later tiles, and every
         // cluster ends after its whole tiles (W + 1/2 tiles on clusters 0 .. 2R-1).
-        const int tt = cluster >> 1;
+        // With a fused epilogue a tile may have more pieces (ks_pieces, when there are fewer tiles
+        // than clusters): all but the last hand over, the last adds them in order.
+        const int P = OP == OP_STORE ? 2 : p.ks_pieces;
+        const int tt = cluster / P, idx = cluster % P;
         if (tt < p.tail_tiles) {
             if (i == 0) {
-                const int kb_all = p.kb0 + p.kb1, kb_mid = kb_all / 2;
+                const int kb_all = p.kb0 + p.kb1;
                 raster(p, p.dp_tiles + tt, w.m, w.n);
-                w.kb_lo = (cluster & 1) ? kb_mid : 0;
-                w.kb_hi = (cluster & 1) ? kb_all : kb_mid;
-                w.piece = 1 + (cluster & 1);
-                w.job = tt;
+                w.kb_lo = kb_all * idx / P;
+                w.kb_hi = kb_all * (idx + 1) / P;
+                w.piece = idx == P - 1 ? 2 : 1;
+                w.job = OP == OP_STORE ? tt : tt * (P - 1) + (idx == P - 1 ? 0 : idx);  // its (first) slot
                 w.col0 = w.n * pair_out_cols(OP);
                 return true;
             }
@@ -286,6 +295,12 @@ __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&v)[W]) {
     else tmem_ld_32x32b_x16(taddr, v);
 }
 
+template <int W>
+__device__ __forceinline__ void tmem_st_row(uint32_t taddr, const uint32_t (&v)[W]) {
+    if constexpr (W == 32) tmem_st_32x32b_x32(taddr, v);
+    else tmem_st_32x32b_x16(taddr, v);
+}
+
 // W columns (a multiple of 8), starting at column c0 of the 64, of row `lane` of the
 // 32 x 64 staging box: fp32 to bf16, 16-byte chunks swizzled as stage_row64's.
 template <int W>
@@ -314,84 +329,123 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 &u, float *f) {
     }
 }
 
-// K-split last-wave tile of a fused epilogue (the hand-over of OP_STORE's, see the kernel):
-// the first half writes its fp32 accumulator to the workspace; the second adds it to its
-// own in tensor memory, so that the epilogue proper reads whole sums.  False after a wait
-// that ran out.
-__device__ __forceinline__ bool ksplit_exchange(const GemmArgs &p, const WorkItem &w, int rank, uint32_t t_row, int q,
-                                                int lane, int epi_tid, uint32_t tempty, volatile int *abort_flag,
-                                                volatile int *ks_ok) {
+// K-split tile of a fused epilogue: every piece but the last writes its fp32 accumulator to its
+// slot of the workspace; the last adds them, in order, to its own in tensor memory, so that the
+// epilogue proper reads whole sums.  Each warp moves the columns that its own epilogue reads (of
+// eight, 64 of every 128: the two warps of a TMEM quarter need no barrier between them).  Slot
+// layout, 128 KB per CTA: float4 [TMEM quarter (4)][half][16-byte column group][row (32)], so
+// that a warp's part is one contiguous range; warps whose rows lie behind the output move
+// nothing.  W columns at a time: 32, or 16 where the dequant warps leave fewer registers.
+// `land`: this warp's 16 or 32 KB of shared memory to bring the others' sums
+// to by bulk copies, a piece at a time (null: the stages are in use, and loads to registers
+// overlap the next tile instead).  False after a wait that ran out.
+constexpr int KS_BAR = 48;  // first of the epilogue warps' mbarriers for that, in the barrier array
+
+template <int EW, int W>
+__device__ __forceinline__ bool ksplit_exchange(const GemmArgs &p, const WorkItem &w, int rank, bool rows, uint32_t t_row,
+                                                int q, int half, int lane, int epi_tid, uint32_t tempty,
+                                                volatile int *abort_flag, volatile int *ks_ok, uint8_t *land,
+                                                uint32_t land_bar) {
     constexpr uint32_t KS_BYTES = 4 * 16 * 128 * 16;
-    const int slot = w.job * 2 + rank;
-    float4 *part = reinterpret_cast<float4 *>(p.ks_part) + static_cast<size_t>(slot) * (KS_BYTES / 16) + q * 32 + lane;
+    constexpr int COLS = PAIR_BN / (EW / 4);  // this warp's columns: its c-th is column_of(c)
+    auto column_of = [&](int c) { return EW == 8 ? c / 64 * 128 + half * 64 + c % 64 : c; };
+    // the 16-byte column group of this warp's c-th column, its rows
+    auto part_of = [&](int slot, int c) {
+        return reinterpret_cast<float4 *>(p.ks_part) + static_cast<size_t>(slot * 2 + rank) * (KS_BYTES / 16) +
+               (q * 64 + half * (COLS / 4) + c / 4) * 32;
+    };
     if (w.piece == 1) {
+        if (rows)
 #pragma unroll 1
-        for (int ch = 0; ch < 8; ++ch) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_row + ch * 32, v);
-            tc_wait_ld();
-            if (ch == 7) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty);
-            }
+            for (int c = 0; c < COLS; c += W) {
+                uint32_t v[W];
+                tmem_ld_row<W>(t_row + column_of(c), v);
+                tc_wait_ld();
+                float4 *part = part_of(w.job, c) + lane;
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-                __stcg(part + (ch * 8 + g) * 128,
-                       make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
-                                   __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3])));
-        }
+                for (int g = 0; g < W / 4; ++g)
+                    __stcg(part + g * 32, make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                                      __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3])));
+            }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty);
         __threadfence();
-        named_bar_sync(1, 128);
-        if (epi_tid == 0) st_release_gpu(p.ks_flag + slot, 1);
+        named_bar_sync(1, 32 * EW);
+        if (epi_tid == 0) st_release_gpu(p.ks_flag + w.job * 2 + rank, 1);
         return true;
     }
+    const int others = p.ks_pieces - 1;
     if (epi_tid == 0) {
-        const bool ok = wait_flag_bounded(p.ks_flag + slot, abort_flag, p.err, DERR_WAIT_PARTIAL);
-        if (ok) p.ks_flag[slot] = 0;  // zero again for the next call
+        bool ok = true;
+        for (int i = 0; ok && i < others; ++i) {
+            int *flag = p.ks_flag + (w.job + i) * 2 + rank;
+            ok = wait_flag_bounded(flag, abort_flag, p.err, DERR_WAIT_PARTIAL);
+            if (ok) *flag = 0;  // zero again for the next call
+        }
         *ks_ok = ok ? 1 : 0;
     }
-    named_bar_sync(1, 128);
+    named_bar_sync(1, 32 * EW);
     if (!*ks_ok) return false;
-#pragma unroll 1
-    for (int ch = 0; ch < 8; ++ch) {
-        float4 o[8];
-#pragma unroll
-        for (int g = 0; g < 8; ++g) o[g] = __ldcg(part + (ch * 8 + g) * 128);
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(t_row + ch * 32, v);
-        tc_wait_ld();
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + o[g].x);
-            v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + o[g].y);
-            v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + o[g].z);
-            v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + o[g].w);
+    if (!rows) return true;
+    bool ok = true;
+    for (int i = 0; i < others; ++i) {
+        if (land) {
+            fence_proxy_async_global();  // the others' stores, acquired above, before the copies' reads
+            fence_proxy_async_smem();    // and this warp's last reads of the landing area before its writes
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(land_bar, COLS / 4 * 512);
+                bulk_load(smem_u32(land), part_of(w.job + i, 0), COLS / 4 * 512, land_bar);
+            }
+            volatile int never = 0;  // the copies have to land whatever the others do
+            ok = wait_bounded(land_bar, static_cast<uint32_t>(i) & 1u, &never, p.err, DERR_WAIT_PARTIAL) && ok;
+            __syncwarp();
         }
-        tmem_st_32x32b_x32(t_row + ch * 32, v);
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += W) {
+            float4 o[W / 4];
+#pragma unroll
+            for (int g = 0; g < W / 4; ++g)
+                o[g] = land ? *reinterpret_cast<const float4 *>(land + (c / 4 + g) * 512 + lane * 16)
+                            : __ldcg(part_of(w.job + i, c) + g * 32 + lane);
+            uint32_t v[W];
+            tmem_ld_row<W>(t_row + column_of(c), v);
+            tc_wait_ld(v);
+#pragma unroll
+            for (int g = 0; g < W / 4; ++g) {
+                v[4 * g] = __float_as_uint(__uint_as_float(v[4 * g]) + o[g].x);
+                v[4 * g + 1] = __float_as_uint(__uint_as_float(v[4 * g + 1]) + o[g].y);
+                v[4 * g + 2] = __float_as_uint(__uint_as_float(v[4 * g + 2]) + o[g].z);
+                v[4 * g + 3] = __float_as_uint(__uint_as_float(v[4 * g + 3]) + o[g].w);
+            }
+            tmem_st_row<W>(t_row + column_of(c), v);
+        }
+        tc_wait_st();
     }
-    tc_wait_st();
-    return true;
+    return __all_sync(0xffffffffu, ok);
 }
 
 // The epilogue of one item: this warp's 32 rows from `row0`, the item's columns from
-// w.col0, 64 at a time.  Each 64-column box of each output goes through one of the warp's
-// two staging buffers and a TMA store, which also clips rows and columns outside the
-// output.  The accumulator is read once per output (tensor memory is far faster than the
-// stores), W columns at a time: 32, or 16 where the dequant warps leave fewer registers.
-// The tile's TMEM is released right after the last read.
-template <int OP, bool DQ>
-__device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem &w, int row0, uint32_t t_row, int lane,
-                                               uint32_t tempty, uint8_t *stage_base) {
+// w.col0, 64 at a time (with eight epilogue warps, `half` tells whose boxes are whose).  Each
+// 64-column box of each output goes through one of the warp's staging buffers and a TMA store,
+// which also clips rows and columns outside the output.  The accumulator is read once per
+// output (tensor memory is far faster than the stores), W columns at a time: 32, or 16 where
+// the dequant warps leave fewer registers.  The tile's TMEM is released right after the
+// warp's last read.
+template <int OP, bool DQ, int EW>
+__device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem &w, int row0, uint32_t t_row, int half,
+                                               int lane, uint32_t tempty, uint8_t *stage_base) {
     constexpr int W = DQ ? 16 : 32;
+    constexpr int BUFS = 8 / EW, STEP = EW / 4;
     const int nch = (pair_out_cols(OP) / 64) / w.nsplit;
     const int row = row0 + lane;
     int n_out = 0;
     // one 64-column box: fill(c, v, last) makes columns c .. c+W of the box
     auto emit = [&](const CUtensorMap *tm, int col, auto &&fill) {
-        uint8_t *sbuf = stage_base + (n_out & 1) * (32 * 128);
+        uint8_t *sbuf = stage_base + (n_out % BUFS) * (32 * 128);
         ++n_out;
-        if (lane == 0) bulk_wait_group_read<1>();
+        if (lane == 0) bulk_wait_group_read<BUFS - 1>();
         __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < 64; c += W) {
@@ -411,17 +465,21 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty);
     };
+    if (half >= nch) {  // a narrow tile of the gated form has one box
+        release();
+        return;
+    }
     if constexpr (OP == OP_GLU) {
         const int up0 = PAIR_BN / 2 / w.nsplit;  // TMEM column of the up half
 #pragma unroll 1
-        for (int ch = 0; ch < nch; ++ch) {
+        for (int ch = half; ch < nch; ch += STEP) {
             const int col = w.col0 + ch * 64;
             if (p.save) {
-                for (int half = 0; half < 2; ++half)
-                    emit(half ? &p.tmS1 : &p.tmS0, col, [&](int c, float(&v)[W]) {
+                for (int h = 0; h < 2; ++h)
+                    emit(h ? &p.tmS1 : &p.tmS0, col, [&](int c, float(&v)[W]) {
                         uint32_t a[W];
-                        tmem_ld_row<W>(t_row + half * up0 + ch * 64 + c, a);
-                        tc_wait_ld();
+                        tmem_ld_row<W>(t_row + h * up0 + ch * 64 + c, a);
+                        tc_wait_ld(a);
 #pragma unroll
                         for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
                     });
@@ -430,8 +488,9 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
                 uint32_t g[W], u[W];
                 tmem_ld_row<W>(t_row + ch * 64 + c, g);
                 tmem_ld_row<W>(t_row + up0 + ch * 64 + c, u);
-                tc_wait_ld();
-                if (ch == nch - 1 && c + W == 64) release();
+                tc_wait_ld(g);
+                tc_wait_ld(u);
+                if (ch + STEP >= nch && c + W == 64) release();
                 act_dispatch(p.act, [&](auto A) {
 #pragma unroll
                     for (int e = 0; e < W; ++e) v[e] = act_value<A.value>(__uint_as_float(g[e])) * __uint_as_float(u[e]);
@@ -439,7 +498,7 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
             });
         }
     } else {
-        // bias and residual, 8 columns a load; columns and rows outside the output read nothing
+        // bias, 8 columns a load; columns outside the output read nothing
         auto add8 = [&](const uint16_t *src, int col, float *v) {
             if (col < p.out_cols) {
                 float f[8];
@@ -450,14 +509,24 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
         };
         const uint16_t *res_row = p.residual && row < p.out_rows
                                       ? p.residual + static_cast<int64_t>(row) * p.out_cols : nullptr;
+        // the residual of W columns (zero outside the output), requested a step ahead of its use
+        auto load_res = [&](int col, uint4 (&r)[W / 8]) {
+#pragma unroll
+            for (int e = 0; e < W / 8; ++e)
+                r[e] = res_row && col + 8 * e < p.out_cols
+                           ? __ldcg(reinterpret_cast<const uint4 *>(res_row + col + 8 * e)) : make_uint4(0, 0, 0, 0);
+            __syncwarp();  // rows outside took the other branch; what follows is warp-wide
+        };
+        uint4 next[W / 8];
+        load_res(w.col0 + half * 64, next);
 #pragma unroll 1
-        for (int ch = 0; ch < nch; ++ch) {
+        for (int ch = half; ch < nch; ch += STEP) {
             const int col = w.col0 + ch * 64;
             if (p.save)
                 emit(&p.tmS0, col, [&](int c, float(&v)[W]) {
                     uint32_t a[W];
                     tmem_ld_row<W>(t_row + ch * 64 + c, a);
-                    tc_wait_ld();
+                    tc_wait_ld(a);
 #pragma unroll
                     for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
                     if (p.bias)
@@ -465,17 +534,14 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
                         for (int e = 0; e < W; e += 8) add8(p.bias, col + c + e, v + e);
                 });
             emit(&p.tmC, col, [&](int c, float(&v)[W]) {
-                uint4 r[W / 8];
-#pragma unroll
-                for (int e = 0; e < W / 8; ++e)
-                    r[e] = res_row && col + c + 8 * e < p.out_cols
-                               ? __ldcg(reinterpret_cast<const uint4 *>(res_row + col + c + 8 * e))
-                               : make_uint4(0, 0, 0, 0);
-                __syncwarp();  // rows past the output took the other branch; the TMEM load is warp-wide
                 uint32_t a[W];
                 tmem_ld_row<W>(t_row + ch * 64 + c, a);
-                tc_wait_ld();
-                if (ch == nch - 1 && c + W == 64) release();
+                tc_wait_ld(a);
+                if (ch + STEP >= nch && c + W == 64) release();
+                uint4 r[W / 8];
+#pragma unroll
+                for (int e = 0; e < W / 8; ++e) r[e] = next[e];
+                if (p.residual && (c + W < 64 || ch + STEP < nch)) load_res(c + W < 64 ? col + c + W : col + STEP * 64, next);
 #pragma unroll
                 for (int e = 0; e < W; ++e) v[e] = __uint_as_float(a[e]);
                 if (p.bias)
@@ -498,9 +564,9 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &p, const WorkItem
 }
 
 template <bool B_MN, int WF, int STAGES, int OP = OP_STORE>
-__global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
+__global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES, OP>::THREADS, 1)
     k_tc_gemm_pair(const __grid_constant__ GemmArgs p) {
-    using Cfg = PairCfg<B_MN, WF, STAGES>;
+    using Cfg = PairCfg<B_MN, WF, STAGES, OP>;
     constexpr bool DQ = Cfg::DQ;  // the weight's B tiles are decoded (4-bit or FP8 codes)
     constexpr int QSLOT = dq_qslot(WF);
     extern __shared__ uint8_t smem_raw[];
@@ -548,9 +614,11 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&tfull_bar[b]), 1);
-            mbar_init(smem_u32(&tempty_bar[b]), 8);
+            mbar_init(smem_u32(&tempty_bar[b]), 2 * Cfg::EPI_WARPS);
         }
         mbar_init(smem_u32(drain_bar), 1);
+        if (OP != OP_STORE)
+            for (int e = 0; e < Cfg::EPI_WARPS; ++e) mbar_init(smem_u32(&bars[KS_BAR + e]), 1);
         if (DQ) {
             for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bready_bar[s]), 2 * dq_group_warps(WF));
             for (int q = 0; q < DQ_WARPS * DQ_QDEPTH; ++q) mbar_init(smem_u32(&qfull_bar[q]), 1);
@@ -582,7 +650,10 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
     cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    grid_dep_wait();
+    // A fused forward's predecessor is the s.xa kernel, which lets it start only once all its own
+    // CTAs have seen everything before it complete: x, W and B are final, and only the rank-r
+    // segment (s.xa) and the epilogue (whose outputs earlier kernels may read) wait for it.
+    if (OP == OP_STORE) grid_dep_wait();
     grid_dep_launch_dependents();
     if (trace && threadIdx.x == 0) {
         trace[TR_SETUP] = globaltimer_ns();
@@ -592,6 +663,7 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
+            bool dep_waited = OP == OP_STORE;
             int stage = 0;
             uint32_t phase = 0;
             uint32_t issued_mask = 0, issued_phase = 0;  // leader's full barriers
@@ -623,6 +695,10 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
                         mbar_arrive_expect_tx(fb_local, tx);
                         issued_mask |= 1u << stage;
                         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    }
+                    if (seg1 && !dep_waited) {
+                        dep_waited = true;
+                        grid_dep_wait();
                     }
                     const int k0 = (seg1 ? kb - p.kb0 : kb) * BK;
                     const uint32_t a_dst = smem_u32(sA + stage * Cfg::A_BYTES);
@@ -794,6 +870,17 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             int j, item, kb, b_row;
             bool valid;
         };
+        // Weight K blocks of item 0 (a piece of a tile cut along K has its own range) and its blocks
+        // with the rank-r ones; every later item has kb0 and kb_all.
+        int k_lo0 = 0, kw0 = p.kb0, kt0 = kb_all;
+        if constexpr (OP != OP_STORE) {
+            WorkItem w0;
+            if (get_pair_item<OP>(p, cluster, n_clusters, 0, w0) && w0.piece > 0) {
+                k_lo0 = w0.kb_lo;
+                kw0 = min(w0.kb_hi, p.kb0) - w0.kb_lo;
+                kt0 = w0.kb_hi - w0.kb_lo;
+            }
+        }
         auto enter_item = [&](Cursor &c) {
             WorkItem wi;
             c.valid = get_pair_item<OP>(p, cluster, n_clusters, c.item, wi);
@@ -802,14 +889,31 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         auto seek = [&](Cursor &c, int j) {
             const int wit = grp + j * DQ_GROUPS;
             c.j = j;
-            c.item = wit / p.kb0;
-            c.kb = wit - c.item * p.kb0;
+            if constexpr (OP == OP_STORE) {
+                c.item = wit / p.kb0;
+                c.kb = wit - c.item * p.kb0;
+            } else if (wit < kw0) {
+                c.item = 0;
+                c.kb = k_lo0 + wit;
+            } else {
+                c.item = 1 + (wit - kw0) / p.kb0;
+                c.kb = (wit - kw0) % p.kb0;
+            }
             enter_item(c);
         };
         auto step = [&](Cursor &c) {
             ++c.j;
             c.kb += DQ_GROUPS;
-            if (c.kb >= p.kb0) {
+            if constexpr (OP != OP_STORE) {
+                int end = c.item == 0 ? k_lo0 + kw0 : p.kb0;
+                if (c.kb >= end) {
+                    for (; c.kb >= end; end = p.kb0) {
+                        c.kb -= end;
+                        ++c.item;
+                    }
+                    enter_item(c);
+                }
+            } else if (c.kb >= p.kb0) {
                 const int adv = c.kb / p.kb0;
                 c.kb -= adv * p.kb0;
                 c.item += adv;
@@ -855,7 +959,8 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         for (int i = 0; i < DQ_RUNS; ++i) sc[i] = scale_bits(cur, i);
         while (cur.valid) {
             const int j = cur.j;
-            const int flat = cur.item * kb_all + cur.kb;
+            const int flat = OP == OP_STORE ? cur.item * kb_all + cur.kb
+                                            : cur.item == 0 ? cur.kb - k_lo0 : kt0 + (cur.item - 1) * kb_all + cur.kb;
             const int stage = flat % STAGES;
             const int slot = j % DQ_QDEPTH;
             const long long c0 = tr_dq ? clock64() : 0;
@@ -958,6 +1063,7 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
         const int epi_tid = threadIdx.x - 64;
         const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty_bar[0]), 0);
         const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty_bar[1]), 0);
+        if (OP != OP_STORE) grid_dep_wait();
         int it = 0;
         WorkItem w;
         for (; get_pair_item<OP>(p, cluster, n_clusters, it, w); ++it) {
@@ -966,23 +1072,29 @@ __global__ void __launch_bounds__(PairCfg<B_MN, WF, STAGES>::THREADS, 1)
             if (epi_tid == 0)
                 epi_ok[it & 1] = wait_bounded(smem_u32(&tfull_bar[buf]), aphase, abort_flag, p.err,
                                               DERR_WAIT_TMEM_FULL) ? 1 : 0;
-            named_bar_sync(1, 128);
+            named_bar_sync(1, 32 * Cfg::EPI_WARPS);
             if (!epi_ok[it & 1]) break;
             tc_fence_after();
             if constexpr (OP != OP_STORE) {
                 const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                        static_cast<uint32_t>(buf * PAIR_BN);
                 const uint32_t tempty = buf ? tempty_leader1 : tempty_leader0;
-                if (!DQ && w.piece > 0) {
-                    if (!ksplit_exchange(p, w, static_cast<int>(rank), t_row, q, lane, epi_tid, tempty, abort_flag, ks_ok))
+                const int row0 = w.m * PAIR_BM + static_cast<int>(rank) * 128 + q * 32;
+                const int ew = warp - 2, half = ew / 4;  // with eight warps: which half of the columns
+                if (w.piece > 0) {
+                    // with no further tile the stages are free once the accumulator is complete
+                    uint8_t *land = p.dp_waves == 0 ? smem + ew * (Cfg::EPI_WARPS == 8 ? 16384 : 32768) : nullptr;
+                    if (!ksplit_exchange<Cfg::EPI_WARPS, DQ ? 16 : 32>(p, w, static_cast<int>(rank), row0 < p.out_rows, t_row, q,
+                                                                       half, lane, epi_tid, tempty, abort_flag, ks_ok, land,
+                                                                       smem_u32(&bars[KS_BAR + ew])))
                         break;
                     if (w.piece == 1) {
                         if (trace && epi_tid == 0 && it < 8) trace[TR_TILE_DONE0 + it] = globaltimer_ns();
                         continue;
                     }
                 }
-                fused_epilogue<OP, DQ>(p, w, w.m * PAIR_BM + static_cast<int>(rank) * 128 + q * 32, t_row, lane,
-                                       tempty, sEpi + (q * Cfg::EPI_BUFS) * (32 * 128));
+                fused_epilogue<OP, DQ, Cfg::EPI_WARPS>(p, w, row0, t_row, half, lane, tempty,
+                                                       sEpi + ew * Cfg::EPI_BUFS * (32 * 128));
                 if (trace && epi_tid == 0 && it < 8) trace[TR_TILE_DONE0 + it] = globaltimer_ns();
                 continue;
             }

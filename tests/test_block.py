@@ -152,11 +152,18 @@ def test_unfused_heads(interleaved, monkeypatch):
 
 
 def test_workspace_sizes(lib):
-    """The forward's workspace is the layer's; the backward's holds the bias partials too."""
+    """The backward's workspace holds the bias partials besides the layer's; the forward's, its own
+    hand-over of tiles cut along K, if any."""
     for op in range(8):
         layer = L.lora_linear_workspace_size(op, 512, 1024, 768, 16)
         own = L.lora_linear_act_workspace_size(op, 512, 1024, 768, 16)
-        assert own == layer if op % 2 == 0 else own >= layer + 768 * 4
+        assert own >= layer + 768 * 4 if op % 2 else own > 0
+    # 16 tiles of 256 x 256 for 256 tokens of 4096 columns: pieces of each on all 74 CTA pairs
+    cut = L.lora_linear_act_workspace_size(L.OP_FWD, 256, 4096, 4096, 8)
+    assert cut >= 3 * 16 * 256 * 256 * 4
+    assert cut == L.lora_linear_act_workspace_size(L.OP_FWD_Q4, 256, 4096, 4096, 8)
+    # a few tokens cut nothing
+    assert L.lora_linear_act_workspace_size(L.OP_FWD, 16, 4096, 4096, 8) < 1 << 20
     assert L.lora_linear_act_workspace_size(8, 512, 1024, 768, 16) == 0
     assert L.lora_linear_act_workspace_size(0, 0, 1024, 768, 16) == 0
     assert L.lora_linear_act_workspace_size(1, 1, 8, 8, 8) > 0

@@ -39,6 +39,13 @@ GLU = [
     (1280, 2056, 2048, 16, "bf16", "silu"),  # 80 tiles, 33 K blocks: the last wave cut along K
     (1280, 264, 2048, 16, "bf16", "silu"),   # 5 K blocks: cut along N
     (1280, 2112, 2048, 16, "q4", "silu"),    # several tiles per CTA pair on a coded weight
+    # fewer tiles than CTA pairs: every tile cut along K, in two to eight pieces
+    (33, 1040, 520, 16, "bf16", "silu"),
+    (200, 4104, 264, 72, "bf16", "gelu"),
+    (40, 4160, 264, 16, "q4", "silu"),
+    (257, 4160, 136, 16, "nf4", "relu"),
+    (129, 4112, 136, 72, "fp8", "silu"),
+    (140, 1088, 72, 16, "q4", "none"),
 ]
 
 
@@ -58,7 +65,7 @@ def _glu_reference(y, act):
 def test_glu_forward(case, save):
     M, d, f, r, fmt, act = case
     y = Layer(M, d, 2 * f, r, fmt, seed=11 + M)
-    ws = L.workspace(y.wt.ops()[0], M, d, 2 * f, r)
+    ws = L.act_workspace(y.wt.ops()[0], M, d, 2 * f, r)
     p, gu, xa = _bf(M, f), _bf(M, 2 * f) if save else None, _bf(M, r) if save else None
     n0 = L.lora_linear_launch_count()
     L.lora_glu_fwd(y.x, y.wt, y.A, y.B, p, gu, xa, y.alpha, act, ws)
@@ -72,6 +79,25 @@ def test_glu_forward(case, save):
     L.lora_glu_fwd(y.x, y.wt, y.A, y.B, again, None, None, y.alpha, act, ws)
     L.lora_linear_check(ws)
     assert torch.equal(p, again)  # the same bits, and the workspace left ready for the next call
+
+
+@pytest.mark.parametrize("M,d,f,r,fmt", [(200, 4104, 264, 72, "bf16"), (256, 4096, 512, 16, "bf16"), (130, 4096, 520, 16, "fp8")])
+def test_k_cut_tiles_give_the_same_bits_every_time(M, d, f, r, fmt):
+    """Few tiles and a long sum: each tile's pieces come from several CTA pairs, and warps of one
+    tile add and read them side by side."""
+    y = Layer(M, d, 2 * f, r, fmt, seed=5)
+    ws = L.act_workspace(y.wt.ops()[0], M, d, 2 * f, r)
+    n = 2 * f
+    res, o = _bf(M, n), [_bf(M, n) for _ in range(2)]
+    res.normal_()
+    p = [_bf(M, f) for _ in range(2)]
+    for i in range(100):
+        L.lora_glu_fwd(y.x, y.wt, y.A, y.B, p[i > 0], None, None, y.alpha, "gelu", ws)
+        L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, None, res, o[i > 0], None, None, y.alpha, "gelu", ws)
+        assert torch.equal(p[0], p[i > 0]) and torch.equal(o[0], o[i > 0]), i
+    L.lora_linear_check(ws)
+    h, err, want, bound = _glu_reference(y, "gelu")
+    assert_within("p", p[1], want, bound)
 
 
 GLU_BWD = [
@@ -126,6 +152,11 @@ ACT = [
     (1280, 2056, 4096, 16, "bf16", "gelu", True, True),  # 80 tiles: cut along K
     (1280, 264, 4104, 16, "bf16", "none", True, True),   # 85 tiles: cut along N
     (1280, 2112, 4096, 16, "fp8", "silu", True, True),
+    (33, 1040, 520, 16, "bf16", "silu", True, True),      # cut along K in two to eight pieces
+    (200, 4104, 264, 72, "bf16", "none", False, True),
+    (40, 4160, 264, 16, "q4", "gelu", True, True),
+    (257, 4160, 136, 16, "nf4", "none", True, False),
+    (129, 4112, 136, 72, "fp8", "silu", False, True),
 ]
 
 
