@@ -4,7 +4,9 @@
 * ``lora_linear_act``: a projection with bias, activation and residual in its epilogue;
 * ``qk_norm_rope``: the norms of queries and keys for each head with the rotation of their
   positions (``rope_table`` makes its angles), and ``qkv_heads``, the same on the stacked
-  output of the q/k/v projections.
+  output of the q/k/v projections;
+* the modules built of them: ``LoraProjections`` (several projections of one x, each with its
+  own adapter), ``LoraQKV`` and ``LoraGatedMLP``.
 
 The projections take the frozen weight as a bf16 tensor or as a ``FrozenWeight`` of any format, and
 trainable adapters A, B of the (stacked) layer; gradients flow to x, A, B, the bias and the
@@ -29,6 +31,7 @@ from torch.autograd.function import once_differentiable
 
 from . import autograd as LA
 from . import lora_linear as L
+from .multi import _exact_f32_product
 
 _ws_lock = threading.Lock()
 _ws_cache: collections.OrderedDict = collections.OrderedDict()
@@ -95,19 +98,25 @@ def _rows(x):
     return x2 if x2.is_contiguous() else x2.contiguous()
 
 
-def _adapter_grads(A, B):
-    """fp32 (dA, dB) next to each other, and a function that gives them in A's and B's types:
-    one cast where those are the same."""
-    both = torch.empty(A.numel() + B.numel(), dtype=torch.float32, device=A.device)
-    na = A.numel()
+def _grad_buffers(*params):
+    """fp32 gradients of `params` (None for None) next to each other, and a function that gives
+    them in the parameters' types: one cast where those are the same."""
+    dtype = {t.dtype for t in params if t is not None}
+    sizes = [0 if t is None else t.numel() for t in params]
+    dev = next((t.device for t in params if t is not None), None)
+    flat = torch.empty(sum(sizes), dtype=torch.float32, device=dev) if dtype else None
+
+    def parts(buf):
+        return [None if t is None else v.view(t.shape) for t, v in zip(params, buf.split(sizes))] if dtype else list(params)
+
+    grads = parts(flat)
 
     def typed():
-        if A.dtype != B.dtype:
-            return both[:na].view(A.shape).to(A.dtype), both[na:].view(B.shape).to(B.dtype)
-        t = both.to(A.dtype)
-        return t[:na].view(A.shape), t[na:].view(B.shape)
+        if len(dtype) == 1:
+            return parts(flat.to(*dtype))
+        return [None if t is None else g.to(t.dtype) for t, g in zip(params, grads)]
 
-    return both[:na].view(A.shape), both[na:].view(B.shape), typed
+    return grads, typed
 
 
 # ------------------------------------------------------------------ gated projections
@@ -141,7 +150,7 @@ class LoraGluFunction(torch.autograd.Function):
         dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
         if M == 0:
             return dX, torch.zeros_like(A), torch.zeros_like(B), None, None, None
-        dA, dB, typed = _adapter_grads(A, B)
+        (dA, dB), typed = _grad_buffers(A, B)
         dGU = torch.empty_like(gu)
         ws = _workspace(L.lora_linear_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_glu_bwd(dP.contiguous(), gu, x, wt, A, B, xa, dGU, dX, dA, dB, ctx.alpha, ctx.act, ws)
@@ -193,30 +202,29 @@ class LoraLinearActFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, A, B, bias, residual, alpha, wt, act):
         out, pre, xa = _act_forward(x, A, B, bias, residual, alpha, wt, act, save=True)
-        ctx.save_for_backward(x, A, B, xa, pre, *wt.tensors)
+        ctx.save_for_backward(x, A, B, xa, pre, bias, *wt.tensors)
         ctx.alpha, ctx.wt, ctx.act = alpha, wt, act
-        ctx.bias_dtype = None if bias is None else bias.dtype
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dOut):
-        x, A, B, xa, pre = ctx.saved_tensors[:5]
+        x, A, B, xa, pre, bias = ctx.saved_tensors[:6]
         wt = ctx.wt
         M, r, n = x.shape[0], A.shape[0], wt.d_out
         dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
         dres = dOut if ctx.needs_input_grad[4] else None
-        want_bias = ctx.needs_input_grad[3]
+        if not ctx.needs_input_grad[3]:
+            bias = None
         if M == 0:
-            dbias = torch.zeros(n, dtype=ctx.bias_dtype, device=x.device) if want_bias else None
+            dbias = None if bias is None else torch.zeros_like(bias)
             return dX, torch.zeros_like(A), torch.zeros_like(B), dbias, dres, None, None, None
         dOut = dOut.contiguous()
-        dA, dB, typed = _adapter_grads(A, B)
-        dbias = torch.empty(n, dtype=torch.float32, device=x.device) if want_bias else None
+        (dA, dB, dbias), typed = _grad_buffers(A, B, bias)
         dPre = torch.empty_like(dOut) if ctx.act != "none" else None
         ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_linear_act_bwd(dOut, pre, x, wt, A, B, xa, dPre, dX, dA, dB, dbias, ctx.alpha, ctx.act, ws)
-        return dX, *typed(), dbias.to(ctx.bias_dtype) if want_bias else None, dres, None, None, None
+        return dX, *typed(), dres, None, None, None
 
 
 def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str = "none"):
@@ -279,17 +287,19 @@ def _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleav
     return q_out, k_out
 
 
-def _heads_backward(grads, ins, weights, tables, outs, want_w, eps, interleaved, norm):
-    """The library's backward into `outs`; the fp32 weight gradients (None where not wanted)."""
-    one = next(t for t in ins if t is not None)
-    M, _, D = one.shape
-    dw = [torch.empty(D, dtype=torch.float32, device=one.device) if w else None for w in want_w]
+def _heads_backward(grads, ins, weights, tables, outs, needs, eps, interleaved, norm):
+    """The library's backward into `outs`; the gradients of those of the weights that need one."""
+    M, hq, D = ins[0].shape
+    trained = [w if n else None for w, n in zip(weights, needs)]
+    if M == 0:
+        return [None if w is None else torch.zeros_like(w) for w in trained]
+    dw, typed = _grad_buffers(*trained)
     ws = None
-    if any(want_w):
-        heads = sum(t.shape[1] for t in ins if t is not None)
-        ws = torch.empty(L.lora_qk_norm_rope_workspace_size(M, heads, D), dtype=torch.uint8, device=one.device)
+    if any(t is not None for t in dw):
+        n = L.lora_qk_norm_rope_workspace_size(M, hq + ins[1].shape[1], D)
+        ws = torch.empty(n, dtype=torch.uint8, device=ins[0].device)
     L.lora_qk_norm_rope_bwd(*grads, *ins, *weights, *tables, *outs, *dw, ws, eps, interleaved, norm)
-    return dw
+    return typed()
 
 
 class QkNormRopeFunction(torch.autograd.Function):
@@ -307,13 +317,8 @@ class QkNormRopeFunction(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
         dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        want = [w is not None and n for w, n in zip((wq, wk), ctx.needs_input_grad[2:4])]
-        if q.shape[0] == 0:
-            dw = [torch.zeros_like(w) if n else None for w, n in zip((wq, wk), want)]
-        else:
-            dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
-                                 (dq, dk), want, *ctx.rest)
-            dw = [None if t is None else t.to(q.dtype) for t in dw]
+        dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
+                             (dq, dk), ctx.needs_input_grad[2:4], *ctx.rest)
         return dq, dk, *dw, None, None, None, None, None, None
 
 
@@ -392,13 +397,8 @@ class QkvHeadsFunction(torch.autograd.Function):
         dq, dk, dv_part = QkvHeadsFunction.split(dh, *ctx.heads)
         dv_part.copy_(dv)
         q, k, _ = QkvHeadsFunction.split(h, *ctx.heads)
-        want = [w is not None and n for w, n in zip((wq, wk), ctx.needs_input_grad[1:3])]
-        if h.shape[0] == 0:
-            dw = [torch.zeros_like(w) if n else None for w, n in zip((wq, wk), want)]
-        else:
-            dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
-                                 (dq, dk), want, *ctx.rest)
-            dw = [None if t is None else t.to(h.dtype) for t in dw]
+        dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
+                             (dq, dk), ctx.needs_input_grad[1:3], *ctx.rest)
         return dh, *dw, *(None,) * 9
 
 
@@ -421,3 +421,128 @@ def qkv_heads(h, hq: int, hk: int, D: int, q_weight=None, k_weight=None, cos=Non
     q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
     outs = (*qk_norm_rope(q, k, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm), v)
     return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)
+
+
+# ------------------------------------------------------------------ modules
+class _OwnBlocks(torch.autograd.Function):
+    """B as it is; its gradient outside the blocks of the projections is zero (those entries are
+    held at zero and belong to no projection)."""
+
+    @staticmethod
+    def forward(ctx, B, rows, r):
+        ctx.rows, ctx.r = rows, r
+        return B.view_as(B)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dB):
+        out = torch.zeros_like(dB)
+        for p, (a, b) in enumerate(ctx.rows):
+            out[a:b, p * ctx.r:(p + 1) * ctx.r] = dB[a:b, p * ctx.r:(p + 1) * ctx.r]
+        return out, None, None
+
+
+def _layer(W, r, alpha):
+    """A LoraLinear over a bf16 tensor or a FrozenWeight."""
+    wt = _frozen(W)
+    return LA.LoraLinear(wt.tensors[0], r, alpha) if wt.kind == "bf16" else LA.LoraLinear(r=r, alpha=alpha, frozen=wt)
+
+
+class LoraProjections(torch.nn.Module):
+    """P projections of one x with a frozen weight each, stacked in W [sum d_outs, d_in] (a bf16
+    tensor or a FrozenWeight), and an adapter of rank r each, as
+    multi.SharedInputProjections lays them out: lora_A [P r, d_in], and lora_B [sum d_outs, P r]
+    block-diagonal, whose other entries stay zero.  A_p and B_p give projection p's own."""
+
+    def __init__(self, W, d_outs, r: int = 8, alpha: float = 16.0):
+        super().__init__()
+        P = len(d_outs)
+        self.layer = _layer(W, P * r, alpha)
+        if P < 1 or sum(d_outs) != self.layer.frozen.d_out:
+            raise ValueError(f"d_outs: widths that add up to the weight's {self.layer.frozen.d_out} rows, got {d_outs}")
+        if not _exact_f32_product(alpha, P):
+            raise ValueError(f"alpha={alpha!r}: {P}*alpha must be exact in fp32")
+        self.d_outs, self.r, self.alpha = list(d_outs), r, float(alpha)
+        self.layer.alpha = P * float(alpha)  # the stacked layer has rank P r: the same alpha / r
+        ends = [0]
+        for d in d_outs:
+            ends.append(ends[-1] + d)
+        self.rows = list(zip(ends, ends[1:]))
+
+    def A_p(self, p: int):
+        return self.layer.lora_A[p * self.r:(p + 1) * self.r]
+
+    def B_p(self, p: int):
+        return self.layer.lora_B[slice(*self.rows[p]), p * self.r:(p + 1) * self.r]
+
+    def operands(self):
+        """(frozen weight, A, B, alpha) of the stacked layer, for the operators above."""
+        B = self.layer.lora_B
+        if torch.is_grad_enabled() and B.requires_grad:
+            B = _OwnBlocks.apply(B, self.rows, self.r)
+        return self.layer._frozen(), self.layer.lora_A, B, self.layer.alpha
+
+    def merged_weight(self):
+        """The stacked W' = w + s.B.A in bf16 (LoraLinear.merged_weight)."""
+        return self.layer.merged_weight()
+
+    def forward(self, x):
+        """[h_0 | h_1 | ...] [..., sum d_outs]."""
+        return lora_linear_act(x, *self.operands())
+
+
+class LoraQKV(LoraProjections):
+    """The q, k and v projections of x with the norms of the heads of q and k (their weights
+    q_norm and k_norm [D] are parameters; norm=False: none) and the rotation of the positions
+    (rotary dimensions `rot`, 0: none)."""
+
+    def __init__(self, W, hq: int, hk: int, D: int, r: int = 8, alpha: float = 16.0, *, max_positions: int = 0,
+                 rot: int = None, theta: float = 10000.0, eps: float = 1e-6, interleaved: bool = False, norm: bool = True):
+        super().__init__(W, (hq * D, hk * D, hk * D), r, alpha)
+        dev = self.layer.lora_A.device
+        self.heads, self.eps, self.interleaved, self.norm = (hq, hk, D), eps, interleaved, norm
+        for name in ("q_norm", "k_norm"):
+            w = torch.nn.Parameter(torch.ones(D, dtype=torch.bfloat16, device=dev)) if norm else None
+            self.register_parameter(name, w)
+        rot = D if rot is None else rot
+        cos, sin = rope_table(max_positions, rot, theta, device=dev) if max_positions and rot else (None, None)
+        self.register_buffer("cos", cos, persistent=False)
+        self.register_buffer("sin", sin, persistent=False)
+        self.table = max_positions, rot, theta
+
+    def _apply(self, fn, recurse=True):
+        """The angles stay in fp32 whatever type the module is converted to."""
+        super()._apply(fn, recurse)
+        if self.cos is not None and self.cos.dtype is not torch.float32:
+            self.cos, self.sin = rope_table(*self.table, device=self.cos.device)
+        return self
+
+    def forward(self, x, positions=None):
+        """(q [..., hq, D], k [..., hk, D], v [..., hk, D]); positions [...] int64."""
+        if self.cos is None:
+            positions = None
+        elif positions is None:
+            raise ValueError("positions: the tokens' positions, int64, one for each")
+        return qkv_heads(super().forward(x), *self.heads, self.q_norm, self.k_norm, self.cos, self.sin, positions,
+                         self.eps, self.interleaved, self.norm)
+
+
+class LoraGatedMLP(torch.nn.Module):
+    """down(act(gate(x)) * up(x)) + residual, an adapter of rank r on each of the three: the
+    gate's and the up projection's frozen weights stacked [2 d_ff, d_in] and the down
+    projection's [d_out, d_ff], each a bf16 tensor or a FrozenWeight."""
+
+    def __init__(self, gate_up, down, r: int = 8, alpha: float = 16.0, act: str = "silu"):
+        super().__init__()
+        L._act(act)
+        gate_up, down = _frozen(gate_up), _frozen(down)
+        if gate_up.d_out != 2 * down.d_in:
+            raise ValueError(f"gate and up give {gate_up.d_out // 2} values, down takes {down.d_in}")
+        self.gate_up = LoraProjections(gate_up, (down.d_in, down.d_in), r, alpha)
+        self.down = _layer(down, r, alpha)
+        self.act = act
+
+    def forward(self, x, residual=None):
+        p = lora_glu(x, *self.gate_up.operands(), act=self.act)
+        d = self.down
+        return lora_linear_act(p, d._frozen(), d.lora_A, d.lora_B, d.alpha, residual=residual)

@@ -206,3 +206,54 @@ def test_unfused_compositions(act, monkeypatch):
     torch.testing.assert_close(o.double(), f(h + bias.detach().double()) + res.detach().double(), rtol=4e-2, atol=6e-2)
     (p.float().sum() + o.float().sum()).backward()
     assert all(t.grad is not None for t in (x, A, Bm, bias, res)) and W.grad is None
+
+
+def test_modules_unfused(monkeypatch):
+    """The stacked projections and the modules over them on the unfused compositions: each
+    projection with its own adapter, no gradient and no change outside their blocks."""
+    monkeypatch.setenv("LORA_LINEAR_FUSED", "0")
+    g = torch.Generator().manual_seed(4)
+
+    def bf(*s):
+        return (torch.randn(*s, generator=g) / s[-1] ** 0.5).to(torch.bfloat16)
+
+    qkv = block.LoraQKV(bf(4 * 16 + 2 * 16, 32), hq=2, hk=2, D=16, r=8, alpha=16.0, max_positions=64, rot=8)
+    mlp = block.LoraGatedMLP(bf(48, 32), bf(40, 24), r=8, alpha=16.0, act="gelu")
+    for stack in (qkv, mlp.gate_up):
+        for p in range(len(stack.d_outs)):
+            with torch.no_grad():
+                stack.B_p(p).copy_(bf(*stack.B_p(p).shape))
+    x = (4 * bf(2, 3, 32)).requires_grad_(True)
+    pos = torch.arange(3).expand(2, 3)
+    h = block.LoraProjections.forward(qkv, x)
+    W = qkv.layer.weight.double()
+    for p, (a, b) in enumerate(qkv.rows):
+        w = W[a:b] + 2.0 * qkv.B_p(p).detach().double() @ qkv.A_p(p).detach().double()
+        torch.testing.assert_close(h[..., a:b].double(), x.detach().double() @ w.t(), rtol=4e-2, atol=4e-2)
+    q, k, v = qkv(x, pos)
+    assert q.shape == (2, 3, 2, 16) and torch.equal(v, h[..., 64:].unflatten(-1, (2, 16)))
+    assert torch.equal(q[:, 0, :, 8:], block.qk_norm_rope(h[..., :32].unflatten(-1, (2, 16)), h[..., 32:64].unflatten(
+        -1, (2, 16)), qkv.q_norm, qkv.k_norm)[0][:, 0, :, 8:])
+    out = mlp(x, residual=torch.ones(2, 3, 40, dtype=torch.bfloat16))
+    assert out.shape == (2, 3, 40)
+    opt = torch.optim.SGD([t for m in (qkv, mlp) for t in m.parameters() if t.requires_grad], lr=0.1)
+    (q.float().square().sum() + k.float().sum() + v.float().sum() + out.float().sum()).backward()
+    opt.step()
+    for stack in (qkv, mlp.gate_up):
+        B, G = stack.layer.lora_B.detach().clone(), stack.layer.lora_B.grad.clone()
+        assert G.any()
+        for p, (a, b) in enumerate(stack.rows):
+            for t in (B, G):
+                t[a:b, p * 8:(p + 1) * 8] = 0
+        assert not B.any() and not G.any()
+    assert qkv.q_norm.grad is not None and mlp.down.lora_A.grad is not None and x.grad is not None
+    qkv.to(torch.float64)
+    assert qkv.cos.dtype == torch.float32
+    with pytest.raises(ValueError, match="positions"):
+        qkv(x)
+    with pytest.raises(ValueError, match="rows"):
+        block.LoraProjections(bf(48, 32), (24, 16), r=8)
+    with pytest.raises(ValueError, match="down takes"):
+        block.LoraGatedMLP(bf(48, 32), bf(40, 32))
+    with pytest.raises(ValueError, match="exact"):
+        block.LoraProjections(bf(48, 32), (16, 16, 16), r=8, alpha=16777217.0 / 16777216.0 * 3.0 + 1e-6)

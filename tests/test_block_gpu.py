@@ -4,7 +4,7 @@ token, last waves cut along K and along N, and the gradients."""
 import pytest
 import torch
 
-from block_cases import ACT_ERR, BF, F32, LIPSCHITZ, Layer, act64, assert_within
+from block_cases import ACT_ERR, BF, F32, LIPSCHITZ, Layer, act64, assert_within, frozen
 from rank_linear_lora_b200 import autograd as LA
 from rank_linear_lora_b200 import block
 from rank_linear_lora_b200 import lora_linear as L
@@ -356,3 +356,141 @@ def test_two_streams_and_two_graphs():
         torch.cuda.synchronize()
         for a, b in zip(alone, outs):
             assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+class Block(torch.nn.Module):
+    """A transformer block on the framework's operators; attention itself, and the norms of x,
+    in torch's own."""
+
+    def __init__(self, d, hq, hk, D, f, r, g, fmts):
+        super().__init__()
+        self.ws = [frozen(fmt, n, k, g) for fmt, n, k in zip(fmts, ((hq + 2 * hk) * D, d, 2 * f, d), (d, hq * D, d, f))]
+        W = [w[0] for w in self.ws]
+        self.hq, self.hk, self.D, self.f = hq, hk, D, f
+        self.qkv = block.LoraQKV(W[0], hq, hk, D, r, 2.0 * r, max_positions=128, rot=D // 2, theta=500.0)
+        self.o = block._layer(W[1], r, 2.0 * r)
+        self.mlp = block.LoraGatedMLP(W[2], W[3], r, 2.0 * r)
+        with torch.no_grad():
+            for B in (*(s.B_p(p) for s in (self.qkv, self.mlp.gate_up) for p in range(len(s.d_outs))), self.o.lora_B,
+                      self.mlp.down.lora_B):
+                B.copy_(torch.randn(B.shape, generator=g) * 0.3 / r ** 0.5)
+            for w in (self.qkv.q_norm, self.qkv.k_norm):
+                w.copy_(1 + 0.1 * torch.randn(D, generator=g))
+
+    def attend(self, q, k, v, cast):
+        k, v = (t.repeat_interleave(self.hq // self.hk, dim=2) for t in (k, v))
+        s = torch.einsum("bihd,bjhd->bhij", cast(q), cast(k)) * self.D ** -0.5
+        T = s.shape[-1]
+        s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=s.device).triu(1), float("-inf"))
+        return torch.einsum("bhij,bjhd->bihd", s.softmax(-1), cast(v)).flatten(2)
+
+    def forward(self, x, pos):
+        y = self.attend(*self.qkv(x, pos), torch.Tensor.float).to(torch.bfloat16)
+        x = block.lora_linear_act(y, self.o._frozen(), self.o.lora_A, self.o.lora_B, self.o.alpha, residual=x)
+        return self.mlp(x, residual=x)
+
+    def trained(self):
+        return {n: t for n, t in self.named_parameters() if t.requires_grad}
+
+    def reference(self, x, pos):
+        """(the leaves in 64 bits, the output)."""
+        leaf = {n: t.detach().double().requires_grad_(True) for n, t in self.trained().items()}
+        x64 = x.detach().double().requires_grad_(True)
+
+        def lin(t, i, name):
+            A, B = leaf[name + ".lora_A"], leaf[name + ".lora_B"]
+            stack = {0: self.qkv, 2: self.mlp.gate_up}.get(i)
+            if stack is not None:
+                own = torch.zeros_like(B)
+                for p, (a, b) in enumerate(stack.rows):
+                    own[a:b, p * stack.r:(p + 1) * stack.r] = 1
+                B = B * own
+            return t @ self.ws[i][1].t() + 2.0 * (t @ A.t()) @ B.t()
+
+        h = lin(x64, 0, "qkv.layer")
+        c, s = (t.double()[pos][:, :, None] for t in (self.qkv.cos, self.qkv.sin))
+
+        def heads(t, w):
+            t = t / (t.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w
+            n = c.shape[-1]
+            a, b = t[..., :n], t[..., n:2 * n]
+            return torch.cat((a * c - b * s, b * c + a * s, t[..., 2 * n:]), -1)
+
+        q, k, v = (t.unflatten(-1, (-1, self.D)) for t in h.split([e - b for b, e in self.qkv.rows], -1))
+        y = self.attend(heads(q, leaf["qkv.q_norm"]), heads(k, leaf["qkv.k_norm"]), v, torch.Tensor.double)
+        x1 = x64 + lin(y, 1, "o")
+        gate, up = lin(x1, 2, "mlp.gate_up.layer").chunk(2, -1)
+        return {"x": x64, **leaf}, x1 + lin(torch.nn.functional.silu(gate) * up, 3, "mlp.down")
+
+
+@pytest.mark.parametrize("fmts", [("bf16",) * 4, ("nf4", "bf16", "q4", "fp8")], ids=["bf16", "coded"])
+@pytest.mark.parametrize("T", [1, 37, 128])
+def test_a_block_of_them_together(T, fmts):
+    """Projections, norms with rotation, projection with residual, gated MLP: outputs and the
+    gradients of x and every parameter, against autograd in 64 bits.  Some forty roundings to
+    bf16 lie between x and a gradient (two of each operator's operands and one of its result,
+    there and back), each of 2^-8 / sqrt(3) of a tensor's norm at most and independent:
+    sqrt(40 / 3) 2^-8 = 1.4e-2 together, which the block (whose factors are of order one)
+    may double."""
+    g = torch.Generator().manual_seed(T)
+    m = Block(256, 4, 2, 64, 320, 8, g, fmts)
+    x = torch.randn(2, T, 256, generator=g).to(torch.bfloat16).cuda().requires_grad_(True)
+    dout = torch.randn(2, T, 256, generator=g).to(torch.bfloat16).cuda()
+    pos = torch.stack((torch.arange(T), torch.randint(0, 128, (T,), generator=g))).cuda()
+    out = m(x, pos)
+    names, leaves = zip(("x", x), *m.trained().items())
+    grads = torch.autograd.grad(out, leaves, dout)
+    leaf, want = m.reference(x, pos)
+    gref = torch.autograd.grad(want, [leaf[n] for n in names], dout.double())
+    def rel(a, b):
+        return ((a.double() - b).norm() / b.norm()).item()
+    assert rel(out, want.detach()) <= 3e-2
+    for n, a, b in zip(names, grads, gref):
+        if T == 1 and ("q_norm" in n or "k_norm" in n):
+            assert a.float().abs().max() <= 1e-2  # one key: a softmax over one score has no gradient
+        else:
+            assert rel(a, b) <= 3e-2, n
+    with torch.no_grad():  # the forward without autograd: nothing saved, the same bits
+        assert torch.equal(m(x, pos), out)
+
+
+def test_a_captured_step_of_the_block():
+    """Forward, backward and a plain SGD step in one graph: replays give what eager steps give."""
+    def model():
+        torch.manual_seed(1)  # lora_A is drawn from the default generator
+        return Block(256, 4, 2, 64, 320, 8, torch.Generator().manual_seed(3), ("bf16", "q4", "fp8", "bf16"))
+
+    g = torch.Generator().manual_seed(5)
+    xs = [torch.randn(1, 24, 256, generator=g).to(torch.bfloat16).cuda() for _ in range(3)]
+    pos = torch.arange(24, device="cuda")[None]
+
+    def step(m, x):
+        out = m(x, pos)
+        leaves = list(m.trained().values())
+        grads = torch.autograd.grad(out.float().square().mean(), leaves)
+        with torch.no_grad():
+            for t, d in zip(leaves, grads):
+                t.sub_(d, alpha=2.0 ** -6)
+        return out.detach()
+
+    eager = model()
+    want = [step(eager, x) for x in xs]
+    m, x = model(), torch.zeros_like(xs[0])
+    keep = [t.detach().clone() for t in m.trained().values()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(m, x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(m, x)
+    with torch.no_grad():
+        for t, k in zip(m.trained().values(), keep):
+            t.copy_(k)
+    for xi, w in zip(xs, want):
+        x.copy_(xi)
+        graph.replay()
+        assert torch.equal(out, w)
+    for a, b in zip(m.trained().values(), eager.trained().values()):
+        assert torch.equal(a, b)
