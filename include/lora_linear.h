@@ -476,8 +476,8 @@ LORA_API lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t 
  * along K.  Pure host function. */
 LORA_API size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r);
 
-/* Element types of the head operators' tensors. */
-typedef enum { LORA_T_BF16 = 0, LORA_T_FP16 = 1, LORA_T_FP32 = 2 } lora_dtype_t;
+/* Element types of the head operators' tensors; LORA_T_WEIGHT_GRADS is or-ed to one of them. */
+typedef enum { LORA_T_BF16 = 0, LORA_T_FP16 = 1, LORA_T_FP32 = 2, LORA_T_WEIGHT_GRADS = 0x100 } lora_dtype_t;
 
 /* A [M, heads, D] tensor: element (m, h, j) at data[m * token_stride + h * head_stride + j]
  * (strides in elements, D contiguous), e.g. a column range of the stacked projection. */
@@ -519,7 +519,8 @@ LORA_API lora_status_t lora_qk_norm_rope_fwd(int dtype, const lora_heads_t *q, c
  * dv = i (dn weight - e mean_j(e dn weight)).
  *   dq_out, dk_out  gradients of the outputs (NULL exactly where q, k are).
  *   dq, dk          outputs; each may be its dq_out / dk_out, in place.
- *   dq_weight, dk_weight  outputs [D] (fp32), or NULL.
+ *   dq_weight, dk_weight  outputs [D] (fp32; with dtype | LORA_T_WEIGHT_GRADS of dtype itself,
+ *                  rounded once from the fp32 sums), or NULL.
  * A token whose position is outside the table makes its dq, dk and the weights' gradients
  * NaN.  Sums run in a fixed order for given sizes: the same call gives the same bits.
  * Workspace: lora_qk_norm_rope_workspace_size(M, heads of q + heads of k, D) bytes, 256-byte aligned
@@ -529,7 +530,7 @@ LORA_API lora_status_t lora_qk_norm_rope_bwd(int dtype, const lora_heads_t *dq_o
                                              const lora_heads_t *q, const lora_heads_t *k, const void *q_weight,
                                              const void *k_weight, const float *cos, const float *sin,
                                              const int64_t *positions, int64_t n_pos, const lora_heads_t *dq,
-                                             const lora_heads_t *dk, float *dq_weight, float *dk_weight, int64_t M,
+                                             const lora_heads_t *dk, void *dq_weight, void *dk_weight, int64_t M,
                                              int D, int rot, int interleaved, int norm, float eps, void *workspace,
                                              size_t workspace_bytes, void *stream);
 

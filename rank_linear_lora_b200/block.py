@@ -40,13 +40,16 @@ _WS_KEPT = 64  # workspaces kept (the least recently used goes first)
 
 def _workspace(size_fn, op: int, M: int, d_in: int, d_out: int, r: int, device) -> torch.Tensor:
     """A zeroed workspace of size_fn(op, ...) bytes for the current stream."""
-    n = size_fn(op, M, d_in, d_out, r)
-    if n == 0:
-        raise ValueError(f"invalid sizes: {M} tokens, {d_in} -> {d_out}, rank {r}")
-    if torch.cuda.is_current_stream_capturing():
+    def new():
+        n = size_fn(op, M, d_in, d_out, r)
+        if n == 0:
+            raise ValueError(f"invalid sizes: {M} tokens, {d_in} -> {d_out}, rank {r}")
         return torch.zeros(n, dtype=torch.uint8, device=device)
-    # the size depends on the plan of the shape, and so does the layout: a new plan, a new workspace
-    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index), op, M, d_in, d_out, r, n, L.plan_epoch)
+
+    if torch.cuda.is_current_stream_capturing():
+        return new()
+    # size and layout depend on the plan of the shape: a new plan, a new workspace
+    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index), size_fn, op, M, d_in, d_out, r, L.plan_epoch)
     with _ws_lock:
         ws = _ws_cache.get(key)
         if ws is None:
@@ -54,7 +57,7 @@ def _workspace(size_fn, op: int, M: int, d_in: int, d_out: int, r: int, device) 
             # stream order behind the kernels that still use them
             while len(_ws_cache) >= _WS_KEPT:
                 _ws_cache.popitem(last=False)
-            ws = _ws_cache[key] = torch.zeros(n, dtype=torch.uint8, device=device)
+            ws = _ws_cache[key] = new()
         else:
             _ws_cache.move_to_end(key)
         return ws
@@ -98,25 +101,9 @@ def _rows(x):
     return x2 if x2.is_contiguous() else x2.contiguous()
 
 
-def _grad_buffers(*params):
-    """fp32 gradients of `params` (None for None) next to each other, and a function that gives
-    them in the parameters' types: one cast where those are the same."""
-    dtype = {t.dtype for t in params if t is not None}
-    sizes = [0 if t is None else t.numel() for t in params]
-    dev = next((t.device for t in params if t is not None), None)
-    flat = torch.empty(sum(sizes), dtype=torch.float32, device=dev) if dtype else None
-
-    def parts(buf):
-        return [None if t is None else v.view(t.shape) for t, v in zip(params, buf.split(sizes))] if dtype else list(params)
-
-    grads = parts(flat)
-
-    def typed():
-        if len(dtype) == 1:
-            return parts(flat.to(*dtype))
-        return [None if t is None else g.to(t.dtype) for t, g in zip(params, grads)]
-
-    return grads, typed
+def _fp32(t):
+    """An fp32 gradient of t."""
+    return torch.empty_like(t, dtype=torch.float32)
 
 
 # ------------------------------------------------------------------ gated projections
@@ -150,11 +137,11 @@ class LoraGluFunction(torch.autograd.Function):
         dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
         if M == 0:
             return dX, torch.zeros_like(A), torch.zeros_like(B), None, None, None
-        (dA, dB), typed = _grad_buffers(A, B)
+        dA, dB = _fp32(A), _fp32(B)
         dGU = torch.empty_like(gu)
         ws = _workspace(L.lora_linear_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_glu_bwd(dP.contiguous(), gu, x, wt, A, B, xa, dGU, dX, dA, dB, ctx.alpha, ctx.act, ws)
-        return dX, *typed(), None, None, None
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None
 
 
 def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
@@ -220,11 +207,12 @@ class LoraLinearActFunction(torch.autograd.Function):
             dbias = None if bias is None else torch.zeros_like(bias)
             return dX, torch.zeros_like(A), torch.zeros_like(B), dbias, dres, None, None, None
         dOut = dOut.contiguous()
-        (dA, dB, dbias), typed = _grad_buffers(A, B, bias)
+        dA, dB, dbias = _fp32(A), _fp32(B), None if bias is None else _fp32(bias)
         dPre = torch.empty_like(dOut) if ctx.act != "none" else None
         ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
         L.lora_linear_act_bwd(dOut, pre, x, wt, A, B, xa, dPre, dX, dA, dB, dbias, ctx.alpha, ctx.act, ws)
-        return dX, *typed(), dres, None, None, None
+        return (dX, dA.to(A.dtype), dB.to(B.dtype), None if bias is None else dbias.to(bias.dtype), dres, None, None,
+                None)
 
 
 def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str = "none"):
@@ -280,8 +268,7 @@ def _addressable(t):
 
 def _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
     """New (q_out, k_out) from the library, contiguous."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)  # contiguous, whatever q's and k's strides
     if q.shape[0] > 0:
         L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
     return q_out, k_out
@@ -290,16 +277,15 @@ def _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleav
 def _heads_backward(grads, ins, weights, tables, outs, needs, eps, interleaved, norm):
     """The library's backward into `outs`; the gradients of those of the weights that need one."""
     M, hq, D = ins[0].shape
-    trained = [w if n else None for w, n in zip(weights, needs)]
+    dw = [(torch.empty_like if M else torch.zeros_like)(w) if n and w is not None else None for w, n in zip(weights, needs)]
     if M == 0:
-        return [None if w is None else torch.zeros_like(w) for w in trained]
-    dw, typed = _grad_buffers(*trained)
+        return dw
     ws = None
-    if any(t is not None for t in dw):
+    if dw[0] is not None or dw[1] is not None:
         n = L.lora_qk_norm_rope_workspace_size(M, hq + ins[1].shape[1], D)
         ws = torch.empty(n, dtype=torch.uint8, device=ins[0].device)
     L.lora_qk_norm_rope_bwd(*grads, *ins, *weights, *tables, *outs, *dw, ws, eps, interleaved, norm)
-    return typed()
+    return dw
 
 
 class QkNormRopeFunction(torch.autograd.Function):
@@ -316,7 +302,7 @@ class QkNormRopeFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
-        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
         dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
                              (dq, dk), ctx.needs_input_grad[2:4], *ctx.rest)
         return dq, dk, *dw, None, None, None, None, None, None

@@ -538,13 +538,14 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
     }
 }
 
-// dw[j] = the sum of the CTAs' partials: 32 columns x 32 row lanes a CTA (y: q or k).
-__global__ void __launch_bounds__(1024) k_heads_dw(const float *partials, float *dwq, float *dwk, int q_ctas, int k_ctas,
-                                                   int D) {
+// dw[j] = the sum of the CTAs' partials, rounded once to T: 32 columns x 32 row lanes a CTA (y:
+// q or k).
+template <class T>
+__global__ void __launch_bounds__(1024) k_heads_dw(const float *partials, T *dwq, T *dwk, int q_ctas, int k_ctas, int D) {
     __shared__ float red[32][33];
     grid_dep_wait();
     grid_dep_launch_dependents();
-    float *dst = blockIdx.y ? dwk : dwq;
+    T *dst = blockIdx.y ? dwk : dwq;
     if (!dst) return;
     const int n = blockIdx.y ? k_ctas : q_ctas;
     const float *src = partials + (blockIdx.y ? static_cast<int64_t>(q_ctas) * D : 0);
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(1024) k_heads_dw(const float *partials, float 
         v = 0.0f;
 #pragma unroll
         for (int r = 0; r < 32; ++r) v += red[r][threadIdx.x];
-        dst[col] = v;
+        dst[col] = T(v);
     }
 }
 
@@ -602,12 +603,14 @@ bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 // A tensor's checks: 0 or a status.
 lora_status_t check_heads(const lora_heads_t *t, int heads, int esize, int vec_bytes, int64_t M, int D) {
     if (!t->data || t->heads < 1 || t->heads > 4096 || t->heads != heads) return LORA_ERR_INVALID_ARG;
-    const int64_t most = int64_t(1) << 40;  // keeps every offset far inside 63 bits
+    const int64_t most = int64_t(1) << 40;
     if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride > most || t->head_stride > most)
         return LORA_ERR_INVALID_ARG;
     // no element twice: tokens outside heads, or heads outside tokens
-    const bool tokens_outside = M == 1 || t->token_stride >= (heads - 1) * t->head_stride + D;
-    const bool heads_outside = heads == 1 || t->head_stride >= (M - 1) * t->token_stride + D;
+    const __int128 over_tokens = __int128(M - 1) * t->token_stride + D, over_heads = __int128(heads - 1) * t->head_stride + D;
+    if (over_tokens + over_heads > (__int128(1) << 58)) return LORA_ERR_INVALID_ARG;  // bytes in 63 bits
+    const bool tokens_outside = M == 1 || t->token_stride >= over_heads;
+    const bool heads_outside = heads == 1 || t->head_stride >= over_tokens;
     if ((M > 1 && t->token_stride < D) || (heads > 1 && t->head_stride < D) || (!tokens_outside && !heads_outside))
         return LORA_ERR_INVALID_ARG;
     if (!aligned(t->data, 16) || (t->token_stride * esize) % vec_bytes || (t->head_stride * esize) % vec_bytes)
@@ -648,10 +651,17 @@ cudaError_t launch_type(const HeadArgs &a, const HeadShape &s, bool inter, bool 
     return s.ns ? launch<T, 4, false, 2>(a, bwd, st) : launch<T, 4, false, 0>(a, bwd, st);
 }
 
+template <class T>
+cudaError_t launch_dw(const HeadArgs &a, void *const dw[2], cudaStream_t st) {
+    return lora_host::launch_pdl(k_heads_dw<T>, dim3((a.D + 31) / 32, 2), dim3(32, 32), 0, st,
+                                 static_cast<const float *>(a.partials), static_cast<T *>(dw[0]), static_cast<T *>(dw[1]),
+                                 a.t[0].ctas, a.t[1].ctas, a.D);
+}
+
 // Both directions: dy null for the forward.
 lora_status_t run(int dtype, const lora_heads_t *const in[2], const lora_heads_t *const dy[2],
                   const lora_heads_t *const out[2], const void *const weight[2], const float *cos, const float *sin,
-                  const int64_t *positions, int64_t n_pos, float *const dw[2], int64_t M, int D, int rot,
+                  const int64_t *positions, int64_t n_pos, void *const dw[2], bool dw_typed, int64_t M, int D, int rot,
                   int interleaved, int norm, float eps, bool bwd, void *ws, size_t ws_bytes, void *stream) {
     if (dtype < LORA_T_BF16 || dtype > LORA_T_FP32) return LORA_ERR_INVALID_ARG;
     if (M < 1 || M > (int64_t(1) << 30) || D < 8 || D > 256 || D % 8 || rot < 0 || rot > D || rot % 8)
@@ -726,9 +736,11 @@ lora_status_t run(int dtype, const lora_heads_t *const in[2], const lora_heads_t
         case LORA_T_FP16: e = launch_type<__half>(a, shape, interleaved != 0, bwd, st); break;
         default: e = launch_type<float>(a, shape, interleaved != 0, bwd, st); break;
     }
-    if (e == cudaSuccess && want_dw)
-        e = lora_host::launch_pdl(k_heads_dw, dim3((D + 31) / 32, 2), dim3(32, 32), 0, st, a.partials, dw[0], dw[1],
-                                  a.t[0].ctas, a.t[1].ctas, D);
+    if (e == cudaSuccess && want_dw) {
+        if (!dw_typed || dtype == LORA_T_FP32) e = launch_dw<float>(a, dw, st);
+        else if (dtype == LORA_T_BF16) e = launch_dw<__nv_bfloat16>(a, dw, st);
+        else e = launch_dw<__half>(a, dw, st);
+    }
     return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
@@ -742,21 +754,23 @@ lora_status_t lora_qk_norm_rope_fwd(int dtype, const lora_heads_t *q, const lora
                                     int D, int rot, int interleaved, int norm, float eps, void *stream) {
     const lora_heads_t *in[2] = {q, k}, *none[2] = {nullptr, nullptr}, *out[2] = {q_out, k_out};
     const void *w[2] = {q_weight, k_weight};
-    float *dw[2] = {nullptr, nullptr};
-    return run(dtype, in, none, out, w, cos, sin, positions, n_pos, dw, M, D, rot, interleaved, norm, eps, false,
+    void *dw[2] = {nullptr, nullptr};
+    return run(dtype, in, none, out, w, cos, sin, positions, n_pos, dw, false, M, D, rot, interleaved, norm, eps, false,
                nullptr, 0, stream);
 }
 
 lora_status_t lora_qk_norm_rope_bwd(int dtype, const lora_heads_t *dq_out, const lora_heads_t *dk_out,
                                     const lora_heads_t *q, const lora_heads_t *k, const void *q_weight,
                                     const void *k_weight, const float *cos, const float *sin, const int64_t *positions,
-                                    int64_t n_pos, const lora_heads_t *dq, const lora_heads_t *dk, float *dq_weight,
-                                    float *dk_weight, int64_t M, int D, int rot, int interleaved, int norm, float eps,
+                                    int64_t n_pos, const lora_heads_t *dq, const lora_heads_t *dk, void *dq_weight,
+                                    void *dk_weight, int64_t M, int D, int rot, int interleaved, int norm, float eps,
                                     void *workspace, size_t workspace_bytes, void *stream) {
     const lora_heads_t *in[2] = {q, k}, *dy[2] = {dq_out, dk_out}, *out[2] = {dq, dk};
     const void *w[2] = {q_weight, k_weight};
-    float *dw[2] = {dq_weight, dk_weight};
-    return run(dtype, in, dy, out, w, cos, sin, positions, n_pos, dw, M, D, rot, interleaved, norm, eps, true, workspace,
+    void *dw[2] = {dq_weight, dk_weight};
+    const bool typed = (dtype & LORA_T_WEIGHT_GRADS) != 0;
+    dtype &= ~static_cast<int>(LORA_T_WEIGHT_GRADS);
+    return run(dtype, in, dy, out, w, cos, sin, positions, n_pos, dw, typed, M, D, rot, interleaved, norm, eps, true, workspace,
                workspace_bytes, stream);
 }
 

@@ -25,6 +25,7 @@ OP_FWD, OP_BWD, OP_FWD_Q4, OP_BWD_Q4, OP_FWD_FP8, OP_BWD_FP8, OP_FWD_NF4, OP_BWD
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # lora_act_t
 WEIGHT_FORMATS = {"bf16": 0, "q4": 1, "fp8": 2, "nf4": 3}                    # lora_weight_format_t
 HEAD_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}        # lora_dtype_t
+WEIGHT_GRADS = 0x100  # LORA_T_WEIGHT_GRADS
 KERNEL_KINDS = ["xa", "fwd_main", "g", "dx_main", "dadb"]
 
 
@@ -116,8 +117,9 @@ def _ws(ws):
     """(pointer, bytes) of a workspace tensor: contiguous, on the current device."""
     if ws is None or not ws.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor")
-    _on_current_device(ws, "workspace")
-    return _ptr(ws), ws.numel() * ws.element_size()
+    if ws.get_device() != torch.cuda.current_device():
+        _on_current_device(ws, "workspace")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _check(status: int, where: str):
@@ -727,16 +729,18 @@ def lora_qk_norm_rope_workspace_size(M: int, heads: int, D: int) -> int:
 
 def lora_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, dq, dk, dq_weight, dk_weight,
                           ws, eps=1e-6, interleaved=False, norm=True, stream=None):
-    """dq, dk (each may be its dq_out / dk_out, in place) and the fp32 weight gradients [D] (or
-    None) from the forward's inputs.  ws: lora_qk_norm_rope_workspace_size bytes, or None where
+    """dq, dk (each may be its dq_out / dk_out, in place) and the weight gradients [D] (or None;
+    fp32, or rounded to q's and k's type) from the forward's inputs.  ws: lora_qk_norm_rope_workspace_size bytes, or None where
     neither weight gradient is asked for."""
     dev = torch.cuda.current_device()
     M, D, dtype, rot, n_pos = _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev)
     qs, ks = None if q is None else q.shape, None if k is None else k.shape
-    _need(dev, torch.float32, (dq_weight, "dq_weight", (D,)), (dk_weight, "dk_weight", (D,)))
+    one = dq_weight if dq_weight is not None else dk_weight
+    typed = one is not None and one.dtype is dtype
+    _need(dev, dtype if typed else torch.float32, (dq_weight, "dq_weight", (D,)), (dk_weight, "dk_weight", (D,)))
     wp, wn = (None, 0) if ws is None else _ws(ws)
     st = load_library().lora_qk_norm_rope_bwd(
-        HEAD_DTYPES[dtype], _heads(dq_out, "dq_out", qs, dtype, dev), _heads(dk_out, "dk_out", ks, dtype, dev),
+        HEAD_DTYPES[dtype] | (WEIGHT_GRADS if typed else 0), _heads(dq_out, "dq_out", qs, dtype, dev), _heads(dk_out, "dk_out", ks, dtype, dev),
         _heads(q, "q", qs, dtype, dev), _heads(k, "k", ks, dtype, dev), _addr(q_weight), _addr(k_weight), _addr(cos),
         _addr(sin), _addr(positions), n_pos, _heads(dq, "dq", qs, dtype, dev), _heads(dk, "dk", ks, dtype, dev),
         _addr(dq_weight), _addr(dk_weight), M, D, rot, interleaved, norm, float(eps), wp, wn, _raw_stream(stream, dev))

@@ -257,3 +257,17 @@ def test_modules_unfused(monkeypatch):
         block.LoraGatedMLP(bf(48, 32), bf(40, 32))
     with pytest.raises(ValueError, match="exact"):
         block.LoraProjections(bf(48, 32), (16, 16, 16), r=8, alpha=16777217.0 / 16777216.0 * 3.0 + 1e-6)
+
+
+def test_head_strides_beyond_any_memory(lib):
+    """Offsets that would pass 63 bits are refused, not wrapped around."""
+    far = 1 << 40
+
+    def fwd(q, qo, M):
+        return lib.lora_qk_norm_rope_fwd(0, q, None, None, None, P(0x2000), P(0x3000), P(0x4000), 16, qo, None, M, 128, 128, 0, 1,
+                                         1e-6, None)
+
+    for M in (1 << 30, (1 << 23) + 1, 1 << 24):
+        for hs in (128, far):
+            assert fwd(_h(ts=far, hs=hs), _h(0x5000), M) == 1
+            assert fwd(_h(), _h(0x5000, ts=far, hs=hs), M) == 1

@@ -170,6 +170,25 @@ def test_in_place_and_other_strides():
     _check("dq in place", dy, *want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_weight_gradients_of_the_tensors_type(dtype):
+    """The fp32 sums rounded once, by the library: the bits that a cast of its fp32 outputs gives."""
+    g = torch.Generator().manual_seed(12)
+    q, k, dq, dk = (torch.randn(77, h, 48, generator=g).to(dtype).cuda() for h in (5, 2, 5, 2))
+    w = (1 + 0.1 * torch.randn(48, generator=g)).to(dtype).cuda()
+    ws = torch.empty(L.lora_qk_norm_rope_workspace_size(77, 7, 48), dtype=torch.uint8, device="cuda")
+    outs = []
+    for t in (torch.float32, dtype):
+        dw = [torch.full((48,), 9.0, dtype=t, device="cuda") for _ in range(2)]
+        L.lora_qk_norm_rope_bwd(dq, dk, q, k, w, w, None, None, None, torch.empty_like(q), torch.empty_like(k), *dw, ws, EPS)
+        outs.append(dw)
+    for a, b in zip(*outs):
+        assert b.dtype is dtype and torch.equal(a.to(dtype), b)
+    with pytest.raises(ValueError, match="dk_weight"):
+        L.lora_qk_norm_rope_bwd(dq, dk, q, k, w, w, None, None, None, torch.empty_like(q), torch.empty_like(k), w.clone(),
+                                torch.empty(48, dtype=torch.float64, device="cuda"), ws, EPS)
+
+
 def test_positions_outside_the_table():
     """They read no table row: the token's rotated dimensions are NaN, all else is right."""
     _, q, k, wq, wk, cos, sin, pos, c64, s64 = _inputs(20, 3, 2, 64, 32, torch.bfloat16)
