@@ -137,6 +137,10 @@ typedef struct {
  * most 256 shapes hold a plan); takes effect for calls made after it returns. */
 LORA_API lora_status_t lora_linear_set_plan(int64_t M, int64_t d_in, int64_t d_out, int r, const lora_plan_t *plan);
 
+/* Plans installed or removed so far.  A workspace's layout follows the plan: one that was
+ * zeroed under an earlier count is not used again for a shape whose plan changed. */
+LORA_API uint64_t lora_linear_plan_epoch(void);
+
 /* The plan `op` uses for this shape: the override's fields and the library's choice for
  * the rest, filled in for the kernels the plan runs (fields of kernels it does not run,
  * e.g. the split-K splits when the side kernels take the products, are 0).  Host-only;

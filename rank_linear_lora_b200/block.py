@@ -22,8 +22,6 @@ its forward).
 """
 from __future__ import annotations
 
-import collections
-import threading
 import warnings
 
 import torch
@@ -33,38 +31,32 @@ from . import autograd as LA
 from . import lora_linear as L
 from .multi import _exact_f32_product
 
-_ws_lock = threading.Lock()
-_ws_cache: collections.OrderedDict = collections.OrderedDict()
-_WS_KEPT = 64  # workspaces kept (the least recently used goes first)
+_native = None
 
 
-def _workspace(size_fn, op: int, M: int, d_in: int, d_out: int, r: int, device) -> torch.Tensor:
-    """A zeroed workspace of size_fn(op, ...) bytes for the current stream."""
-    def new():
-        n = size_fn(op, M, d_in, d_out, r)
-        if n == 0:
-            raise ValueError(f"invalid sizes: {M} tokens, {d_in} -> {d_out}, rank {r}")
-        return torch.zeros(n, dtype=torch.uint8, device=device)
-
-    if torch.cuda.is_current_stream_capturing():
-        return new()
-    # size and layout depend on the plan of the shape: a new plan, a new workspace
-    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index), size_fn, op, M, d_in, d_out, r, L.plan_epoch)
-    with _ws_lock:
-        ws = _ws_cache.get(key)
-        if ws is None:
-            # evicted workspaces go back to their stream's pool of the caching allocator, in
-            # stream order behind the kernels that still use them
-            while len(_ws_cache) >= _WS_KEPT:
-                _ws_cache.popitem(last=False)
-            ws = _ws_cache[key] = new()
-        else:
-            _ws_cache.move_to_end(key)
-        return ws
+def _ops():
+    """The native side of the operators (csrc/torch_ops.cpp): checks, workspaces, autograd."""
+    global _native
+    if _native is None:
+        L.load_library()  # raises, with what to do, if nothing was built
+        try:
+            from . import _ops as native
+        except ImportError as e:
+            raise RuntimeError("the operators' native module is not built or does not load (run "
+                               f"rank_linear_lora_b200/build.py): {e}") from e
+        _native = native
+    return _native
 
 
 def _frozen(W) -> LA.FrozenWeight:
     return W if isinstance(W, LA.FrozenWeight) else LA.FrozenWeight("bf16", (W,))
+
+
+def _operands(wt):
+    """A FrozenWeight as the native operators take it."""
+    t, kind = wt.tensors, wt.kind
+    return (L.WEIGHT_FORMATS[kind], t[0], t[1] if len(t) > 1 else None,
+            L._codebook(wt.codebook)[0].tolist() if kind == "nf4" else ())
 
 
 def _declined(e=None):
@@ -101,49 +93,7 @@ def _rows(x):
     return x2 if x2.is_contiguous() else x2.contiguous()
 
 
-def _fp32(t):
-    """An fp32 gradient of t."""
-    return torch.empty_like(t, dtype=torch.float32)
-
-
 # ------------------------------------------------------------------ gated projections
-def _glu_forward(x, A, B, alpha, wt, act, save):
-    M, r, n = x.shape[0], A.shape[0], wt.d_out
-    p = torch.empty(M, n // 2, dtype=torch.bfloat16, device=x.device)
-    gu = torch.empty(M, n, dtype=torch.bfloat16, device=x.device) if save else None
-    xa = torch.empty(M, r, dtype=torch.bfloat16, device=x.device) if save else None
-    if M > 0:
-        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
-        L.lora_glu_fwd(x, wt, A, B, p, gu, xa, alpha, act, ws)
-    return p, gu, xa
-
-
-class LoraGluFunction(torch.autograd.Function):
-    """p = act(g) * u, [g | u] = x.w^T + (alpha / r).(x.A^T).B^T; x [M, d_in] bf16."""
-
-    @staticmethod
-    def forward(ctx, x, A, B, alpha, wt, act):
-        p, gu, xa = _glu_forward(x, A, B, alpha, wt, act, save=True)
-        ctx.save_for_backward(x, A, B, xa, gu, *wt.tensors)
-        ctx.alpha, ctx.wt, ctx.act = alpha, wt, act
-        return p
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dP):
-        x, A, B, xa, gu = ctx.saved_tensors[:5]
-        wt = ctx.wt
-        M, r, n = x.shape[0], A.shape[0], wt.d_out
-        dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
-        if M == 0:
-            return dX, torch.zeros_like(A), torch.zeros_like(B), None, None, None
-        dA, dB = _fp32(A), _fp32(B)
-        dGU = torch.empty_like(gu)
-        ws = _workspace(L.lora_linear_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
-        L.lora_glu_bwd(dP.contiguous(), gu, x, wt, A, B, xa, dGU, dX, dA, dB, ctx.alpha, ctx.act, ws)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None
-
-
 def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
     """act(g) * u for [g | u] = x.W^T + (alpha / r).(x.A^T).B^T, x [..., d_in] bf16.
 
@@ -152,15 +102,12 @@ def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
     multi.SharedInputProjections lays them out (rank P r and P alpha for the call, B
     block-diagonal).  act: one of L.ACTIVATIONS."""
     wt = _frozen(W)
-    L._act(act)
+    code = L._act(act)
     x2 = _rows(x)
     p = None
     if LA.fused_enabled():
         try:
-            if _grad_wanted(x2, A, B):
-                p = LoraGluFunction.apply(x2, A, B, alpha, wt, act)
-            else:
-                p = _glu_forward(x2, A, B, alpha, wt, act, save=False)[0]
+            p = _ops().glu(x2, A, B, alpha, code, *_operands(wt))
         except L.LoraError as e:
             _declined(e)
     else:
@@ -172,55 +119,12 @@ def lora_glu(x, W, A, B, alpha: float, act: str = "silu"):
 
 
 # ------------------------------------------------------------------ projection with an epilogue
-def _act_forward(x, A, B, bias, residual, alpha, wt, act, save):
-    M, r, n = x.shape[0], A.shape[0], wt.d_out
-    out = torch.empty(M, n, dtype=torch.bfloat16, device=x.device)
-    pre = torch.empty_like(out) if save and act != "none" else None
-    xa = torch.empty(M, r, dtype=torch.bfloat16, device=x.device) if save else None
-    if M > 0:
-        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[0], M, wt.d_in, n, r, x.device)
-        L.lora_linear_act_fwd(x, wt, A, B, bias, residual, out, pre, xa, alpha, act, ws)
-    return out, pre, xa
-
-
-class LoraLinearActFunction(torch.autograd.Function):
-    """out = act(x.w^T + (alpha / r).(x.A^T).B^T + bias) + residual; x [M, d_in] bf16."""
-
-    @staticmethod
-    def forward(ctx, x, A, B, bias, residual, alpha, wt, act):
-        out, pre, xa = _act_forward(x, A, B, bias, residual, alpha, wt, act, save=True)
-        ctx.save_for_backward(x, A, B, xa, pre, bias, *wt.tensors)
-        ctx.alpha, ctx.wt, ctx.act = alpha, wt, act
-        return out
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dOut):
-        x, A, B, xa, pre, bias = ctx.saved_tensors[:6]
-        wt = ctx.wt
-        M, r, n = x.shape[0], A.shape[0], wt.d_out
-        dX = torch.empty_like(x) if ctx.needs_input_grad[0] else None
-        dres = dOut if ctx.needs_input_grad[4] else None
-        if not ctx.needs_input_grad[3]:
-            bias = None
-        if M == 0:
-            dbias = None if bias is None else torch.zeros_like(bias)
-            return dX, torch.zeros_like(A), torch.zeros_like(B), dbias, dres, None, None, None
-        dOut = dOut.contiguous()
-        dA, dB, dbias = _fp32(A), _fp32(B), None if bias is None else _fp32(bias)
-        dPre = torch.empty_like(dOut) if ctx.act != "none" else None
-        ws = _workspace(L.lora_linear_act_workspace_size, wt.ops()[1], M, wt.d_in, n, r, x.device)
-        L.lora_linear_act_bwd(dOut, pre, x, wt, A, B, xa, dPre, dX, dA, dB, dbias, ctx.alpha, ctx.act, ws)
-        return (dX, dA.to(A.dtype), dB.to(B.dtype), None if bias is None else dbias.to(bias.dtype), dres, None, None,
-                None)
-
-
 def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str = "none"):
     """act(x.W^T + (alpha / r).(x.A^T).B^T + bias) + residual, x [..., d_in] bf16, residual
     [..., d_out], bias [d_out] (bf16), each optional.  W: a bf16 tensor [d_out, d_in] or a
     FrozenWeight.  act: one of L.ACTIVATIONS."""
     wt = _frozen(W)
-    L._act(act)
+    code = L._act(act)
     x2, res2 = _rows(x), residual
     if residual is not None:
         if residual.shape != (*x.shape[:-1], wt.d_out):
@@ -229,10 +133,7 @@ def lora_linear_act(x, W, A, B, alpha: float, bias=None, residual=None, act: str
     out = None
     if LA.fused_enabled():
         try:
-            if _grad_wanted(x2, A, B, bias, res2):
-                out = LoraLinearActFunction.apply(x2, A, B, bias, res2, alpha, wt, act)
-            else:
-                out = _act_forward(x2, A, B, bias, res2, alpha, wt, act, save=False)[0]
+            out = _ops().linear_act(x2, A, B, bias, res2, alpha, code, *_operands(wt))
         except L.LoraError as e:
             _declined(e)
     else:
@@ -288,26 +189,6 @@ def _heads_backward(grads, ins, weights, tables, outs, needs, eps, interleaved, 
     return dw
 
 
-class QkNormRopeFunction(torch.autograd.Function):
-    """The norms and the rotation of q [M, hq, D] and k [M, hk, D]."""
-
-    @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
-        q_out, k_out = _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm)
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
-        ctx.rest = eps, interleaved, norm
-        return q_out, k_out
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dq_out, dk_out):
-        q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
-        dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
-        dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
-                             (dq, dk), ctx.needs_input_grad[2:4], *ctx.rest)
-        return dq, dk, *dw, None, None, None, None, None, None
-
-
 def _unfused_heads(v, w, cos, sin, positions, eps, interleaved, norm):
     f = v.float()
     if norm:
@@ -339,14 +220,10 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     else:
         q3, k3 = q.reshape(-1, *q.shape[-2:]), k.reshape(-1, *k.shape[-2:])
         pos = None if positions is None else positions.reshape(-1).contiguous()
-    q3, k3 = _addressable(q3), _addressable(k3)
     outs = None
     if LA.fused_enabled():
         try:
-            if _grad_wanted(q, k, q_weight, k_weight):
-                outs = QkNormRopeFunction.apply(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
-            else:
-                outs = _heads_forward(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
+            outs = _ops().qk_norm_rope(q3, k3, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm)
         except L.LoraError as e:
             _declined(e)
     else:

@@ -572,6 +572,7 @@ struct PlanOverride {
 };
 std::mutex g_plan_mu;
 std::vector<PlanOverride> g_overrides;
+std::atomic<uint64_t> g_plan_epoch{0};
 constexpr size_t MAX_OVERRIDES = 256;
 
 bool find_override(int64_t M, int64_t d_in, int64_t d_out, int r, lora_plan_t *out) {
@@ -600,6 +601,11 @@ Split forced_split(int64_t kb, int splits) {
 struct FusedCut {
     int pieces = 1, cut = 0;
     int slots() const { return cut * (pieces - 1); }
+    // Clusters (of PLAN_SMS / 2) that the last round keeps busy.
+    int64_t last_round(int64_t M, int64_t d_out) const {
+        const int64_t T = cdiv(M, 256) * cdiv(d_out, 256), C = PLAN_SMS / 2;
+        return cut > 0 ? int64_t(cut) * pieces : T % C ? T % C : C;
+    }
 };
 FusedCut fused_cut(int64_t M, int64_t d_out, int64_t K, int r, int64_t C) {
     FusedCut f;
@@ -641,7 +647,17 @@ bool make_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r, int sms, P
     pl->s_g = ov.splitk[1] ? forced_split(cdiv(d_out, BK), ov.splitk[1]) : choose_split(mt_tok, cdiv(d_out, BK), sms);
     pl->s_db = ov.splitk[2] ? forced_split(cdiv(M, BK), ov.splitk[2]) : choose_split(mt_out, cdiv(M, BK), sms);
     pl->s_da = ov.splitk[3] ? forced_split(cdiv(M, BK), ov.splitk[3]) : choose_split(mt_in, cdiv(M, BK), sms);
-    if (pl->side) pl->sx = side_plan(mt_tok, cdiv(d_in, BK), sms, SIDE_MAX_C, ov.xa_cluster);
+    if (pl->side) {
+        pl->sx = side_plan(mt_tok, cdiv(d_in, BK), sms, SIDE_MAX_C, ov.xa_cluster);
+        // A fused forward starts beside s.xa, and its CTA pairs that get s.xa's SMs start late: pairs
+        // of CTAs instead of fours for s.xa where that leaves it only as many SMs as the GEMM's last
+        // round leaves idle (4096 x 4096: 1024 tokens 41.8 -> 33.8 us, 2048 tokens 66.3 -> 57.5 us);
+        // where it does not, fours are faster (4096 tokens 112 us, not 117; 512 tokens 28, not 31).
+        if (fused && !ov.xa_cluster && pl->sx.C == 4) {
+            const int64_t idle = PLAN_SMS - 2 * fused_cut(M, d_out, d_in, r, PLAN_SMS / 2).last_round(M, d_out);
+            if (4 * mt_tok > idle && 2 * mt_tok <= idle) pl->sx = side_plan(mt_tok, cdiv(d_in, BK), sms, 2, 2);
+        }
+    }
     if (pl->side_bwd) {
         pl->sg = side_plan_gdb(M, d_out, r, sms, ov.g_cluster, ov.g_group);
         pl->sd = side_plan(mt_in, mt_tok, sms, SIDE_MAX_C_DA, ov.da_cluster);
@@ -1450,6 +1466,8 @@ lora_status_t lora_linear_bwd_fp8(const uint16_t *dY, const uint16_t *x, const u
                     stream);
 }
 
+uint64_t lora_linear_plan_epoch(void) { return g_plan_epoch.load(std::memory_order_relaxed); }
+
 lora_status_t lora_linear_set_plan(int64_t M, int64_t d_in, int64_t d_out, int r, const lora_plan_t *plan) {
     if (check_shapes(M, d_in, d_out, r, 1.0f, WF_BF16) != LORA_OK) return LORA_ERR_INVALID_ARG;
     if (plan) {
@@ -1470,6 +1488,7 @@ lora_status_t lora_linear_set_plan(int64_t M, int64_t d_in, int64_t d_out, int r
         if (q.g_group > 0 && q.g_group * r > SIDE_RED_BYTES / (128 * 4)) return LORA_ERR_UNSUPPORTED;
     }
     std::lock_guard<std::mutex> lk(g_plan_mu);
+    g_plan_epoch.fetch_add(1, std::memory_order_relaxed);
     for (size_t i = 0; i < g_overrides.size(); ++i)
         if (g_overrides[i].M == M && g_overrides[i].d_in == d_in && g_overrides[i].d_out == d_out &&
             g_overrides[i].r == r) {

@@ -1,0 +1,525 @@
+// torch_ops.cpp -- the operators around the LoRA layer for PyTorch: argument checks, outputs,
+// workspaces and autograd nodes over the C entry points of include/lora_linear.h.  Host code
+// only; every value is computed by the library's kernels.
+//
+// One token's projection is 18 us on the device and a training step of the head norms at 8192
+// tokens 92 us; marshalled in Python they took the host 23 us and 182 us (an autograd function in
+// Python that computes nothing takes 59 us by itself), so these operators are marshalled here.
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/extension.h>
+
+#include <array>
+#include <list>
+#include <mutex>
+#include <optional>
+#include <string>
+#include <tuple>
+#include <vector>
+
+#include "lora_linear.h"
+
+namespace {
+
+using at::Tensor;
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+using OptTensor = std::optional<Tensor>;
+
+// A status of the library other than LORA_OK (LoraError in Python).
+struct StatusError : std::runtime_error {
+    int status;
+    std::string where;
+    StatusError(int s, const char *w)
+        : std::runtime_error(std::string(w) + ": " + lora_status_string(static_cast<lora_status_t>(s))), status(s), where(w) {}
+};
+
+void check(lora_status_t s, const char *where) {
+    if (s != LORA_OK) throw StatusError(s, where);
+}
+
+// ------------------------------------------------------------------ arguments
+bool has(const OptTensor &t) { return t.has_value() && t->defined(); }
+void *addr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+template <class T>
+T *addr(const Tensor &t) { return static_cast<T *>(addr(t)); }
+const uint16_t *bf16(const Tensor &t) { return addr<const uint16_t>(t); }
+const uint16_t *bf16(const OptTensor &t) { return has(t) ? bf16(*t) : nullptr; }
+
+std::string expected(at::ScalarType type, at::IntArrayRef shape, int dev, const Tensor &t) {
+    std::ostringstream s;
+    s << "expected a contiguous " << type << " tensor of shape " << shape << " on cuda:" << dev << ", the current device, got "
+      << t.scalar_type() << " " << t.sizes() << " on " << t.device();
+    return s.str();
+}
+
+// t contiguous, of this type and shape, on the current device.
+void need(const Tensor &t, const char *name, at::ScalarType type, at::IntArrayRef shape, int dev) {
+    TORCH_CHECK_VALUE(t.scalar_type() == type && t.is_cuda() && t.get_device() == dev && t.sizes() == shape && t.is_contiguous(),
+                      name, ": ", expected(type, shape, dev, t));
+}
+void need(const OptTensor &t, const char *name, at::ScalarType type, at::IntArrayRef shape, int dev) {
+    if (has(t)) need(*t, name, type, shape, dev);
+}
+
+// The frozen weight: bf16 [d_out, d_in], or codes with scales (and a codebook).
+struct Weight {
+    int format = 0;
+    Tensor data, scale;
+    std::array<float, 16> codebook{};
+    int64_t d_out = 0, d_in = 0;
+
+    int op(bool bwd) const { return 2 * format + bwd; }  // lora_op_t
+
+    lora_weight_t c() const {
+        lora_weight_t w;
+        w.format = format;
+        w.data = addr(data);
+        w.scale = addr<uint16_t>(scale);
+        w.codebook = format == LORA_W_NF4 ? codebook.data() : nullptr;
+        return w;
+    }
+};
+static_assert(LORA_OP_FWD_Q4 == 2 * LORA_W_Q4 && LORA_OP_FWD_FP8 == 2 * LORA_W_FP8 && LORA_OP_BWD_NF4 == 2 * LORA_W_NF4 + 1, "");
+
+Weight make_weight(int64_t format, const Tensor &data, const OptTensor &scale, const std::vector<float> &codebook, int dev) {
+    TORCH_CHECK_VALUE(data.dim() == 2, "W: expected a tensor [d_out, d_in], got shape ", data.sizes());
+    Weight w;
+    w.format = static_cast<int>(format);
+    w.data = data;
+    const bool packed = format == LORA_W_Q4 || format == LORA_W_NF4;
+    w.d_out = data.size(0);
+    w.d_in = data.size(1) * (packed ? 2 : 1);
+    if (format == LORA_W_BF16) {
+        need(data, "W", at::kBFloat16, {w.d_out, w.d_in}, dev);
+        return w;
+    }
+    need(data, "W's codes", at::kByte, data.sizes(), dev);
+    TORCH_CHECK_VALUE(has(scale), "W: codes need scales");
+    w.scale = *scale;
+    if (packed) need(w.scale, "W's scales", at::kBFloat16, {w.d_out, w.d_in / 64}, dev);
+    else need(w.scale, "W's scales", at::kBFloat16, {w.d_out}, dev);
+    if (format == LORA_W_NF4) {
+        TORCH_CHECK_VALUE(codebook.size() == 16, "codebook: expected 16 values");
+        std::copy(codebook.begin(), codebook.end(), w.codebook.begin());
+    }
+    return w;
+}
+
+Tensor new_bf16(const Tensor &like, at::IntArrayRef shape) { return at::empty(shape, like.options().dtype(at::kBFloat16)); }
+
+// fp32 gradients of bf16 parameters next to each other, and all of them rounded to bf16 by one
+// launch.  (Every size is a multiple of 8: A [r, d_in], B [d_out, r] and the bias [d_out].)
+struct Grads {
+    Tensor flat;
+    std::vector<Tensor> like;
+
+    explicit Grads(std::vector<Tensor> params) : like(std::move(params)) {
+        int64_t n = 0;
+        for (const Tensor &t : like) n += t.defined() ? t.numel() : 0;
+        flat = at::empty({n}, like[0].options().dtype(at::kFloat));
+    }
+    float *operator[](size_t i) const {
+        if (!like[i].defined()) return nullptr;
+        int64_t at = 0;
+        for (size_t j = 0; j < i; ++j) at += like[j].defined() ? like[j].numel() : 0;
+        return flat.data_ptr<float>() + at;
+    }
+    variable_list rounded() const {
+        const Tensor all = flat.to(at::kBFloat16);
+        variable_list out;
+        int64_t at = 0;
+        for (const Tensor &t : like) {
+            out.push_back(t.defined() ? all.narrow(0, at, t.numel()).view(t.sizes()) : Tensor());
+            at += t.defined() ? t.numel() : 0;
+        }
+        return out;
+    }
+};
+
+// ------------------------------------------------------------------ workspaces
+// Kept per device, stream, shape and plan, so that calls on two streams never share one; under
+// capture a new one from the graph's pool, so that two graphs can replay at the same time.
+struct Workspaces {
+    using Key = std::tuple<int, void *, bool, int, int64_t, int64_t, int64_t, int, uint64_t>;
+    static constexpr size_t KEPT = 64;  // the least recently used goes first
+    std::mutex mu;
+    std::list<std::pair<Key, Tensor>> kept;
+};
+
+// `layer`: the layer's own workspace (lora_linear_workspace_size), else lora_linear_act_workspace_size's.
+Tensor workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int r, const c10::cuda::CUDAStream &st) {
+    static Workspaces *const w = new Workspaces;  // never destroyed: tensors must not outlive the device at exit
+    auto make = [&] {
+        const size_t n = layer ? lora_linear_workspace_size(op, M, d_in, d_out, r)
+                               : lora_linear_act_workspace_size(op, M, d_in, d_out, r);
+        TORCH_CHECK_VALUE(n > 0, "invalid sizes: ", M, " tokens, ", d_in, " -> ", d_out, ", rank ", r);
+        return at::zeros({static_cast<int64_t>(n)}, at::TensorOptions().dtype(at::kByte).device(st.device()));
+    };
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return make();
+    const Workspaces::Key key(st.device_index(), st.stream(), layer, op, M, d_in, d_out, r, lora_linear_plan_epoch());
+    const std::lock_guard<std::mutex> lk(w->mu);
+    for (auto it = w->kept.begin(); it != w->kept.end(); ++it)
+        if (it->first == key) {
+            w->kept.splice(w->kept.begin(), w->kept, it);
+            return it->second;
+        }
+    // a workspace that goes returns to its stream's pool of the caching allocator, in stream order
+    // behind the kernels that still use it
+    while (w->kept.size() >= Workspaces::KEPT) w->kept.pop_back();
+    w->kept.emplace_front(key, make());
+    return w->kept.front().second;
+}
+
+// ------------------------------------------------------------------ autograd
+bool trained(const Tensor &t) { return t.requires_grad(); }
+bool trained(const OptTensor &t) { return has(t) && t->requires_grad(); }
+template <class... Ts>
+bool wants_grad(const Ts &...ts) { return at::GradMode::is_enabled() && (trained(ts) || ...); }
+
+// What a node keeps besides its tensors.
+struct Kept : torch::CustomClassHolder {
+    Weight w;
+    double alpha = 0, eps = 0;
+    int act = 0;
+    bool interleaved = false, norm = true, bias = false, residual = false;
+};
+void keep(AutogradContext *ctx, c10::intrusive_ptr<Kept> k) { ctx->saved_data["kept"] = c10::IValue::make_capsule(std::move(k)); }
+const Kept &kept(AutogradContext *ctx, c10::intrusive_ptr<torch::CustomClassHolder> &hold) {
+    hold = ctx->saved_data["kept"].toCapsule();
+    return static_cast<const Kept &>(*hold);
+}
+
+// The kernels' gradients have no graph of their own: differentiating through them is an error, not
+// a silent zero.
+variable_list once(variable_list grads, const variable_list &ups) {
+    bool any = false;
+    if (at::GradMode::is_enabled())
+        for (const Tensor &t : ups) any |= t.defined() && t.requires_grad();
+    if (!any) return grads;
+    for (Tensor &t : grads)
+        if (t.defined()) t = t.detach().requires_grad_(true);
+    auto err = std::make_shared<torch::autograd::DelayedError>(
+        "trying to differentiate twice a function that can be differentiated once", static_cast<int64_t>(grads.size()));
+    return (*err)(std::move(grads));
+}
+
+// ------------------------------------------------------------------ gated projections
+struct GluOut {
+    Tensor p, gu, xa;
+};
+GluOut glu_forward(const Tensor &x, const Tensor &A, const Tensor &B, double alpha, const Weight &w, int act, bool save) {
+    const int dev = c10::cuda::current_device();
+    const int64_t M = x.size(0), r = A.size(0), n = w.d_out;
+    TORCH_CHECK_VALUE(n % 2 == 0, "W: the gate's and the up projection's rows, got ", n);
+    need(x, "x", at::kBFloat16, {M, w.d_in}, dev);
+    need(A, "A", at::kBFloat16, {r, w.d_in}, dev);
+    need(B, "B", at::kBFloat16, {n, r}, dev);
+    GluOut o;
+    o.p = new_bf16(x, {M, n / 2});
+    if (save) {
+        o.gu = new_bf16(x, {M, n});
+        o.xa = new_bf16(x, {M, r});
+    }
+    if (M > 0) {
+        const auto st = c10::cuda::getCurrentCUDAStream(dev);
+        const Tensor ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
+        const lora_weight_t cw = w.c();
+        check(lora_glu_fwd(bf16(x), &cw, bf16(A), bf16(B), addr<uint16_t>(o.p), addr<uint16_t>(o.gu), addr<uint16_t>(o.xa), M,
+                           w.d_in, n / 2, static_cast<int>(r), static_cast<float>(alpha), act, ws.data_ptr(), ws.nbytes(),
+                           st.stream()),
+              "lora_glu_fwd");
+    }
+    return o;
+}
+
+// p = act(g) * u, [g | u] = x.w^T + (alpha / r).(x.A^T).B^T
+struct Glu : torch::autograd::Function<Glu> {
+    static Tensor forward(AutogradContext *ctx, const Tensor &x, const Tensor &A, const Tensor &B, double alpha,
+                          const Weight &w, int64_t act) {
+        GluOut o = glu_forward(x, A, B, alpha, w, static_cast<int>(act), true);
+        ctx->save_for_backward({x, A, B, o.xa, o.gu, w.data, w.scale});
+        auto k = c10::make_intrusive<Kept>();
+        k->w = w;
+        k->alpha = alpha;
+        k->act = static_cast<int>(act);
+        keep(ctx, std::move(k));
+        return o.p;
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list up) {
+        const variable_list s = ctx->get_saved_variables();
+        c10::intrusive_ptr<torch::CustomClassHolder> hold;
+        const Kept &k = kept(ctx, hold);
+        const Tensor &x = s[0], &A = s[1], &B = s[2], &xa = s[3], &gu = s[4];
+        const int dev = c10::cuda::current_device();
+        const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
+        Tensor dX = ctx->needs_input_grad(0) ? at::empty_like(x) : Tensor();
+        if (M == 0) return once({dX, at::zeros_like(A), at::zeros_like(B), Tensor(), Tensor(), Tensor()}, up);
+        const Tensor dP = up[0].contiguous();
+        need(dP, "the gradient of p", at::kBFloat16, {M, n / 2}, dev);
+        const Grads d({A, B});
+        const Tensor dGU = at::empty_like(gu);
+        const auto st = c10::cuda::getCurrentCUDAStream(dev);
+        const Tensor ws = workspace(true, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+        const lora_weight_t cw = k.w.c();
+        check(lora_glu_bwd(bf16(dP), bf16(gu), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dGU),
+                           addr<uint16_t>(dX), d[0], d[1], M, k.w.d_in, n / 2, static_cast<int>(r),
+                           static_cast<float>(k.alpha), k.act, ws.data_ptr(), ws.nbytes(), st.stream()),
+              "lora_glu_bwd");
+        const variable_list g = d.rounded();
+        return once({dX, g[0], g[1], Tensor(), Tensor(), Tensor()}, up);
+    }
+};
+
+Tensor glu(const Tensor &x, const Tensor &A, const Tensor &B, double alpha, int64_t act, int64_t format, const Tensor &data,
+           const OptTensor &scale, const std::vector<float> &codebook) {
+    const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
+    if (wants_grad(x, A, B))
+        return Glu::apply(x, A, B, alpha, w, act);
+    return glu_forward(x, A, B, alpha, w, static_cast<int>(act), false).p;
+}
+
+// ------------------------------------------------------------------ projection with an epilogue
+struct ActOut {
+    Tensor out, pre, xa;
+};
+ActOut act_forward(const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias, const OptTensor &residual,
+                   double alpha, const Weight &w, int act, bool save) {
+    const int dev = c10::cuda::current_device();
+    const int64_t M = x.size(0), r = A.size(0), n = w.d_out;
+    need(x, "x", at::kBFloat16, {M, w.d_in}, dev);
+    need(A, "A", at::kBFloat16, {r, w.d_in}, dev);
+    need(B, "B", at::kBFloat16, {n, r}, dev);
+    need(bias, "bias", at::kBFloat16, {n}, dev);
+    need(residual, "residual", at::kBFloat16, {M, n}, dev);
+    ActOut o;
+    o.out = new_bf16(x, {M, n});
+    if (save) {
+        if (act != LORA_ACT_NONE) o.pre = new_bf16(x, {M, n});
+        o.xa = new_bf16(x, {M, r});
+    }
+    if (M > 0) {
+        const auto st = c10::cuda::getCurrentCUDAStream(dev);
+        const Tensor ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
+        const lora_weight_t cw = w.c();
+        check(lora_linear_act_fwd(bf16(x), &cw, bf16(A), bf16(B), bf16(bias), bf16(residual), addr<uint16_t>(o.out),
+                                  addr<uint16_t>(o.pre), addr<uint16_t>(o.xa), M, w.d_in, n, static_cast<int>(r),
+                                  static_cast<float>(alpha), act, ws.data_ptr(), ws.nbytes(), st.stream()),
+              "lora_linear_act_fwd");
+    }
+    return o;
+}
+
+// out = act(x.w^T + (alpha / r).(x.A^T).B^T + bias) + residual
+struct LinearAct : torch::autograd::Function<LinearAct> {
+    static Tensor forward(AutogradContext *ctx, const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias,
+                          const OptTensor &residual, double alpha, const Weight &w, int64_t act) {
+        ActOut o = act_forward(x, A, B, bias, residual, alpha, w, static_cast<int>(act), true);
+        ctx->save_for_backward({x, A, B, o.xa, o.pre, has(bias) ? *bias : Tensor(), w.data, w.scale});
+        auto k = c10::make_intrusive<Kept>();
+        k->w = w;
+        k->alpha = alpha;
+        k->act = static_cast<int>(act);
+        k->bias = has(bias);
+        k->residual = has(residual);
+        keep(ctx, std::move(k));
+        return o.out;
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list up) {
+        const variable_list s = ctx->get_saved_variables();
+        c10::intrusive_ptr<torch::CustomClassHolder> hold;
+        const Kept &k = kept(ctx, hold);
+        const Tensor &x = s[0], &A = s[1], &B = s[2], &xa = s[3], &pre = s[4], &bias = s[5];
+        const int dev = c10::cuda::current_device();
+        const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
+        // needs_input_grad counts the tensors that were given
+        const bool want_bias = k.bias && ctx->needs_input_grad(3);
+        const bool want_res = k.residual && ctx->needs_input_grad(3 + k.bias);
+        Tensor dX = ctx->needs_input_grad(0) ? at::empty_like(x) : Tensor(), dRes = want_res ? up[0] : Tensor();
+        if (M == 0)
+            return once({dX, at::zeros_like(A), at::zeros_like(B), want_bias ? at::zeros_like(bias) : Tensor(), dRes, Tensor(),
+                         Tensor(), Tensor()}, up);
+        const Tensor dOut = up[0].contiguous();
+        need(dOut, "the gradient of out", at::kBFloat16, {M, n}, dev);
+        const Grads d({A, B, want_bias ? bias : Tensor()});
+        const Tensor dPre = k.act != LORA_ACT_NONE ? at::empty_like(dOut) : Tensor();
+        const auto st = c10::cuda::getCurrentCUDAStream(dev);
+        const Tensor ws = workspace(false, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+        const lora_weight_t cw = k.w.c();
+        check(lora_linear_act_bwd(bf16(dOut), bf16(pre), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dPre),
+                                  addr<uint16_t>(dX), d[0], d[1], d[2], M, k.w.d_in, n, static_cast<int>(r),
+                                  static_cast<float>(k.alpha), k.act, ws.data_ptr(), ws.nbytes(), st.stream()),
+              "lora_linear_act_bwd");
+        const variable_list g = d.rounded();
+        return once({dX, g[0], g[1], g[2], dRes, Tensor(), Tensor(), Tensor()}, up);
+    }
+};
+
+Tensor linear_act(const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias, const OptTensor &residual,
+                  double alpha, int64_t act, int64_t format, const Tensor &data, const OptTensor &scale,
+                  const std::vector<float> &codebook) {
+    const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
+    if (wants_grad(x, A, B, bias, residual))
+        return LinearAct::apply(x, A, B, bias, residual, alpha, w, act);
+    return act_forward(x, A, B, bias, residual, alpha, w, static_cast<int>(act), false).out;
+}
+
+// ------------------------------------------------------------------ norms of q and k with the rotation
+int head_type(const Tensor &t) {
+    switch (t.scalar_type()) {
+        case at::kBFloat16: return LORA_T_BF16;
+        case at::kHalf: return LORA_T_FP16;
+        case at::kFloat: return LORA_T_FP32;
+        default: TORCH_CHECK_VALUE(false, "q, k: bfloat16, float16 or float32, got ", t.scalar_type());
+    }
+}
+
+// t [M, heads, D] itself if the library's strides can name it, else a contiguous copy.
+Tensor addressable(const Tensor &t) {
+    if (t.dim() != 3) return t;
+    const int64_t M = t.size(0), H = t.size(1), D = t.size(2), unit = 16 / t.element_size();
+    auto named = [&](int64_t n, int64_t stride) { return n == 1 || (stride >= D && stride % unit == 0); };
+    if (t.stride(2) == 1 && named(M, t.stride(0)) && named(H, t.stride(1)) &&
+        reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
+        return t;
+    return t.contiguous();
+}
+
+lora_heads_t heads(const Tensor &t, const char *name, const Tensor &like, int dev) {
+    TORCH_CHECK_VALUE(t.scalar_type() == like.scalar_type() && t.sizes() == like.sizes() && t.stride(2) == 1 && t.is_cuda() &&
+                          t.get_device() == dev,
+                      name, ": expected a ", like.scalar_type(), " tensor ", like.sizes(), " on cuda:", dev,
+                      ", the current device, its last dimension contiguous, got ", t.scalar_type(), " ", t.sizes(),
+                      " with strides ", t.strides(), " on ", t.device());
+    lora_heads_t h;
+    h.data = addr(t);
+    h.token_stride = t.stride(0);
+    h.head_stride = t.stride(1);
+    h.heads = static_cast<int32_t>(t.size(1));
+    return h;
+}
+
+struct Rope {
+    const float *cos = nullptr, *sin = nullptr;
+    const int64_t *positions = nullptr;
+    int64_t n_pos = 0;
+    int rot = 0;
+};
+Rope rope(const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, int64_t M, int dev) {
+    Rope t;
+    if (!has(cos)) return t;
+    TORCH_CHECK_VALUE(has(sin) && has(positions) && cos->dim() == 2, "cos, sin [n_pos, rot / 2] and positions go together");
+    need(*cos, "cos", at::kFloat, cos->sizes(), dev);
+    need(*sin, "sin", at::kFloat, cos->sizes(), dev);
+    need(*positions, "positions", at::kLong, {M}, dev);
+    t.cos = addr<float>(*cos);
+    t.sin = addr<float>(*sin);
+    t.positions = addr<int64_t>(*positions);
+    t.n_pos = cos->size(0);
+    t.rot = static_cast<int>(2 * cos->size(1));
+    return t;
+}
+
+std::pair<Tensor, Tensor> heads_forward(const Tensor &q, const Tensor &k, const OptTensor &wq, const OptTensor &wk,
+                                        const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, double eps,
+                                        bool interleaved, bool norm) {
+    const int dev = c10::cuda::current_device();
+    TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3 && k.size(0) == q.size(0) && k.size(2) == q.size(2),
+                      "q, k: expected [tokens, heads, D] of the same tokens and D, got ", q.sizes(), " and ", k.sizes());
+    const int64_t M = q.size(0), D = q.size(2);
+    TORCH_CHECK_VALUE(k.scalar_type() == q.scalar_type(), "k: ", k.scalar_type(), ", q: ", q.scalar_type());
+    const int type = head_type(q);
+    need(wq, "q_weight", q.scalar_type(), {D}, dev);
+    need(wk, "k_weight", q.scalar_type(), {D}, dev);
+    const Rope t = rope(cos, sin, positions, M, dev);
+    const lora_heads_t qi = heads(q, "q", q, dev), ki = heads(k, "k", k, dev);
+    Tensor q_out = at::empty(q.sizes(), q.options()), k_out = at::empty(k.sizes(), k.options());
+    if (M > 0) {
+        const lora_heads_t qo = heads(q_out, "q_out", q, dev), ko = heads(k_out, "k_out", k, dev);
+        check(lora_qk_norm_rope_fwd(type, &qi, &ki, has(wq) ? addr(*wq) : nullptr, has(wk) ? addr(*wk) : nullptr, t.cos, t.sin,
+                                    t.positions, t.n_pos, &qo, &ko, M, static_cast<int>(D), t.rot, interleaved, norm,
+                                    static_cast<float>(eps), c10::cuda::getCurrentCUDAStream(dev).stream()),
+              "lora_qk_norm_rope_fwd");
+    }
+    return {q_out, k_out};
+}
+
+struct QkNormRope : torch::autograd::Function<QkNormRope> {
+    static variable_list forward(AutogradContext *ctx, const Tensor &q, const Tensor &k, const OptTensor &wq,
+                                 const OptTensor &wk, const OptTensor &cos, const OptTensor &sin, const OptTensor &positions,
+                                 double eps, bool interleaved, bool norm) {
+        auto o = heads_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
+        auto t = [](const OptTensor &v) { return has(v) ? *v : Tensor(); };
+        ctx->save_for_backward({q, k, t(wq), t(wk), t(cos), t(sin), t(positions)});
+        auto kp = c10::make_intrusive<Kept>();
+        kp->eps = eps;
+        kp->interleaved = interleaved;
+        kp->norm = norm;
+        keep(ctx, std::move(kp));
+        return {o.first, o.second};
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list up) {
+        const variable_list s = ctx->get_saved_variables();
+        c10::intrusive_ptr<torch::CustomClassHolder> hold;
+        const Kept &kp = kept(ctx, hold);
+        const Tensor &q = s[0], &k = s[1], &wq = s[2], &wk = s[3];
+        const int dev = c10::cuda::current_device();
+        const int64_t M = q.size(0), D = q.size(2);
+        Tensor dq = at::empty(q.sizes(), q.options()), dk = at::empty(k.sizes(), k.options()), dwq, dwk;
+        int edge = 2;  // needs_input_grad counts the tensors that were given
+        if (wq.defined() && ctx->needs_input_grad(edge++)) dwq = M ? at::empty_like(wq) : at::zeros_like(wq);
+        if (wk.defined() && ctx->needs_input_grad(edge++)) dwk = M ? at::empty_like(wk) : at::zeros_like(wk);
+        if (M > 0) {
+            const Tensor dqo = addressable(up[0]), dko = addressable(up[1]);
+            const Rope t = rope(s[4], s[5], s[6], M, dev);
+            const lora_heads_t qi = heads(q, "q", q, dev), ki = heads(k, "k", k, dev), gq = heads(dqo, "the gradient of q", q, dev),
+                               gk = heads(dko, "the gradient of k", k, dev), qo = heads(dq, "dq", q, dev),
+                               ko = heads(dk, "dk", k, dev);
+            Tensor ws;
+            if (dwq.defined() || dwk.defined())
+                ws = at::empty({static_cast<int64_t>(lora_qk_norm_rope_workspace_size(
+                                   M, static_cast<int>(q.size(1) + k.size(1)), static_cast<int>(D)))},
+                               q.options().dtype(at::kByte));
+            check(lora_qk_norm_rope_bwd(head_type(q) | LORA_T_WEIGHT_GRADS, &gq, &gk, &qi, &ki, addr(wq), addr(wk), t.cos, t.sin,
+                                        t.positions, t.n_pos, &qo, &ko, addr(dwq), addr(dwk), M, static_cast<int>(D), t.rot,
+                                        kp.interleaved, kp.norm, static_cast<float>(kp.eps), addr(ws),
+                                        ws.defined() ? ws.nbytes() : 0, c10::cuda::getCurrentCUDAStream(dev).stream()),
+                  "lora_qk_norm_rope_bwd");
+        }
+        return once({dq, dk, dwq, dwk, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()}, up);
+    }
+};
+
+std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, const OptTensor &wq, const OptTensor &wk,
+                                       const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, double eps,
+                                       bool interleaved, bool norm) {
+    const Tensor q = addressable(q_in), k = addressable(k_in);
+    if (wants_grad(q, k, wq, wk)) {
+        const variable_list o = QkNormRope::apply(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
+        return {o[0], o[1]};
+    }
+    return heads_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_ops, m) {
+    m.doc() = "The operators around the LoRA layer over liblora_linear.so, with autograd.";
+    py::register_exception_translator([](std::exception_ptr p) {
+        try {
+            if (p) std::rethrow_exception(p);
+        } catch (const StatusError &e) {
+            const py::object type = py::module_::import("rank_linear_lora_b200.lora_linear").attr("LoraError");
+            const py::object value = type(e.status, e.where);
+            PyErr_SetObject(type.ptr(), value.ptr());
+        }
+    });
+    m.def("glu", &glu);
+    m.def("linear_act", &linear_act);
+    m.def("qk_norm_rope", &qk_norm_rope);
+}

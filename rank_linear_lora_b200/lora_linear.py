@@ -73,6 +73,8 @@ def load_library():
     for f in ("lora_glu_fwd", "lora_glu_bwd", "lora_linear_act_fwd", "lora_linear_act_bwd", "lora_qk_norm_rope_fwd",
               "lora_qk_norm_rope_bwd"):
         getattr(lib, f).restype = I
+    lib.lora_linear_plan_epoch.argtypes = []
+    lib.lora_linear_plan_epoch.restype = ctypes.c_uint64
     lib.lora_linear_check.argtypes = [P, P]
     lib.lora_linear_check.restype = I
     lib.lora_status_string.argtypes = [I]
@@ -294,13 +296,13 @@ class lora_plan_t(ctypes.Structure):
         return p
 
 
-plan_epoch = 0  # plans installed or removed so far: a workspace laid out by an earlier plan is not reused
+def lora_linear_plan_epoch() -> int:
+    """Plans installed or removed so far: a workspace laid out under an earlier one is not reused."""
+    return int(load_library().lora_linear_plan_epoch())
 
 
 def lora_linear_set_plan(M: int, d_in: int, d_out: int, r: int, plan):
     """Install a plan (a lora_plan_t or a dict of its fields) for this shape; None removes it."""
-    global plan_epoch
-    plan_epoch += 1
     fn = load_library().lora_linear_set_plan
     fn.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p]
     fn.restype = ctypes.c_int

@@ -494,3 +494,101 @@ def test_a_captured_step_of_the_block():
         assert torch.equal(out, w)
     for a, b in zip(m.trained().values(), eager.trained().values()):
         assert torch.equal(a, b)
+
+
+def test_which_gradients_are_asked_for():
+    """Any subset of the inputs may want a gradient; the others get none, and the wanted ones are
+    the same bits as when all are."""
+    y = Layer(40, 64, 96, 8, seed=21)
+    cos, sin = block.rope_table(64, 16, device="cuda")
+    pos = torch.arange(40, device="cuda")
+    wq, wk = (1 + 0.1 * y.randn(2, 32)).unbind(0)
+    cases = [
+        (lambda x, A, B, b, r: block.lora_linear_act(x, y.wt, A, B, y.alpha, bias=b, residual=r, act="silu"),
+         [y.x, y.A, y.B, y.bias, y.residual], y.randn(40, 96)),
+        (lambda x, A, B, r: block.lora_linear_act(x, y.wt, A, B, y.alpha, residual=r), [y.x, y.A, y.B, y.residual],
+         y.randn(40, 96)),
+        (lambda x, A, B: block.lora_glu(x, y.wt, A, B, y.alpha), [y.x, y.A, y.B], y.randn(40, 48)),
+        (lambda q, k, a, b: torch.cat(block.qk_norm_rope(q, k, a, b, cos, sin, pos), 1),
+         [y.randn(40, 3, 32), y.randn(40, 2, 32), wq, wk], y.randn(40, 5, 32)),
+        (lambda q, k, b: torch.cat(block.qk_norm_rope(q, k, None, b), 1), [y.randn(40, 3, 32), y.randn(40, 2, 32), wk],
+         y.randn(40, 5, 32)),
+    ]
+    for f, ins, up in cases:
+        leaves = [t.clone().requires_grad_(True) for t in ins]
+        whole = torch.autograd.grad(f(*leaves), leaves, up)
+        for wanted in range(1, 1 << len(ins)):
+            some = [t.clone().requires_grad_(bool(wanted >> i & 1)) for i, t in enumerate(ins)]
+            f(*some).backward(up)
+            for i, t in enumerate(some):
+                assert (t.grad is None) if not wanted >> i & 1 else torch.equal(t.grad, whole[i]), (wanted, i)
+
+
+def test_errors_of_the_native_side():
+    """Types, shapes and devices by name; differentiating twice and inputs changed before the
+    backward are errors; a call after them works."""
+    y = Layer(24, 64, 96, 8, seed=22)
+    cos, sin = block.rope_table(64, 16, device="cuda")
+    q, k, pos = y.randn(24, 3, 32), y.randn(24, 2, 32), torch.arange(24, device="cuda")
+    for match, f in [
+        ("x:", lambda: block.lora_glu(y.x.float(), y.wt, y.A, y.B, 16.0)),
+        ("A:", lambda: block.lora_glu(y.x, y.wt, y.A[:, :56], y.B, 16.0)),
+        ("B:", lambda: block.lora_glu(y.x, y.wt, y.A, y.B.t(), 16.0)),
+        ("bias:", lambda: block.lora_linear_act(y.x, y.wt, y.A, y.B, 16.0, bias=y.bias[:88])),
+        ("residual:", lambda: block.lora_linear_act(y.x, y.wt, y.A, y.B, 16.0, residual=y.residual.half())),
+        ("A:", lambda: block.lora_linear_act(y.x, y.wt, y.A.cpu(), y.B, 16.0)),
+        ("rows", lambda: block.lora_glu(y.x, y.wt.tensors[0][:95], y.A, y.B[:95], 16.0)),
+        ("W", lambda: block.lora_glu(y.x, y.wt.tensors[0].half(), y.A, y.B, 16.0)),
+        ("q, k", lambda: block.qk_norm_rope(q, k[:23], None, None)),
+        ("k:", lambda: block.qk_norm_rope(q, k.half(), None, None)),
+        ("q, k", lambda: block.qk_norm_rope(q.double(), k.double(), None, None)),
+        ("q_weight:", lambda: block.qk_norm_rope(q, k, torch.ones(31, dtype=torch.bfloat16, device="cuda"), None)),
+        ("go together", lambda: block.qk_norm_rope(q, k, None, None, cos, None, pos)),
+        ("sin:", lambda: block.qk_norm_rope(q, k, None, None, cos, sin[:, :4], pos)),
+        ("positions:", lambda: block.qk_norm_rope(q, k, None, None, cos, sin, pos[:23])),
+        ("positions:", lambda: block.qk_norm_rope(q, k, None, None, cos, sin, pos.int())),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            f()
+    with pytest.raises(L.LoraError, match="lora_qk_norm_rope_fwd") as e:
+        block.qk_norm_rope(q, k, None, None, eps=-1.0)
+    assert e.value.status == 1
+    with pytest.raises(L.LoraError, match="lora_linear_act_fwd"):
+        block.lora_linear_act(y.x, y.wt, y.A, y.B, float("inf"))
+    x = y.x.clone().requires_grad_(True)
+    for f in (lambda: block.lora_glu(x, y.wt, y.A, y.B, 16.0), lambda: block.lora_linear_act(x, y.wt, y.A, y.B, 16.0)):
+        up = torch.ones_like(f()).requires_grad_(True)
+        g, = torch.autograd.grad(f(), x, up, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice"):
+            g.sum().backward()
+        out = f()
+        with torch.no_grad():
+            x.add_(1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.backward(up)
+        f().backward(up.detach())
+    assert x.grad is not None
+
+
+def test_threads_and_many_shapes():
+    """Calls from two threads on streams of their own, over more shapes than workspaces are kept,
+    give what the calls give alone."""
+    import threading
+    y = Layer(90, 64, 96, 8, seed=23)
+    alone = [block.lora_glu(y.x[:m], y.wt, y.A, y.B, y.alpha) for m in range(1, 91)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(3):
+                for m in range(1, 91):
+                    if not torch.equal(block.lora_glu(y.x[:m], y.wt, y.A, y.B, y.alpha), alone[m - 1]):
+                        bad.append(m)
+
+    ts = [threading.Thread(target=work) for _ in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
