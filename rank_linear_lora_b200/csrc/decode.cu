@@ -19,8 +19,14 @@
 // here a tile goes from shared memory into fragment registers once, and at a few tokens the
 // tensor pipe has nothing to do either way.  Both operands may order k in any one way, so a
 // lane's fragment registers are 8 or 16 consecutive weights of one row, and x is laid out to
-// match, in shared memory where it fits there.  TMA's 128-byte swizzle and the order in which
-// fragment rows take tile rows keep those reads free of bank conflicts.
+// match, in shared memory.  TMA's 128-byte swizzle and the order in which fragment rows take
+// tile rows keep those reads free of bank conflicts.
+//
+// Where x does not fit into shared memory whole, batches of 2 or 4 groups share its segments: the
+// product warps go through all groups of a batch with one segment before the next one, their
+// sums of each group waiting in shared memory, while a finishing warp brings the segment after
+// it (28672 -> 8192 in bf16: 74 us for 8 tokens, the weight's 470 MB at 6.4 TB/s, 103 us for
+// 16; with x's fragments read from L2 stage by stage it was 151 and 170).
 //
 // Codes are widened in registers, and no decoded weight is rounded.  A 4-bit code under the
 // exponent of 128 is 128 + q; the products take that, and 136 times the block's sum of x
@@ -55,30 +61,38 @@ constexpr int TILE_BYTES = 128;  // of a row per tile
 constexpr int BOX = ROWS * TILE_BYTES;
 constexpr int TILE = 128;       // values of an m-tile x n-tile
 constexpr int FIN_WARPS = 4;     // finishing warps: a thread for each value of an n-tile
-constexpr int STAGE = 2 * BOX;
 enum DecodeOp { D_ACT = 1, D_GLU = 2 };
 enum DecodeFmt { F_BF16 = LORA_W_BF16, F_Q4 = LORA_W_Q4, F_FP8 = LORA_W_FP8, F_CB = LORA_W_NF4 };
 
-template <int FMT, int OP, int NT>
+template <int FMT, int OP, int NT, bool SEG>
 struct Cfg {
     static constexpr bool NIBBLE = FMT == F_Q4 || FMT == F_CB;
     static constexpr int MT = OP == D_GLU ? 2 : 1;
     // Widening 4-bit codes is bound by instructions, not by memory: more warps, and the ring they
     // leave room for (8192 -> 2 x 28672, four tokens: 66 us; 8 warps x 4 stages 78, 16 x 2, which
     // spill, 94).  The other formats stream at 8 x 4 (4096 -> 2 x 11008 in bf16, one token: 30 us).
-    static constexpr int WARPS = NIBBLE ? 12 : 8;
-    static constexpr int STAGES = NIBBLE ? 2 : 4;
+    // With x in segments a 4-bit stage is one box, so that a short segment still has stages for all
+    // warps, and 12 warps pay only where their sums leave the segments room (28672 -> 8192, 8
+    // tokens: 12 x 2 56 us, 8 x 4 66; 16 tokens 113 with 12 x 2 stages of two boxes, 97).
+    static constexpr int WARPS = NIBBLE && (!SEG || MT * NT == 1) ? 12 : 8;
+    static constexpr int BOXES = MT == 2 || !(NIBBLE && SEG) ? 2 : 1;  // of a stage
+    static constexpr int STAGE = BOXES * BOX;
+    static constexpr int STAGES = NIBBLE && (WARPS == 12 || BOXES == 2) ? 2 : 4;
     static constexpr int THREADS = (WARPS + FIN_WARPS) * 32;
     static constexpr int BOX_K = FMT == F_BF16 ? 64 : FMT == F_FP8 ? 128 : 256;  // k of a box
-    static constexpr int STAGE_K = MT == 2 ? BOX_K : 2 * BOX_K;
+    static constexpr int STAGE_K = MT == 2 ? BOX_K : BOXES * BOX_K;
     static constexpr int BLOCKS = STAGE_K / 64;                // 64-wide blocks of k
     static constexpr int BOX_BLOCKS = BOX_K / 64;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int OUT = MT * NT * TILE;                 // fp32 sums of a group
-    static constexpr int RED = 2 * WARPS * OUT * 4;
+    // Groups of a batch, which share each segment of x: their sums take room from the segments.
+    static constexpr int GROUPS = !SEG ? 1 : MT * NT == 4 && !NIBBLE ? 2 : 4;
+    static constexpr int SLOTS = SEG ? GROUPS : 2;             // groups' sums kept
+    static constexpr int RED = SLOTS * WARPS * OUT * 4;
     static constexpr int TABLE = FMT == F_CB ? 256 * 32 * 4 : 0;
-    static constexpr int BARS = (WARPS * STAGES + 4) * 8;
+    static constexpr int BARS = (WARPS * STAGES + 2 * SLOTS + 4) * 8;
     static constexpr int FIXED = 1024 + RING + RED + OUT * 4 + TABLE + BARS + 16 + 128;
+    static constexpr int X_PAD = SEG && FMT != F_BF16 ? 16 : 64;  // behind a token of x: reads of tokens side by side share no bank
     static constexpr int X_MAX = (232448 - FIXED) / 64 * 64;   // room for x
 };
 
@@ -157,34 +171,43 @@ __device__ __forceinline__ bool fin_any(bool v) {
     return r != 0;
 }
 
-// XS: x is in shared memory (else its fragments come from memory stage by stage).
-template <int FMT, int OP, int NT, bool XS>
-__global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const __grid_constant__ DecodeArgs a) {
-    using C_ = Cfg<FMT, OP, NT>;
-    constexpr int MT = C_::MT, WARPS = C_::WARPS, STAGES = C_::STAGES, OUT = C_::OUT, BLOCKS = C_::BLOCKS;
+// SEG: x does not fit into shared memory whole.
+template <int FMT, int OP, int NT, bool SEG>
+__global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(const __grid_constant__ DecodeArgs a) {
+    using C_ = Cfg<FMT, OP, NT, SEG>;
+    constexpr int SLOTS = C_::SLOTS, GROUPS = C_::GROUPS;
+    constexpr int MT = C_::MT, WARPS = C_::WARPS, STAGES = C_::STAGES, STAGE = C_::STAGE, OUT = C_::OUT, BLOCKS = C_::BLOCKS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *red = reinterpret_cast<float *>(smem + C_::RING);  // [2][WARPS][OUT]
-    float *tail = red + 2 * WARPS * OUT;                      // [OUT] the low-rank term
+    float *red = reinterpret_cast<float *>(smem + C_::RING);  // [SLOTS][WARPS][OUT]
+    float *tail = red + SLOTS * WARPS * OUT;                  // [OUT] the low-rank term
     uint32_t *table = reinterpret_cast<uint32_t *>(tail + OUT);
     uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(table) + C_::TABLE);  // [WARPS][STAGES]
-    uint64_t *red_full = bars + WARPS * STAGES, *red_empty = red_full + 2;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(red_empty + 2);
-    uint8_t *zero = reinterpret_cast<uint8_t *>(red_empty + 2) + 16;  // 128 bytes: a block of a token behind M
-    uint8_t *xs = zero + 128;                                         // x, rows x_stride bytes
+    uint64_t *red_full = bars + WARPS * STAGES, *red_empty = red_full + SLOTS;
+    uint64_t *x_full = red_empty + SLOTS, *x_empty = x_full + 2;      // SEG: of the two segments
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(x_empty + 2);
+    uint8_t *zero = reinterpret_cast<uint8_t *>(x_empty + 2) + 16;    // 128 bytes: a block of a token behind M
+    uint8_t *xs = zero + 128;                                         // x, rows x_stride bytes (SEG: two segments)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, j = lane & 3;
     const int S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;      // stages of a group
     const int groups = (a.N + ROWS - 1) / ROWS;
     const int u0 = blockIdx.x, u_step = gridDim.x;
+    const int mine = (groups - u0 + u_step - 1) / u_step;     // groups of this CTA: u0 + i u_step
+    const int SS = SEG ? a.seg_stages : S, n_seg = SEG ? (S + SS - 1) / SS : 1;
+    auto seg_len = [&](int seg) { return SEG ? min(SS, S - seg * SS) : S; };
     const int row_in = tile_row<C_::NIBBLE>(g);  // tile rows of the lane: row_in, row_in + 8
 
     if (warp < WARPS && lane == 0)
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[warp * STAGES + s]), 1);
     if (threadIdx.x == WARPS * 32) {
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < SLOTS; ++b) {
             mbar_init(smem_u32(&red_full[b]), WARPS);
             mbar_init(smem_u32(&red_empty[b]), FIN_WARPS);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&x_full[b]), 1);
+            mbar_init(smem_u32(&x_empty[b]), WARPS);
         }
         *abort_flag = 0;
     }
@@ -194,61 +217,102 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
 
     // x: 64-wide blocks laid out as the fragments take them, zero behind K.  Its loads go out
     // before the stream's, which would hold them up by the whole ring.
-    const int x_cols = S * C_::STAGE_K, x_stride = x_cols * 2 + 64;  // 64 bytes apart mod 128: no two tokens' reads share a bank
-    const int x_chunks = XS ? a.M * (x_cols / 8) : 0;
+    const int x_stride = SS * C_::STAGE_K * 2 + C_::X_PAD, x_buf = a.M * x_stride;
+    const int x_cols8 = S * (C_::STAGE_K / 8), x_chunks = SEG ? 0 : a.M * x_cols8;
     constexpr int X_AHEAD = 8;
     uint4 xv[X_AHEAD];
     auto x_load = [&](int c) {
-        const int m = c / (x_cols / 8), k = (c - m * (x_cols / 8)) * 8;
+        const int m = c / x_cols8, k = (c - m * x_cols8) * 8;
         return k < a.K ? __ldcg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * a.K + k)) : make_uint4(0, 0, 0, 0);
     };
     auto x_store = [&](int c, uint4 v) {
-        const int m = c / (x_cols / 8), k = (c - m * (x_cols / 8)) * 8;
+        const int m = c / x_cols8, k = (c - m * x_cols8) * 8;
         int at = k;
         if (FMT != F_BF16) at = (k & ~63) + ((k >> 3) & 1) * 32 + ((k >> 4) & 3) * 8;  // 16 in a row per lane
         if (FMT == F_Q4)
             v = make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
         *reinterpret_cast<uint4 *>(xs + m * x_stride + at * 2) = v;
     };
+    // SEG: segment `seg` of x to buffer `buf` by bulk copies, as it is, zero behind K; one warp
+    auto x_fill = [&](int seg, int buf) {
+        const int k0 = seg * SS * C_::STAGE_K, width = seg_len(seg) * C_::STAGE_K, cols = min(width, a.K - k0);
+        uint8_t *dst = xs + buf * x_buf;
+        const int behind = (width - cols) / 8;
+        for (int c = lane; c < a.M * behind; c += 32)
+            *reinterpret_cast<uint4 *>(dst + c / behind * x_stride + cols * 2 + c % behind * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        const uint32_t bar = smem_u32(&x_full[buf]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.M * cols * 2));
+        __syncwarp();
+        if (lane < a.M) bulk_load(smem_u32(dst + lane * x_stride), a.x + static_cast<int64_t>(lane) * a.K + k0, cols * 2, bar);
+        __syncwarp();
+    };
+    if constexpr (SEG) {
+        if (warp == WARPS) x_fill(0, 0);
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < X_AHEAD; ++i)
         if (static_cast<int>(threadIdx.x) + i * C_::THREADS < x_chunks) xv[i] = x_load(threadIdx.x + i * C_::THREADS);
 
-    // Requests of a product warp, whose stages are the CTA's warp, warp + WARPS, ...: the cursor
-    // (group req_u, stage req_s of it) runs STAGES ahead of the stage in use.
+    // A product warp's stages are the CTA's warp, warp + WARPS, ..., of all batches, their segments, the
+    // segments' groups and the groups' stages, in that order.
+    struct Cursor {
+        int u, st;         // group, stage of the segment
+        int base, seg, i;  // SEG: the batch's first group (of `mine`), segment, group of the batch
+    };
+    auto settle = [&](Cursor &c) {
+        while (c.st >= seg_len(c.seg) && (!SEG || c.base < mine)) {
+            c.st -= seg_len(c.seg);
+            c.u += u_step;
+            if constexpr (SEG) {
+                const int n = min(GROUPS, mine - c.base);
+                if (++c.i < n) continue;
+                c.i = 0;
+                if (++c.seg < n_seg) {
+                    c.u -= n * u_step;
+                    continue;
+                }
+                c.seg = 0;
+                c.base += GROUPS;
+            }
+        }
+    };
+    auto more = [&](const Cursor &c) { return SEG ? c.base < mine : c.u < groups; };
+    // Its requests run STAGES ahead of the stage in use.
     uint8_t *ring = smem + warp * (STAGES * STAGE);  // (product warps only)
-    int req_u = u0 + warp / S * u_step, req_s = warp % S, requested = 0;
+    Cursor rq{u0, warp, 0, 0, 0};
+    int requested = 0;
     auto advance = [&]() {
-        if (req_u >= groups) return;
+        if (!more(rq)) return;
         if (lane == 0) {
             const int s = requested & (STAGES - 1);
             const uint32_t bar = smem_u32(&bars[warp * STAGES + s]), dst = smem_u32(ring + s * STAGE);
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(STAGE));
-            const int byte = req_s * (MT == 2 ? 1 : 2) * TILE_BYTES, row = req_u * ROWS;
+            const int byte = (rq.seg * SS + rq.st) * (MT == 2 ? 1 : C_::BOXES) * TILE_BYTES, row = rq.u * ROWS;
             tma_load_2d(dst, &a.tmW, bar, byte, row);
-            tma_load_2d(dst + BOX, &a.tmW, bar, MT == 2 ? byte : byte + TILE_BYTES, MT == 2 ? a.N + row : row);
+            if (C_::BOXES == 2) tma_load_2d(dst + BOX, &a.tmW, bar, MT == 2 ? byte : byte + TILE_BYTES, MT == 2 ? a.N + row : row);
         }
         ++requested;
-        req_s += WARPS;
-        while (req_s >= S) {
-            req_s -= S;
-            req_u += u_step;
-        }
+        rq.st += WARPS;
+        settle(rq);
     };
     static_assert((STAGES & (STAGES - 1)) == 0, "stages are counted by masks");
-    if (warp < WARPS)
+    if (warp < WARPS) {
+        settle(rq);
         for (int s = 0; s < STAGES; ++s) advance();
+    }
 
 #pragma unroll
     for (int i = 0; i < X_AHEAD; ++i)
         if (static_cast<int>(threadIdx.x) + i * C_::THREADS < x_chunks) x_store(threadIdx.x + i * C_::THREADS, xv[i]);
     for (int c = threadIdx.x + X_AHEAD * C_::THREADS; c < x_chunks; c += C_::THREADS) x_store(c, x_load(c));
     if (threadIdx.x < 32) reinterpret_cast<uint32_t *>(zero)[threadIdx.x] = 0;
-    // 4-bit codes: -136 times each block's sum of x, [block][token] (zero behind M)
-    float *xsum = reinterpret_cast<float *>(xs + (XS ? a.M * x_stride : 0));
-    if constexpr (XS && FMT == F_Q4) {
+    // 4-bit codes: -136 times each block's sum of x, [block][token] (zero behind M), behind x
+    float *xsum = reinterpret_cast<float *>(xs + x_buf);
+    if constexpr (!SEG && FMT == F_Q4) {
         __syncthreads();
-        const int nb = x_cols / 64;
+        const int nb = S * BLOCKS;
         for (int c = threadIdx.x; c < nb * 8 * NT; c += C_::THREADS) {
             const int b = c / (8 * NT), m = c % (8 * NT);
             float v = 0.0f;
@@ -289,28 +353,16 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const bool in = n * 8 + g < a.M;
-            xp[n] = smem_u32(in ? xs + (n * 8 + g) * x_stride : zero) + j * 16;
+            xp[n] = smem_u32(in ? xs + (n * 8 + g) * x_stride : zero) + j * (SEG && FMT != F_BF16 ? 32 : 16);
             x_step[n] = in ? 128u : 0u;
         }
+        uint32_t x_at = 0;  // byte of the segment's buffer
         auto load_x = [&](int n, int block, uint32_t (&v)[8]) {
-            uint4 u, w;
-            if constexpr (XS) {
-                const uint32_t p = xp[n] + block * x_step[n];
-                u = lds16(p);
-                w = lds16(p + 64);
-            } else {
-                u = w = make_uint4(0, 0, 0, 0);
-                const int ka = block * 64 + (FMT == F_BF16 ? 8 * j : 16 * j), kb = ka + (FMT == F_BF16 ? 32 : 8);
-                const uint16_t *p = a.x + static_cast<int64_t>(n * 8 + g) * a.K;
-                if (n * 8 + g < a.M) {
-                    if (ka < a.K) u = __ldcg(reinterpret_cast<const uint4 *>(p + ka));
-                    if (kb < a.K) w = __ldcg(reinterpret_cast<const uint4 *>(p + kb));
-                }
-                __syncwarp();
-                if (FMT == F_Q4) {
-                    u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
-                    w = make_uint4(prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632), prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
-                }
+            const uint32_t p = xp[n] + block * x_step[n] + (SEG && x_step[n] ? x_at : 0);
+            uint4 u = lds16(p), w = lds16(p + (SEG && FMT != F_BF16 ? 16 : 64));
+            if (SEG && FMT == F_Q4) {
+                u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
+                w = make_uint4(prmt(w.x, w.z, 0x5410), prmt(w.x, w.z, 0x7632), prmt(w.y, w.w, 0x5410), prmt(w.y, w.w, 0x7632));
             }
             v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w, v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
         };
@@ -328,8 +380,8 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
         const bool sc_aligned = n_kb % 4 == 0;  // four scales are 8 aligned bytes
         auto load_scales = [&](int s, uint2 (&sc)[2][2]) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // box
-                const int kb = MT == 2 ? s * 4 : s * 8 + x * 4;
+            for (int x = 0; x < C_::BOXES; ++x) {
+                const int kb = MT == 2 ? s * 4 : (s * C_::BOXES + x) * 4;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint16_t *p = sc_row[MT == 2 ? x : 0][h] + kb;
@@ -345,44 +397,57 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
             }
         };
         bool ok = true;
-        int used = 0, part = 0;
-        int u = u0 + warp / S * u_step, st = warp % S;  // the warp's next stage
+        int used = 0, fill = 0;
+        Cursor at{u0, warp, 0, 0, 0};  // the warp's next stage
+        settle(at);
         uint2 sc[2][2], sc_next[2][2];
-        int sc_u = u;  // the group of sc_row
+        int sc_u = at.u;  // the group of sc_row
         if constexpr (C_::NIBBLE)
-            if (u < groups) {
-                scale_rows(u);
-                load_scales(st, sc_next);
+            if (more(at)) {
+                scale_rows(sc_u);
+                load_scales(at.seg * SS + at.st, sc_next);
             }
-        for (int gu = u0; gu < groups; gu += u_step, ++part) {
+        for (int base = 0; ok && (SEG ? base < mine : u0 + base * u_step < groups); base += GROUPS)
+        for (int seg = 0; ok && seg < n_seg; ++seg, ++fill) {
+        if constexpr (SEG) {
+            ok = wait_bounded(smem_u32(&x_full[fill & 1]), static_cast<uint32_t>(fill >> 1) & 1u, abort_flag, a.err,
+                              DERR_WAIT_FULL);
+            ok = __all_sync(0xffffffffu, ok);
+            x_at = static_cast<uint32_t>((fill & 1) * x_buf);
+        }
+        for (int i = 0; ok && i < (SEG ? min(GROUPS, mine - base) : 1); ++i) {
+            const int gu = u0 + (base + i) * u_step;
+            const int sums = SEG ? i : base & 1;  // slot of the group's sums
             float acc[MT][NT][4] = {};
-            float row_scale[MT][2];
-            if constexpr (FMT == F_FP8) {
+            if (SEG && seg > 0)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&red[(sums * WARPS + warp) * OUT + (m * NT + n) * TILE + lane * 4]);
+                        acc[m][n][0] = v.x, acc[m][n][1] = v.y, acc[m][n][2] = v.z, acc[m][n][3] = v.w;
+                    }
+            const bool last = seg == n_seg - 1;
+            float row_scale[MT][2] = {};
+            if (FMT == F_FP8 && last) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         row_scale[m][h] = bf16_f32(__ldg(a.wscale + m * a.N + min(gu * ROWS + row_in + 8 * h, a.N - 1)));
             }
-            while (u == gu) {
-                const int slot = used & (STAGES - 1), s = st;
-                st += WARPS;
-                while (st >= S) {
-                    st -= S;
-                    u += u_step;
-                }
+            while (SEG ? at.base == base && at.seg == seg && at.i == i : at.u == gu) {
+                const int slot = used & (STAGES - 1), s = at.st;
+                at.st += WARPS;
+                settle(at);
                 if constexpr (C_::NIBBLE) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) sc[x][0] = sc_next[x][0], sc[x][1] = sc_next[x][1];
-                    if (u < groups) {
-                        if (u != sc_u) scale_rows(sc_u = u);
-                        load_scales(st, sc_next);
+                    for (int x = 0; x < C_::BOXES; ++x) sc[x][0] = sc_next[x][0], sc[x][1] = sc_next[x][1];
+                    if (more(at)) {
+                        if (at.u != sc_u) scale_rows(sc_u = at.u);
+                        load_scales(at.seg * SS + at.st, sc_next);
                     }
                 }
-                uint32_t x[XS ? 1 : 2][NT][8];
-                if constexpr (!XS)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) load_x(n, s * BLOCKS, x[0][n]);
                 if (ok) ok = wait_bounded(smem_u32(&bars[warp * STAGES + slot]), static_cast<uint32_t>(used / STAGES) & 1u,
                                           abort_flag, a.err, DERR_WAIT_FULL);
                 ok = __all_sync(0xffffffffu, ok);
@@ -390,11 +455,9 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
                 const uint32_t box0 = ring0 + slot * STAGE;
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b) {
-                    if (XS || b + 1 < BLOCKS) {
+                    uint32_t xb[NT][8];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) load_x(n, s * BLOCKS + (XS ? b : b + 1), x[XS ? 0 : (b + 1) & 1][n]);
-                    }
-                    const uint32_t(&xb)[NT][8] = x[XS ? 0 : b & 1];
+                    for (int n = 0; n < NT; ++n) load_x(n, s * BLOCKS + b, xb[n]);
                     const int bb = b % C_::BOX_BLOCKS;  // block of its box
                     // the lane's weights of the block, as loaded: two rows of each m-tile
                     uint4 q[MT][2][FMT == F_BF16 ? 2 : 1];
@@ -449,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
                                 }
                             }
                         }
-                        if constexpr (FMT == F_Q4 && !XS) {  // one more product, with -136 for the weights
+                        if constexpr (FMT == F_Q4 && SEG) {  // one more product, with -136 for the weights
                             constexpr uint32_t off = 0xC308C308u;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
@@ -458,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
                             }
                         }
                     }
-                    if constexpr (FMT == F_Q4 && XS) {
+                    if constexpr (FMT == F_Q4 && !SEG) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint2 v = lds8(xsum0 + ((s * BLOCKS + b) * 8 * NT + n * 8) * 4);
@@ -488,10 +551,10 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
                 ++used;
                 advance();
             }
-            // the group's sums of this warp, once the buffer's last group is finished
-            const int buf = part & 1;
-            if (ok) ok = wait_bounded(smem_u32(&red_empty[buf]), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, abort_flag,
-                                      a.err, DERR_WAIT_TMEM_EMPTY);
+            // the group's sums of this warp, once the slot's last group is finished
+            const uint32_t round = static_cast<uint32_t>(SEG ? base / GROUPS : base >> 1);  // of the slot
+            if (ok && seg == 0) ok = wait_bounded(smem_u32(&red_empty[sums]), (round & 1u) ^ 1u, abort_flag, a.err,
+                                                  DERR_WAIT_TMEM_EMPTY);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
 #pragma unroll
@@ -502,14 +565,19 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         v[e] = acc[m][n][e];
-                        if constexpr (FMT == F_FP8) v[e] *= row_scale[m][e >> 1];
-                        if constexpr (FMT == F_Q4) v[e] *= 1.0f / 7.0f;
+                        if (FMT == F_FP8 && last) v[e] *= row_scale[m][e >> 1];
+                        if (FMT == F_Q4 && last) v[e] *= 1.0f / 7.0f;
                     }
-                    *reinterpret_cast<float4 *>(&red[(buf * WARPS + warp) * OUT + (m * NT + n) * TILE + lane * 4]) =
+                    *reinterpret_cast<float4 *>(&red[(sums * WARPS + warp) * OUT + (m * NT + n) * TILE + lane * 4]) =
                         make_float4(v[0], v[1], v[2], v[3]);
                 }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&red_full[buf]));
+            if (last && lane == 0) mbar_arrive(smem_u32(&red_full[sums]));
+        }
+        if constexpr (SEG) {
+            __syncwarp();  // every lane has read the segment
+            if (lane == 0) mbar_arrive(smem_u32(&x_empty[fill & 1]));
+        }
         }
         // After a wait that ran out: copies still in flight land before the CTA leaves.
         if (!ok && lane == 0)
@@ -524,7 +592,6 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
     // ---------------------------------------------------------------------- finish
     const int fw = warp - WARPS, o = threadIdx.x - WARPS * 32;  // a thread: value o of each n-tile
     const int l = o >> 2, oi = o & 3;
-    grid_dep_wait();  // s.xa is there, and no earlier kernel still reads what is stored here
     // s.xa and the fragments of B run through the same products; warp fw takes tile fw of MT x NT
     auto low_rank = [&](int u) {
         if (fw < MT * NT) {
@@ -570,14 +637,26 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
             a.out[at] = f32_bf16(y);
         }
     };
-    int part = 0;
-    for (int u = u0; u < groups; u += u_step, ++part) {
-        const int buf = part & 1;
+    const int fills = (mine + GROUPS - 1) / GROUPS * n_seg;
+    bool ok = true;
+    for (int base = 0; ok && base < mine; base += GROUPS) {
+        // segments of x: each while the products use the one before, the next batch's first at the end
+        if (SEG && fw == 0)
+            for (int f = base / GROUPS * n_seg + 1, seg = 1; ok && seg <= n_seg && f < fills; ++f, ++seg) {
+                if (f >= 2)
+                    ok = wait_bounded(smem_u32(&x_empty[f & 1]), static_cast<uint32_t>((f >> 1) - 1) & 1u, abort_flag, a.err,
+                                      DERR_WAIT_EMPTY);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) x_fill(seg < n_seg ? seg : 0, f & 1);
+            }
+        if (base == 0) grid_dep_wait();  // s.xa is there, and no earlier kernel still reads what is stored here
+        for (int i = 0; i < min(GROUPS, mine - base); ++i) {
+        const int u = u0 + (base + i) * u_step, sums = SEG ? i : base & 1;
+        const uint32_t round = static_cast<uint32_t>(SEG ? base / GROUPS : base >> 1);
         low_rank(u);
         // the low-rank term of all four warps is there, and all four agree on how the wait ended
-        if (fin_any(!wait_bounded(smem_u32(&red_full[buf]), static_cast<uint32_t>(part >> 1) & 1u, abort_flag, a.err,
-                                  DERR_WAIT_TMEM_FULL)))
-            break;
+        ok = !fin_any(!ok || !wait_bounded(smem_u32(&red_full[sums]), round & 1u, abort_flag, a.err, DERR_WAIT_TMEM_FULL));
+        if (!ok) break;
         float v[NT][MT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -585,13 +664,14 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT>::THREADS, 1) k_decode(const _
             for (int m = 0; m < MT; ++m) {
                 v[n][m] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) v[n][m] += red[(buf * WARPS + w) * OUT + (m * NT + n) * TILE + o];
+                for (int w = 0; w < WARPS; ++w) v[n][m] += red[(sums * WARPS + w) * OUT + (m * NT + n) * TILE + o];
                 v[n][m] += tail[(m * NT + n) * TILE + o];
             }
         named_bar_sync(1, FIN_WARPS * 32);  // read by all before the next group's low-rank term
-        if (lane == 0) mbar_arrive(smem_u32(&red_empty[buf]));
+        if (lane == 0) mbar_arrive(smem_u32(&red_empty[sums]));
 #pragma unroll
         for (int n = 0; n < NT; ++n) epilogue(u, n, v[n]);
+        }
     }
 }
 
@@ -682,9 +762,9 @@ void launch_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute (&attr)[2], int 
 std::mutex g_mu;
 
 // Raise an instantiation's shared-memory limit, once a device.
-template <int FMT, int OP, int NT, bool XS>
+template <int FMT, int OP, int NT, bool SEG>
 cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t st) {
-    using C_ = Cfg<FMT, OP, NT>;
+    using C_ = Cfg<FMT, OP, NT, SEG>;
     static bool done[64] = {};  // shared-memory limit raised, once a device
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
@@ -692,7 +772,7 @@ cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t 
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!done[d]) {
-            e = cudaFuncSetAttribute(k_decode<FMT, OP, NT, XS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(k_decode<FMT, OP, NT, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C_::FIXED + C_::X_MAX);
             if (e != cudaSuccess) return e;
             done[d] = true;
@@ -700,8 +780,8 @@ cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t 
     }
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    launch_config(&cfg, attr, grid, C_::THREADS, C_::FIXED + (XS ? static_cast<size_t>(x_bytes) : 0), 1, st);
-    e = cudaLaunchKernelEx(&cfg, k_decode<FMT, OP, NT, XS>, a);
+    launch_config(&cfg, attr, grid, C_::THREADS, C_::FIXED + static_cast<size_t>(x_bytes), 1, st);
+    e = cudaLaunchKernelEx(&cfg, k_decode<FMT, OP, NT, SEG>, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     lora_host::count_launch();
     return e;
@@ -709,16 +789,22 @@ cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t 
 
 template <int FMT, int OP, int NT>
 cudaError_t launch_x(const DecodeArgs &a, int sms, cudaStream_t st) {
-    using C_ = Cfg<FMT, OP, NT>;
+    using C_ = Cfg<FMT, OP, NT, false>;
     // One CTA an SM, each with as many groups as the fullest has to have: fewer SMs than all of
     // them still draw the whole bandwidth, and none waits for a last one.
     const int groups = (a.N + ROWS - 1) / ROWS, rounds = (groups + sms - 1) / sms;
     const int grid = (groups + rounds - 1) / rounds;
     const int64_t S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;
-    int64_t x_bytes = a.M * (S * C_::STAGE_K * 2 + 64);
-    if (FMT == F_Q4) x_bytes += S * C_::BLOCKS * 8 * NT * 4;  // and its blocks' sums
-    return x_bytes <= C_::X_MAX ? launch<FMT, OP, NT, true>(a, grid, x_bytes, st)
-                                : launch<FMT, OP, NT, false>(a, grid, 0, st);
+    // all of x, with 4-bit codes and its blocks' sums
+    const int64_t x_bytes = a.M * (S * C_::STAGE_K * 2 + C_::X_PAD) + (FMT == F_Q4 ? S * C_::BLOCKS * 8 * NT * 4 : 0);
+    if (x_bytes <= C_::X_MAX) return launch<FMT, OP, NT, false>(a, grid, x_bytes, st);
+    // The longest segments of which two fit.
+    using G_ = Cfg<FMT, OP, NT, true>;
+    static_assert(G_::X_MAX / 2 >= 8 * NT * (G_::STAGE_K * 2 + G_::X_PAD), "one stage of x");
+    const int64_t most = (G_::X_MAX / 2 / a.M - G_::X_PAD) / (G_::STAGE_K * 2), n_seg = (S + most - 1) / most;
+    DecodeArgs seg = a;
+    seg.seg_stages = static_cast<int>((S + n_seg - 1) / n_seg);
+    return launch<FMT, OP, NT, true>(seg, grid, 2 * a.M * (int64_t(seg.seg_stages) * G_::STAGE_K * 2 + G_::X_PAD), st);
 }
 
 // The s.xa kernel asks for the shared-memory split that k_decode needs, so that an SM it runs on

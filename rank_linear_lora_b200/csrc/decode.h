@@ -27,6 +27,7 @@ struct DecodeArgs {
     int *err;                 // device error word
     int M, N, K, r;
     int act;
+    int seg_stages;           // stages of a segment of x; set by launch_decode
 };
 
 // s.xa = bf16(s . x.A^T) into xa [M, r], then the projection with the weight (or its codes) w

@@ -595,9 +595,11 @@ Split forced_split(int64_t kb, int splits) {
 }
 
 // How a fused forward's tiles on C clusters are cut along K: `pieces` per cut tile (1: none), of
-// `cut` tiles.  With fewer tiles than clusters, as many pieces as put a cluster on each, of 8 K
-// blocks or more (4096 x 4096, 256 tokens: 16 tiles of 65 blocks; a piece costs the hand-over of
-// its accumulator); else the last wave's tiles in two, as the forward's.
+// `cut` tiles.  With fewer tiles than clusters, up to three pieces, as there are clusters for them,
+// of 8 K blocks or more: a tile's last piece adds the others one after the other, some 2 us each
+// (17 tokens, in two / three / four / eight pieces: 5632 -> 2048 26.2 / 24.2 / 25.7 / 33.7 us,
+// 4096 -> 1024 22.0 / 21.0 / 22.6 / 30.0, 11008 -> 4096 42.2 / 35.9 / 37.7).  Else the last wave's
+// tiles in two, as the forward's.
 struct FusedCut {
     int pieces = 1, cut = 0;
     int slots() const { return cut * (pieces - 1); }
@@ -612,7 +614,7 @@ FusedCut fused_cut(int64_t M, int64_t d_out, int64_t K, int r, int64_t C) {
     const int64_t T = cdiv(M, 256) * cdiv(d_out, 256), kb = cdiv(K, BK) + cdiv(r, BK);
     if (C < 1) return f;
     if (T < C) {
-        const int64_t P = std::min<int64_t>({C / T, kb / 8, 8});
+        const int64_t P = std::min<int64_t>({C / T, kb / 8, 3});
         if (P >= 2) {
             f.pieces = static_cast<int>(P);
             f.cut = static_cast<int>(T);

@@ -119,9 +119,8 @@ def _ws(ws):
     """(pointer, bytes) of a workspace tensor: contiguous, on the current device."""
     if ws is None or not ws.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor")
-    if ws.get_device() != torch.cuda.current_device():
-        _on_current_device(ws, "workspace")
-    return ws.data_ptr(), ws.nbytes
+    _on_current_device(ws, "workspace")
+    return _ptr(ws), ws.numel() * ws.element_size()
 
 
 def _check(status: int, where: str):

@@ -158,9 +158,9 @@ def test_workspace_sizes(lib):
         layer = L.lora_linear_workspace_size(op, 512, 1024, 768, 16)
         own = L.lora_linear_act_workspace_size(op, 512, 1024, 768, 16)
         assert own >= layer + 768 * 4 if op % 2 else own > 0
-    # 16 tiles of 256 x 256 for 256 tokens of 4096 columns: pieces of each on all 74 CTA pairs
+    # 16 tiles of 256 x 256 for 256 tokens of 4096 columns: three pieces of each, two of them handed over
     cut = L.lora_linear_act_workspace_size(L.OP_FWD, 256, 4096, 4096, 8)
-    assert cut >= 3 * 16 * 256 * 256 * 4
+    assert cut >= 2 * 16 * 256 * 256 * 4
     assert cut == L.lora_linear_act_workspace_size(L.OP_FWD_Q4, 256, 4096, 4096, 8)
     # a few tokens cut nothing
     assert L.lora_linear_act_workspace_size(L.OP_FWD, 16, 4096, 4096, 8) < 1 << 20

@@ -39,7 +39,7 @@ GLU = [
     (1280, 2056, 2048, 16, "bf16", "silu"),  # 80 tiles, 33 K blocks: the last wave cut along K
     (1280, 264, 2048, 16, "bf16", "silu"),   # 5 K blocks: cut along N
     (1280, 2112, 2048, 16, "q4", "silu"),    # several tiles per CTA pair on a coded weight
-    # fewer tiles than CTA pairs: every tile cut along K, in two to eight pieces
+    # fewer tiles than CTA pairs: every tile cut along K, in two or three pieces
     (33, 1040, 520, 16, "bf16", "silu"),
     (200, 4104, 264, 72, "bf16", "gelu"),
     (40, 4160, 264, 16, "q4", "silu"),
@@ -152,7 +152,7 @@ ACT = [
     (1280, 2056, 4096, 16, "bf16", "gelu", True, True),  # 80 tiles: cut along K
     (1280, 264, 4104, 16, "bf16", "none", True, True),   # 85 tiles: cut along N
     (1280, 2112, 4096, 16, "fp8", "silu", True, True),
-    (33, 1040, 520, 16, "bf16", "silu", True, True),      # cut along K in two to eight pieces
+    (33, 1040, 520, 16, "bf16", "silu", True, True),      # cut along K in two or three pieces
     (200, 4104, 264, 72, "bf16", "none", False, True),
     (40, 4160, 264, 16, "q4", "gelu", True, True),
     (257, 4160, 136, 16, "nf4", "none", True, False),
@@ -592,3 +592,41 @@ def test_threads_and_many_shapes():
     for t in ts:
         t.join()
     assert not bad
+
+
+# A few tokens whose x does not fit into shared memory whole: several segments of it (the last one
+# shorter), one group of rows per CTA or more than share a segment, the last batch not full.
+# M, d_in, d_out, r, format
+FEW = [
+    (8, 13000, 1008, 16, "bf16"),
+    (16, 5064, 9616, 24, "bf16"),
+    (9, 20040, 144, 8, "bf16"),
+    (3, 28672, 272, 16, "bf16"),
+    (2, 65544, 80, 8, "bf16"),
+    (16, 5056, 9616, 24, "q4"),
+    (8, 12992, 5008, 16, "q4"),
+    (5, 20032, 272, 16, "q4"),
+    (16, 5056, 9616, 24, "nf4"),
+    (7, 12992, 5008, 16, "nf4"),
+    (16, 5072, 9616, 16, "fp8"),
+    (6, 20016, 1008, 16, "fp8"),
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=["-".join(map(str, c)) for c in FEW])
+def test_few_tokens_of_many_values(case):
+    M, d, n, r, fmt = case
+    y = Layer(M, d, n, r, fmt, seed=50 + M)
+    ws = L.act_workspace(y.wt.ops()[0], M, d, n, r)
+    want = {"out": _act_reference(y, "silu", True, True)[2:], "p": _glu_reference(y, "silu")[2:]}
+    first = None
+    for _ in range(3):
+        got = {"out": _bf(M, n), "p": _bf(M, n // 2)}
+        L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, y.residual, got["out"], None, None, y.alpha, "silu", ws)
+        L.lora_glu_fwd(y.x, y.wt, y.A, y.B, got["p"], None, None, y.alpha, "silu", ws)
+        L.lora_linear_check(ws)
+        first = first or got
+        for name, t in got.items():
+            assert torch.equal(t, first[name])
+    for name, t in first.items():
+        assert_within(name, t, *want[name])
