@@ -79,14 +79,6 @@ _TORCH_ACT = {
 }
 
 
-def _grad_wanted(*tensors) -> bool:
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                return True
-    return False
-
-
 def _rows(x):
     """x [..., d] as contiguous rows [M, d]."""
     x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
@@ -154,41 +146,6 @@ def rope_table(n_pos: int, rot: int, theta: float = 10000.0, device=None):
     return angle.cos().float(), angle.sin().float()
 
 
-def _addressable(t):
-    """t [M, heads, D] if the library's strides can name it, else a contiguous copy."""
-    if t is None or t.dim() != 3:
-        return t
-    M, H, D = t.shape
-    ts, hs, one = t.stride()
-    unit = 16 // t.element_size()
-    if one == 1 and (M == 1 or (ts >= D and ts % unit == 0)) and (H == 1 or (hs >= D and hs % unit == 0)) \
-            and t.data_ptr() % 16 == 0:
-        return t
-    return t.contiguous()
-
-
-def _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm):
-    """New (q_out, k_out) from the library, contiguous."""
-    q_out, k_out = q.new_empty(q.shape), k.new_empty(k.shape)  # contiguous, whatever q's and k's strides
-    if q.shape[0] > 0:
-        L.lora_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, norm)
-    return q_out, k_out
-
-
-def _heads_backward(grads, ins, weights, tables, outs, needs, eps, interleaved, norm):
-    """The library's backward into `outs`; the gradients of those of the weights that need one."""
-    M, hq, D = ins[0].shape
-    dw = [(torch.empty_like if M else torch.zeros_like)(w) if n and w is not None else None for w, n in zip(weights, needs)]
-    if M == 0:
-        return dw
-    ws = None
-    if dw[0] is not None or dw[1] is not None:
-        n = L.lora_qk_norm_rope_workspace_size(M, hq + ins[1].shape[1], D)
-        ws = torch.empty(n, dtype=torch.uint8, device=ins[0].device)
-    L.lora_qk_norm_rope_bwd(*grads, *ins, *weights, *tables, *outs, *dw, ws, eps, interleaved, norm)
-    return dw
-
-
 def _unfused_heads(v, w, cos, sin, positions, eps, interleaved, norm):
     f = v.float()
     if norm:
@@ -234,37 +191,6 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     return outs if q.dim() == 3 else (outs[0].reshape(q.shape), outs[1].reshape(k.shape))
 
 
-class QkvHeadsFunction(torch.autograd.Function):
-    """q, k, v from the stacked projection h [M, (hq + 2 hk) D] = [q | k | v]: q and k with
-    norm and rotation, v a view.  The backward writes dq and dk straight into their columns
-    of one dh, the gradient the stacked projection's backward reads."""
-
-    @staticmethod
-    def forward(ctx, h, q_weight, k_weight, cos, sin, positions, hq, hk, D, eps, interleaved, norm):
-        q, k, v = QkvHeadsFunction.split(h, hq, hk, D)
-        q_out, k_out = _heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, norm)
-        ctx.save_for_backward(h, q_weight, k_weight, cos, sin, positions)
-        ctx.heads, ctx.rest = (hq, hk, D), (eps, interleaved, norm)
-        return q_out, k_out, v
-
-    @staticmethod
-    def split(h, hq, hk, D):
-        return (h[:, :hq * D].unflatten(1, (hq, D)), h[:, hq * D:(hq + hk) * D].unflatten(1, (hk, D)),
-                h[:, (hq + hk) * D:].unflatten(1, (hk, D)))
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dq_out, dk_out, dv):
-        h, wq, wk, cos, sin, positions = ctx.saved_tensors
-        dh = torch.empty_like(h)
-        dq, dk, dv_part = QkvHeadsFunction.split(dh, *ctx.heads)
-        dv_part.copy_(dv)
-        q, k, _ = QkvHeadsFunction.split(h, *ctx.heads)
-        dw = _heads_backward((_addressable(dq_out), _addressable(dk_out)), (q, k), (wq, wk), (cos, sin, positions),
-                             (dq, dk), ctx.needs_input_grad[1:3], *ctx.rest)
-        return dh, *dw, *(None,) * 9
-
-
 def qkv_heads(h, hq: int, hk: int, D: int, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
               eps: float = 1e-6, interleaved: bool = False, norm: bool = True):
     """(q [..., hq, D], k [..., hk, D], v [..., hk, D]) from h [..., (hq + 2 hk) D] = [q | k | v],
@@ -274,15 +200,18 @@ def qkv_heads(h, hq: int, hk: int, D: int, q_weight=None, k_weight=None, cos=Non
         raise ValueError(f"h: expected {(hq + 2 * hk) * D} columns for {hq} + 2 x {hk} heads of {D}, got {h.shape[-1]}")
     h2 = _rows(h)
     pos = None if positions is None else positions.reshape(-1).contiguous()
-    if LA.fused_enabled() and _grad_wanted(h2, q_weight, k_weight):
+    outs = None
+    if LA.fused_enabled():
         try:
-            outs = QkvHeadsFunction.apply(h2, q_weight, k_weight, cos, sin, pos, hq, hk, D, eps, interleaved, norm)
-            return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)
+            outs = _ops().qkv_heads(h2, q_weight, k_weight, cos, sin, pos, hq, hk, D, eps, interleaved, norm)
         except L.LoraError as e:
-            if e.status != 3:
-                raise
-    q, k, v = QkvHeadsFunction.split(h2, hq, hk, D)
-    outs = (*qk_norm_rope(q, k, q_weight, k_weight, cos, sin, pos, eps, interleaved, norm), v)
+            _declined(e)
+    else:
+        _declined()
+    if outs is None:
+        q, k, v = (t.unflatten(1, (-1, D)) for t in h2.split([hq * D, hk * D, hk * D], dim=1))
+        outs = (_unfused_heads(q, q_weight, cos, sin, pos, eps, interleaved, norm),
+                _unfused_heads(k, k_weight, cos, sin, pos, eps, interleaved, norm), v)
     return tuple(t.reshape(*h.shape[:-1], *t.shape[1:]) for t in outs)
 
 

@@ -185,6 +185,7 @@ struct Kept : torch::CustomClassHolder {
     double alpha = 0, eps = 0;
     int act = 0;
     bool interleaved = false, norm = true, bias = false, residual = false;
+    int64_t hq = 0, hk = 0, D = 0;
 };
 void keep(AutogradContext *ctx, c10::intrusive_ptr<Kept> k) { ctx->saved_data["kept"] = c10::IValue::make_capsule(std::move(k)); }
 const Kept &kept(AutogradContext *ctx, c10::intrusive_ptr<torch::CustomClassHolder> &hold) {
@@ -448,6 +449,38 @@ std::pair<Tensor, Tensor> heads_forward(const Tensor &q, const Tensor &k, const 
     return {q_out, k_out};
 }
 
+// dq, dk and the weights' gradients from up[0], up[1]; the saved tensors from s[at] on are the
+// weights, cos, sin and positions.  `edge`: the first weight's place among the tensors that were
+// given, which needs_input_grad counts.
+std::pair<Tensor, Tensor> heads_backward(AutogradContext *ctx, const Kept &kp, const variable_list &up, const Tensor &q,
+                                         const Tensor &k, const variable_list &s, size_t at, int edge, const Tensor &dq,
+                                         const Tensor &dk) {
+    const Tensor &wq = s[at], &wk = s[at + 1];
+    const int dev = c10::cuda::current_device();
+    const int64_t M = q.size(0), D = q.size(2);
+    Tensor dwq, dwk;
+    if (wq.defined() && ctx->needs_input_grad(edge++)) dwq = M ? at::empty_like(wq) : at::zeros_like(wq);
+    if (wk.defined() && ctx->needs_input_grad(edge++)) dwk = M ? at::empty_like(wk) : at::zeros_like(wk);
+    if (M > 0) {
+        const Tensor dqo = addressable(up[0]), dko = addressable(up[1]);
+        const Rope t = rope(s[at + 2], s[at + 3], s[at + 4], M, dev);
+        const lora_heads_t qi = heads(q, "q", q, dev), ki = heads(k, "k", k, dev), gq = heads(dqo, "the gradient of q", q, dev),
+                           gk = heads(dko, "the gradient of k", k, dev), qo = heads(dq, "dq", q, dev),
+                           ko = heads(dk, "dk", k, dev);
+        Tensor ws;
+        if (dwq.defined() || dwk.defined())
+            ws = at::empty({static_cast<int64_t>(lora_qk_norm_rope_workspace_size(M, static_cast<int>(q.size(1) + k.size(1)),
+                                                                                  static_cast<int>(D)))},
+                           q.options().dtype(at::kByte));
+        check(lora_qk_norm_rope_bwd(head_type(q) | LORA_T_WEIGHT_GRADS, &gq, &gk, &qi, &ki, addr(wq), addr(wk), t.cos, t.sin,
+                                    t.positions, t.n_pos, &qo, &ko, addr(dwq), addr(dwk), M, static_cast<int>(D), t.rot,
+                                    kp.interleaved, kp.norm, static_cast<float>(kp.eps), addr(ws), ws.defined() ? ws.nbytes() : 0,
+                                    c10::cuda::getCurrentCUDAStream(dev).stream()),
+              "lora_qk_norm_rope_bwd");
+    }
+    return {dwq, dwk};
+}
+
 struct QkNormRope : torch::autograd::Function<QkNormRope> {
     static variable_list forward(AutogradContext *ctx, const Tensor &q, const Tensor &k, const OptTensor &wq,
                                  const OptTensor &wk, const OptTensor &cos, const OptTensor &sin, const OptTensor &positions,
@@ -467,31 +500,54 @@ struct QkNormRope : torch::autograd::Function<QkNormRope> {
         const variable_list s = ctx->get_saved_variables();
         c10::intrusive_ptr<torch::CustomClassHolder> hold;
         const Kept &kp = kept(ctx, hold);
-        const Tensor &q = s[0], &k = s[1], &wq = s[2], &wk = s[3];
-        const int dev = c10::cuda::current_device();
-        const int64_t M = q.size(0), D = q.size(2);
-        Tensor dq = at::empty(q.sizes(), q.options()), dk = at::empty(k.sizes(), k.options()), dwq, dwk;
-        int edge = 2;  // needs_input_grad counts the tensors that were given
-        if (wq.defined() && ctx->needs_input_grad(edge++)) dwq = M ? at::empty_like(wq) : at::zeros_like(wq);
-        if (wk.defined() && ctx->needs_input_grad(edge++)) dwk = M ? at::empty_like(wk) : at::zeros_like(wk);
-        if (M > 0) {
-            const Tensor dqo = addressable(up[0]), dko = addressable(up[1]);
-            const Rope t = rope(s[4], s[5], s[6], M, dev);
-            const lora_heads_t qi = heads(q, "q", q, dev), ki = heads(k, "k", k, dev), gq = heads(dqo, "the gradient of q", q, dev),
-                               gk = heads(dko, "the gradient of k", k, dev), qo = heads(dq, "dq", q, dev),
-                               ko = heads(dk, "dk", k, dev);
-            Tensor ws;
-            if (dwq.defined() || dwk.defined())
-                ws = at::empty({static_cast<int64_t>(lora_qk_norm_rope_workspace_size(
-                                   M, static_cast<int>(q.size(1) + k.size(1)), static_cast<int>(D)))},
-                               q.options().dtype(at::kByte));
-            check(lora_qk_norm_rope_bwd(head_type(q) | LORA_T_WEIGHT_GRADS, &gq, &gk, &qi, &ki, addr(wq), addr(wk), t.cos, t.sin,
-                                        t.positions, t.n_pos, &qo, &ko, addr(dwq), addr(dwk), M, static_cast<int>(D), t.rot,
-                                        kp.interleaved, kp.norm, static_cast<float>(kp.eps), addr(ws),
-                                        ws.defined() ? ws.nbytes() : 0, c10::cuda::getCurrentCUDAStream(dev).stream()),
-                  "lora_qk_norm_rope_bwd");
-        }
-        return once({dq, dk, dwq, dwk, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()}, up);
+        const Tensor &q = s[0], &k = s[1];
+        const Tensor dq = at::empty(q.sizes(), q.options()), dk = at::empty(k.sizes(), k.options());
+        const auto dw = heads_backward(ctx, kp, up, q, k, s, 2, 2, dq, dk);
+        return once({dq, dk, dw.first, dw.second, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()}, up);
+    }
+};
+
+// The same on the stacked projection h [M, (hq + 2 hk) D] = [q | k | v]: v is a view of h, and the
+// backward writes dq and dk straight into their columns of one dh.
+std::array<Tensor, 3> split_heads(const Tensor &h, int64_t hq, int64_t hk, int64_t D) {
+    const int64_t M = h.size(0), row = h.stride(0);
+    auto part = [&](int64_t col, int64_t n) { return h.narrow(1, col, n * D).as_strided({M, n, D}, {row, D, 1}); };
+    return {part(0, hq), part(hq * D, hk), part((hq + hk) * D, hk)};
+}
+
+struct QkvHeads : torch::autograd::Function<QkvHeads> {
+    static variable_list forward(AutogradContext *ctx, const Tensor &h, const OptTensor &wq, const OptTensor &wk,
+                                 const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, int64_t hq,
+                                 int64_t hk, int64_t D, double eps, bool interleaved, bool norm) {
+        auto qkv = split_heads(h, hq, hk, D);
+        auto o = heads_forward(qkv[0], qkv[1], wq, wk, cos, sin, positions, eps, interleaved, norm);
+        auto t = [](const OptTensor &v) { return has(v) ? *v : Tensor(); };
+        ctx->save_for_backward({h, t(wq), t(wk), t(cos), t(sin), t(positions)});
+        auto kp = c10::make_intrusive<Kept>();
+        kp->eps = eps;
+        kp->interleaved = interleaved;
+        kp->norm = norm;
+        kp->hq = hq;
+        kp->hk = hk;
+        kp->D = D;
+        keep(ctx, std::move(kp));
+        return {o.first, o.second, qkv[2]};
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list up) {
+        const variable_list s = ctx->get_saved_variables();
+        c10::intrusive_ptr<torch::CustomClassHolder> hold;
+        const Kept &kp = kept(ctx, hold);
+        const auto in = split_heads(s[0], kp.hq, kp.hk, kp.D);
+        const Tensor dh = at::empty_like(s[0]);
+        const auto d = split_heads(dh, kp.hq, kp.hk, kp.D);
+        d[2].copy_(up[2]);
+        const auto dw = heads_backward(ctx, kp, up, in[0], in[1], s, 1, 1, d[0], d[1]);
+        variable_list out(12);
+        out[0] = dh;
+        out[1] = dw.first;
+        out[2] = dw.second;
+        return once(std::move(out), up);
     }
 };
 
@@ -504,6 +560,20 @@ std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, c
         return {o[0], o[1]};
     }
     return heads_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
+}
+
+std::tuple<Tensor, Tensor, Tensor> qkv_heads(const Tensor &h, const OptTensor &wq, const OptTensor &wk, const OptTensor &cos,
+                                             const OptTensor &sin, const OptTensor &positions, int64_t hq, int64_t hk,
+                                             int64_t D, double eps, bool interleaved, bool norm) {
+    TORCH_CHECK_VALUE(h.dim() == 2 && hq > 0 && hk > 0 && D > 0 && h.size(1) == (hq + 2 * hk) * D, "h: expected ",
+                      (hq + 2 * hk) * D, " columns, got ", h.sizes());
+    if (wants_grad(h, wq, wk)) {
+        const variable_list o = QkvHeads::apply(h, wq, wk, cos, sin, positions, hq, hk, D, eps, interleaved, norm);
+        return {o[0], o[1], o[2]};
+    }
+    const auto qkv = split_heads(h, hq, hk, D);
+    const auto o = heads_forward(qkv[0], qkv[1], wq, wk, cos, sin, positions, eps, interleaved, norm);
+    return {o.first, o.second, qkv[2]};
 }
 
 }  // namespace
@@ -522,4 +592,5 @@ PYBIND11_MODULE(_ops, m) {
     m.def("glu", &glu);
     m.def("linear_act", &linear_act);
     m.def("qk_norm_rope", &qk_norm_rope);
+    m.def("qkv_heads", &qkv_heads);
 }
