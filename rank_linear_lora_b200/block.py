@@ -18,7 +18,8 @@ Workspaces are kept per device, stream and shape, so calls on two streams never 
 a call that is being captured into a CUDA graph takes a workspace of its own from the
 graph's memory pool, so two graphs can replay at the same time.  To capture a backward,
 capture the forward with it in the same graph (autograd runs a backward on the streams of
-its forward).
+its forward), while no eager graph of the same leaves lives: as with torch's own operators,
+autograd would accumulate on that graph's stream, and the capture raises.
 """
 from __future__ import annotations
 

@@ -141,7 +141,9 @@ struct Grads {
 
 // ------------------------------------------------------------------ workspaces
 // Kept per device, stream, shape and plan, so that calls on two streams never share one; under
-// capture a new one from the graph's pool, so that two graphs can replay at the same time.
+// capture a new one from the graph's pool, so that two graphs can replay at the same time.  Two
+// threads may call on one stream: a call holds its lock until all its kernels are enqueued, so
+// that none of another call's, which would use the same workspace, come between them.
 struct Workspaces {
     using Key = std::tuple<int, void *, bool, int, int64_t, int64_t, int64_t, int, uint64_t>;
     static constexpr size_t KEPT = 64;  // the least recently used goes first
@@ -149,8 +151,15 @@ struct Workspaces {
     std::list<std::pair<Key, Tensor>> kept;
 };
 
+struct Lease {
+    std::unique_lock<std::mutex> lock;
+    Tensor ws;
+    void *data() const { return ws.data_ptr(); }
+    size_t bytes() const { return ws.nbytes(); }
+};
+
 // `layer`: the layer's own workspace (lora_linear_workspace_size), else lora_linear_act_workspace_size's.
-Tensor workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int r, const c10::cuda::CUDAStream &st) {
+Lease workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int r, const c10::cuda::CUDAStream &st) {
     static Workspaces *const w = new Workspaces;  // never destroyed: tensors must not outlive the device at exit
     auto make = [&] {
         const size_t n = layer ? lora_linear_workspace_size(op, M, d_in, d_out, r)
@@ -158,19 +167,19 @@ Tensor workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int
         TORCH_CHECK_VALUE(n > 0, "invalid sizes: ", M, " tokens, ", d_in, " -> ", d_out, ", rank ", r);
         return at::zeros({static_cast<int64_t>(n)}, at::TensorOptions().dtype(at::kByte).device(st.device()));
     };
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return make();
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return {{}, make()};
     const Workspaces::Key key(st.device_index(), st.stream(), layer, op, M, d_in, d_out, r, lora_linear_plan_epoch());
-    const std::lock_guard<std::mutex> lk(w->mu);
+    std::unique_lock<std::mutex> lk(w->mu);
     for (auto it = w->kept.begin(); it != w->kept.end(); ++it)
         if (it->first == key) {
             w->kept.splice(w->kept.begin(), w->kept, it);
-            return it->second;
+            return {std::move(lk), w->kept.front().second};
         }
     // a workspace that goes returns to its stream's pool of the caching allocator, in stream order
     // behind the kernels that still use it
     while (w->kept.size() >= Workspaces::KEPT) w->kept.pop_back();
     w->kept.emplace_front(key, make());
-    return w->kept.front().second;
+    return {std::move(lk), w->kept.front().second};
 }
 
 // ------------------------------------------------------------------ autograd
@@ -226,10 +235,10 @@ GluOut glu_forward(const Tensor &x, const Tensor &A, const Tensor &B, double alp
     }
     if (M > 0) {
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Tensor ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
+        const Lease ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = w.c();
         check(lora_glu_fwd(bf16(x), &cw, bf16(A), bf16(B), addr<uint16_t>(o.p), addr<uint16_t>(o.gu), addr<uint16_t>(o.xa), M,
-                           w.d_in, n / 2, static_cast<int>(r), static_cast<float>(alpha), act, ws.data_ptr(), ws.nbytes(),
+                           w.d_in, n / 2, static_cast<int>(r), static_cast<float>(alpha), act, ws.data(), ws.bytes(),
                            st.stream()),
               "lora_glu_fwd");
     }
@@ -264,11 +273,11 @@ struct Glu : torch::autograd::Function<Glu> {
         const Grads d({A, B});
         const Tensor dGU = at::empty_like(gu);
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Tensor ws = workspace(true, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+        const Lease ws = workspace(true, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = k.w.c();
         check(lora_glu_bwd(bf16(dP), bf16(gu), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dGU),
                            addr<uint16_t>(dX), d[0], d[1], M, k.w.d_in, n / 2, static_cast<int>(r),
-                           static_cast<float>(k.alpha), k.act, ws.data_ptr(), ws.nbytes(), st.stream()),
+                           static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
               "lora_glu_bwd");
         const variable_list g = d.rounded();
         return once({dX, g[0], g[1], Tensor(), Tensor(), Tensor()}, up);
@@ -304,11 +313,11 @@ ActOut act_forward(const Tensor &x, const Tensor &A, const Tensor &B, const OptT
     }
     if (M > 0) {
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Tensor ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
+        const Lease ws = workspace(false, w.op(false), M, w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = w.c();
         check(lora_linear_act_fwd(bf16(x), &cw, bf16(A), bf16(B), bf16(bias), bf16(residual), addr<uint16_t>(o.out),
                                   addr<uint16_t>(o.pre), addr<uint16_t>(o.xa), M, w.d_in, n, static_cast<int>(r),
-                                  static_cast<float>(alpha), act, ws.data_ptr(), ws.nbytes(), st.stream()),
+                                  static_cast<float>(alpha), act, ws.data(), ws.bytes(), st.stream()),
               "lora_linear_act_fwd");
     }
     return o;
@@ -349,11 +358,11 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
         const Grads d({A, B, want_bias ? bias : Tensor()});
         const Tensor dPre = k.act != LORA_ACT_NONE ? at::empty_like(dOut) : Tensor();
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Tensor ws = workspace(false, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+        const Lease ws = workspace(false, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = k.w.c();
         check(lora_linear_act_bwd(bf16(dOut), bf16(pre), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dPre),
                                   addr<uint16_t>(dX), d[0], d[1], d[2], M, k.w.d_in, n, static_cast<int>(r),
-                                  static_cast<float>(k.alpha), k.act, ws.data_ptr(), ws.nbytes(), st.stream()),
+                                  static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
               "lora_linear_act_bwd");
         const variable_list g = d.rounded();
         return once({dX, g[0], g[1], g[2], dRes, Tensor(), Tensor(), Tensor()}, up);

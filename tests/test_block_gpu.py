@@ -594,6 +594,36 @@ def test_threads_and_many_shapes():
     assert not bad
 
 
+def test_threads_on_one_stream():
+    """Forwards and backwards from two threads on one stream (their backwards in the threads
+    themselves, not one after the other in autograd's own) do not mix up each other's workspace."""
+    import threading
+    y = [Layer(70, 264, 400, 16, seed=s) for s in (24, 25)]
+    up = y[0].randn(70, 400)
+
+    def step(i):
+        x, A, B = (t.clone().requires_grad_(True) for t in (y[i].x, y[i].A, y[i].B))
+        out = block.lora_linear_act(x, y[i].wt, A, B, y[i].alpha, act="silu")
+        return (out.detach(), *torch.autograd.grad(out, (x, A, B), up))
+
+    alone = [step(i) for i in (0, 1)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.autograd.set_multithreading_enabled(False):
+            for _ in range(60):
+                got[i].append(step(i))
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for i in (0, 1):
+        assert len(got[i]) == 60 and all(torch.equal(a, b) for g in got[i] for a, b in zip(g, alone[i]))
+
+
 # A few tokens whose x does not fit into shared memory whole: several segments of it (the last one
 # shorter), one group of rows per CTA or more than share a segment, the last batch not full.
 # M, d_in, d_out, r, format
