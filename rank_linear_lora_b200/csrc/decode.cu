@@ -3,12 +3,13 @@
 //   acc[n, m] = sum_k W[n, k] x[m, k] + sum_j B[n, j] (s.xa)[m, j],   then the epilogue
 //
 // Bound by reading W once.  A 256 x 256 tensor-core tile per CTA pair would put only
-// d_out / 256 pairs of SMs on that stream, so here one persistent CTA an SM takes groups of 16
-// weight rows (the gate's and the up projection's 16, when gated), every CTA the same number:
+// d_out / 256 pairs of SMs on that stream, so here one persistent CTA an SM takes groups of 16 or
+// 32 weight rows (16 of the gate and 16 of the up projection, when gated), every CTA the same
+// number:
 //
 //   product warps    a group's rows are cut along K into stages of two 2 KB boxes (128 bytes of
-//                    16 rows: both projections' when gated, else two in a row); the warps take
-//                    the CTA's stages in turn.  Each streams its own by TMA into a private ring
+//                    16 rows: both of a group's, or two in a row); the warps take the CTA's
+//                    stages in turn.  Each streams its own by TMA into a private ring
 //                    in shared memory, several ahead and on into the next groups, and at a
 //                    group's end leaves its sums in one of two buffers.
 //   finishing warps  finish a group while the others go on: the warps' sums in a fixed order,
@@ -25,8 +26,8 @@
 // Where x does not fit into shared memory whole, batches of 2 or 4 groups share its segments: the
 // product warps go through all groups of a batch with one segment before the next one, their
 // sums of each group waiting in shared memory, while a finishing warp brings the segment after
-// it (28672 -> 8192 in bf16: 74 us for 8 tokens, the weight's 470 MB at 6.4 TB/s, 103 us for
-// 16; with x's fragments read from L2 stage by stage it was 151 and 170).
+// it (28672 -> 8192 in bf16: 74 us for 8 tokens, the weight's 470 MB at 6.4 TB/s, 89 us for 16;
+// with x's fragments read from L2 stage by stage it was 151 and 170).
 //
 // Codes are widened in registers, and no decoded weight is rounded.  A 4-bit code under the
 // exponent of 128 is 128 + q; the products take that, and 136 times the block's sum of x
@@ -64,16 +65,16 @@ constexpr int FIN_WARPS = 4;     // finishing warps: a thread for each value of 
 enum DecodeOp { D_ACT = 1, D_GLU = 2 };
 enum DecodeFmt { F_BF16 = LORA_W_BF16, F_Q4 = LORA_W_Q4, F_FP8 = LORA_W_FP8, F_CB = LORA_W_NF4 };
 
-template <int FMT, int OP, int NT, bool SEG>
+template <int FMT, int OP, int NT, bool SEG, int MT>
 struct Cfg {
     static constexpr bool NIBBLE = FMT == F_Q4 || FMT == F_CB;
-    static constexpr int MT = OP == D_GLU ? 2 : 1;
+    static constexpr int GROUP_ROWS = OP == D_GLU ? ROWS : MT * ROWS;  // of each projection
     // Widening 4-bit codes is bound by instructions, not by memory: more warps, and the ring they
     // leave room for (8192 -> 2 x 28672, four tokens: 66 us; 8 warps x 4 stages 78, 16 x 2, which
     // spill, 94).  The other formats stream at 8 x 4 (4096 -> 2 x 11008 in bf16, one token: 30 us).
     // With x in segments a 4-bit stage is one box, so that a short segment still has stages for all
-    // warps, and 12 warps pay only where their sums leave the segments room (28672 -> 8192, 8
-    // tokens: 12 x 2 56 us, 8 x 4 66; 16 tokens 113 with 12 x 2 stages of two boxes, 97).
+    // warps, and 12 warps pay only where their sums leave the segments room (28672 -> 8192 in groups
+    // of 16 rows, 8 tokens: 12 x 2 56 us, 8 x 4 66; 16 tokens: 12 x 2 stages of two boxes 113, 97).
     static constexpr int WARPS = NIBBLE && (!SEG || MT * NT == 1) ? 12 : 8;
     static constexpr int BOXES = MT == 2 || !(NIBBLE && SEG) ? 2 : 1;  // of a stage
     static constexpr int STAGE = BOXES * BOX;
@@ -172,11 +173,11 @@ __device__ __forceinline__ bool fin_any(bool v) {
 }
 
 // SEG: x does not fit into shared memory whole.
-template <int FMT, int OP, int NT, bool SEG>
-__global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(const __grid_constant__ DecodeArgs a) {
-    using C_ = Cfg<FMT, OP, NT, SEG>;
+template <int FMT, int OP, int NT, bool SEG, int MT>
+__global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decode(const __grid_constant__ DecodeArgs a) {
+    using C_ = Cfg<FMT, OP, NT, SEG, MT>;
     constexpr int SLOTS = C_::SLOTS, GROUPS = C_::GROUPS;
-    constexpr int MT = C_::MT, WARPS = C_::WARPS, STAGES = C_::STAGES, STAGE = C_::STAGE, OUT = C_::OUT, BLOCKS = C_::BLOCKS;
+    constexpr int GROUP_ROWS = C_::GROUP_ROWS, WARPS = C_::WARPS, STAGES = C_::STAGES, STAGE = C_::STAGE, OUT = C_::OUT, BLOCKS = C_::BLOCKS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *red = reinterpret_cast<float *>(smem + C_::RING);  // [SLOTS][WARPS][OUT]
@@ -191,7 +192,11 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, j = lane & 3;
     const int S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;      // stages of a group
-    const int groups = (a.N + ROWS - 1) / ROWS;
+    const int groups = (a.N + GROUP_ROWS - 1) / GROUP_ROWS;
+    // row of m-tile m of a group in W, and in what has a value a row of it; rows behind N read the last
+    auto w_row = [&](int u, int m, int row) {
+        return OP == D_GLU ? min(u * ROWS + row, a.N - 1) + m * a.N : min(u * GROUP_ROWS + m * ROWS + row, a.N - 1);
+    };
     const int u0 = blockIdx.x, u_step = gridDim.x;
     const int mine = (groups - u0 + u_step - 1) / u_step;     // groups of this CTA: u0 + i u_step
     const int SS = SEG ? a.seg_stages : S, n_seg = SEG ? (S + SS - 1) / SS : 1;
@@ -289,9 +294,9 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
             const int s = requested & (STAGES - 1);
             const uint32_t bar = smem_u32(&bars[warp * STAGES + s]), dst = smem_u32(ring + s * STAGE);
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(STAGE));
-            const int byte = (rq.seg * SS + rq.st) * (MT == 2 ? 1 : C_::BOXES) * TILE_BYTES, row = rq.u * ROWS;
+            const int byte = (rq.seg * SS + rq.st) * (MT == 2 ? 1 : C_::BOXES) * TILE_BYTES, row = rq.u * GROUP_ROWS;
             tma_load_2d(dst, &a.tmW, bar, byte, row);
-            if (C_::BOXES == 2) tma_load_2d(dst + BOX, &a.tmW, bar, MT == 2 ? byte : byte + TILE_BYTES, MT == 2 ? a.N + row : row);
+            if (C_::BOXES == 2) tma_load_2d(dst + BOX, &a.tmW, bar, MT == 2 ? byte : byte + TILE_BYTES, OP == D_GLU ? a.N + row : MT == 2 ? row + ROWS : row);
         }
         ++requested;
         rq.st += WARPS;
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    sc_row[m][h] = a.wscale + static_cast<int64_t>(min(u * ROWS + row_in + 8 * h, a.N - 1) + m * a.N) * n_kb;
+                    sc_row[m][h] = a.wscale + static_cast<int64_t>(w_row(u, m, row_in + 8 * h)) * n_kb;
         };
         const bool sc_aligned = n_kb % 4 == 0;  // four scales are 8 aligned bytes
         auto load_scales = [&](int s, uint2 (&sc)[2][2]) {
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        row_scale[m][h] = bf16_f32(__ldg(a.wscale + m * a.N + min(gu * ROWS + row_in + 8 * h, a.N - 1)));
+                        row_scale[m][h] = bf16_f32(__ldg(a.wscale + w_row(gu, m, row_in + 8 * h)));
             }
             while (SEG ? at.base == base && at.seg == seg && at.i == i : at.u == gu) {
                 const int slot = used & (STAGES - 1), s = at.st;
@@ -596,8 +601,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
     auto low_rank = [&](int u) {
         if (fw < MT * NT) {
             const int m = fw / NT, n = fw % NT;
-            const int64_t r0 = static_cast<int64_t>(m) * a.N + min(u * ROWS + row_in, a.N - 1);
-            const int64_t r1 = static_cast<int64_t>(m) * a.N + min(u * ROWS + row_in + 8, a.N - 1);
+            const int64_t r0 = w_row(u, m, row_in), r1 = w_row(u, m, row_in + 8);
             const uint4 zero = make_uint4(0, 0, 0, 0);
             float c[4] = {};
 #pragma unroll 2
@@ -615,26 +619,31 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG>::THREADS, 1) k_decode(co
         }
     };
     auto epilogue = [&](int u, int n, const float (&v)[MT]) {
-        const int col = u * ROWS + tile_row<C_::NIBBLE>(l >> 2) + 8 * (oi >> 1);
+        const int col0 = u * GROUP_ROWS + tile_row<C_::NIBBLE>(l >> 2) + 8 * (oi >> 1);
         const int token = n * 8 + 2 * (l & 3) + (oi & 1);
-        if (col >= a.N || token >= a.M) return;
-        const int64_t at = static_cast<int64_t>(token) * a.N + col;
+        if (token >= a.M) return;
+        const int64_t row = static_cast<int64_t>(token) * a.N;
         if constexpr (OP == D_GLU) {
+            if (col0 >= a.N) return;
             if (a.save) {
-                const int64_t s = static_cast<int64_t>(token) * 2 * a.N + col;
-                a.save[s] = f32_bf16(v[0]);
-                a.save[s + a.N] = f32_bf16(v[1]);
+                a.save[2 * row + col0] = f32_bf16(v[0]);
+                a.save[2 * row + col0 + a.N] = f32_bf16(v[1]);
             }
             float y = 0.0f;
             act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(v[0]); });
-            a.out[at] = f32_bf16(y * v[1]);
+            a.out[row + col0] = f32_bf16(y * v[1]);
         } else {
-            float y = v[0];
-            if (a.bias) y += bf16_f32(__ldcg(a.bias + col));
-            if (a.save) a.save[at] = f32_bf16(y);
-            act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(y); });
-            if (a.residual) y += bf16_f32(__ldcg(a.residual + at));
-            a.out[at] = f32_bf16(y);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int col = col0 + m * ROWS;
+                if (col >= a.N) break;
+                float y = v[m];
+                if (a.bias) y += bf16_f32(__ldcg(a.bias + col));
+                if (a.save) a.save[row + col] = f32_bf16(y);
+                act_dispatch(a.act, [&](auto A) { y = act_value<A.value>(y); });
+                if (a.residual) y += bf16_f32(__ldcg(a.residual + row + col));
+                a.out[row + col] = f32_bf16(y);
+            }
         }
     };
     const int fills = (mine + GROUPS - 1) / GROUPS * n_seg;
@@ -762,9 +771,9 @@ void launch_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute (&attr)[2], int 
 std::mutex g_mu;
 
 // Raise an instantiation's shared-memory limit, once a device.
-template <int FMT, int OP, int NT, bool SEG>
+template <int FMT, int OP, int NT, bool SEG, int MT>
 cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t st) {
-    using C_ = Cfg<FMT, OP, NT, SEG>;
+    using C_ = Cfg<FMT, OP, NT, SEG, MT>;
     static bool done[64] = {};  // shared-memory limit raised, once a device
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
@@ -772,7 +781,7 @@ cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t 
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!done[d]) {
-            e = cudaFuncSetAttribute(k_decode<FMT, OP, NT, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(k_decode<FMT, OP, NT, SEG, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C_::FIXED + C_::X_MAX);
             if (e != cudaSuccess) return e;
             done[d] = true;
@@ -781,30 +790,31 @@ cudaError_t launch(const DecodeArgs &a, int grid, int64_t x_bytes, cudaStream_t 
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     launch_config(&cfg, attr, grid, C_::THREADS, C_::FIXED + static_cast<size_t>(x_bytes), 1, st);
-    e = cudaLaunchKernelEx(&cfg, k_decode<FMT, OP, NT, SEG>, a);
+    e = cudaLaunchKernelEx(&cfg, k_decode<FMT, OP, NT, SEG, MT>, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     lora_host::count_launch();
     return e;
 }
 
-template <int FMT, int OP, int NT>
+template <int FMT, int OP, int NT, int MT>
 cudaError_t launch_x(const DecodeArgs &a, int sms, cudaStream_t st) {
-    using C_ = Cfg<FMT, OP, NT, false>;
+    using C_ = Cfg<FMT, OP, NT, false, MT>;
     // One CTA an SM, each with as many groups as the fullest has to have: fewer SMs than all of
     // them still draw the whole bandwidth, and none waits for a last one.
-    const int groups = (a.N + ROWS - 1) / ROWS, rounds = (groups + sms - 1) / sms;
+    const int groups = (a.N + C_::GROUP_ROWS - 1) / C_::GROUP_ROWS, rounds = (groups + sms - 1) / sms;
     const int grid = (groups + rounds - 1) / rounds;
     const int64_t S = (a.K + C_::STAGE_K - 1) / C_::STAGE_K;
     // all of x, with 4-bit codes and its blocks' sums
     const int64_t x_bytes = a.M * (S * C_::STAGE_K * 2 + C_::X_PAD) + (FMT == F_Q4 ? S * C_::BLOCKS * 8 * NT * 4 : 0);
-    if (x_bytes <= C_::X_MAX) return launch<FMT, OP, NT, false>(a, grid, x_bytes, st);
+    if (x_bytes <= C_::X_MAX) return launch<FMT, OP, NT, false, MT>(a, grid, x_bytes, st);
     // The longest segments of which two fit.
-    using G_ = Cfg<FMT, OP, NT, true>;
+    using G_ = Cfg<FMT, OP, NT, true, MT>;
     static_assert(G_::X_MAX / 2 >= 8 * NT * (G_::STAGE_K * 2 + G_::X_PAD), "one stage of x");
-    const int64_t most = (G_::X_MAX / 2 / a.M - G_::X_PAD) / (G_::STAGE_K * 2), n_seg = (S + most - 1) / most;
+    const int64_t seg_S = (a.K + G_::STAGE_K - 1) / G_::STAGE_K;
+    const int64_t most = (G_::X_MAX / 2 / a.M - G_::X_PAD) / (G_::STAGE_K * 2), n_seg = (seg_S + most - 1) / most;
     DecodeArgs seg = a;
-    seg.seg_stages = static_cast<int>((S + n_seg - 1) / n_seg);
-    return launch<FMT, OP, NT, true>(seg, grid, 2 * a.M * (int64_t(seg.seg_stages) * G_::STAGE_K * 2 + G_::X_PAD), st);
+    seg.seg_stages = static_cast<int>((seg_S + n_seg - 1) / n_seg);
+    return launch<FMT, OP, NT, true, MT>(seg, grid, 2 * a.M * (int64_t(seg.seg_stages) * G_::STAGE_K * 2 + G_::X_PAD), st);
 }
 
 // The s.xa kernel asks for the shared-memory split that k_decode needs, so that an SM it runs on
@@ -825,9 +835,28 @@ cudaError_t prepare_xa() {
     return cudaSuccess;
 }
 
+// Groups of 32 rows (two m-tiles) read x once for both.  The gated projections' are such by nature;
+// plain ones take them where the products weigh more than the stream and the fullest CTA has at
+// most a fifth more rows to do: 28672 -> 8192, 8 tokens in FP8 66 -> 60 us and 4-bit 56 -> 50, 16
+// tokens in bf16 106 -> 89 us.  2048 -> 2048, where they leave half the CTAs, 7.1 us -> 7.4 (4-bit, 8
+// tokens); in bf16 up to 8 tokens (11008 -> 4096, one token) 18.0 -> 18.6; codebook, 16 tokens
+// of 11008 -> 4096, 24 -> 31.
+template <int FMT, int OP, int NT>
+cudaError_t launch_mt(const DecodeArgs &a, int sms, cudaStream_t st) {
+    if constexpr (OP == D_GLU) {
+        return launch_x<FMT, OP, NT, 2>(a, sms, st);
+    } else {
+        if constexpr (NT == 1 ? FMT != F_BF16 : FMT != F_CB) {
+            auto rounds = [&](int rows) { return ((a.N + rows - 1) / rows + sms - 1) / sms; };
+            if (2 * rounds(2 * ROWS) * 5 <= 6 * rounds(ROWS)) return launch_x<FMT, OP, NT, 2>(a, sms, st);
+        }
+        return launch_x<FMT, OP, NT, 1>(a, sms, st);
+    }
+}
+
 template <int FMT, int OP>
 cudaError_t launch_nt(const DecodeArgs &a, int sms, cudaStream_t st) {
-    return a.M <= 8 ? launch_x<FMT, OP, 1>(a, sms, st) : launch_x<FMT, OP, 2>(a, sms, st);
+    return a.M <= 8 ? launch_mt<FMT, OP, 1>(a, sms, st) : launch_mt<FMT, OP, 2>(a, sms, st);
 }
 
 template <int OP>

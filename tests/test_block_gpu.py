@@ -624,7 +624,7 @@ def test_threads_on_one_stream():
         assert len(got[i]) == 60 and all(torch.equal(a, b) for g in got[i] for a, b in zip(g, alone[i]))
 
 
-# A few tokens whose x does not fit into shared memory whole: several segments of it (the last one
+# A few tokens.  x does not fit into shared memory whole: several segments of it (the last one
 # shorter), one group of rows per CTA or more than share a segment, the last batch not full.
 # M, d_in, d_out, r, format
 FEW = [
@@ -640,6 +640,17 @@ FEW = [
     (7, 12992, 5008, 16, "nf4"),
     (16, 5072, 9616, 16, "fp8"),
     (6, 20016, 1008, 16, "fp8"),
+    # groups of 32 rows, x whole and in segments, the last group with a first half only
+    (12, 520, 4112, 16, "bf16"),
+    (16, 5064, 4112, 24, "bf16"),
+    (4, 512, 4112, 16, "q4"),
+    (13, 576, 4112, 16, "q4"),
+    (8, 12992, 4112, 16, "q4"),
+    (7, 576, 4112, 16, "nf4"),
+    (8, 13056, 4112, 16, "nf4"),
+    (1, 528, 4112, 16, "fp8"),
+    (11, 528, 4112, 16, "fp8"),
+    (8, 13072, 4112, 16, "fp8"),
 ]
 
 
