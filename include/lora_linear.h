@@ -525,8 +525,8 @@ LORA_API lora_status_t lora_qk_norm_rope_fwd(int dtype, const lora_heads_t *q, c
  *   dq, dk          outputs; each may be its dq_out / dk_out, in place.
  *   dq_weight, dk_weight  outputs [D] (fp32; with dtype | LORA_T_WEIGHT_GRADS of dtype itself,
  *                  rounded once from the fp32 sums), or NULL.
- * A token whose position is outside the table makes its dq, dk and the weights' gradients
- * NaN.  Sums run in a fixed order for given sizes: the same call gives the same bits.
+ * A token whose position is outside the table makes its dq and dk NaN, and the weights'
+ * gradients in the rotated dimensions.  Sums run in a fixed order for given sizes: the same call gives the same bits.
  * Workspace: lora_qk_norm_rope_workspace_size(M, heads of q + heads of k, D) bytes, 256-byte aligned
  * (it need not be zeroed); may be NULL when neither weight gradient is asked for.
  */

@@ -10,9 +10,12 @@
 // lane: the vector with dimension j and the one with its partner j + rot/2, so the rotation
 // needs no exchange), a warp holds 32 / L heads of one token at a time and goes through the
 // token's heads (or a range of them, where tokens are few) with several heads' loads in
-// flight; the token's cos and sin stay in registers over its heads, so the fp32 tables,
-// as wide as a head itself, are read once a token instead of once a head.  The backward
-// forms sum v^2 and sum v dn w in the same shuffles.
+// flight (forward in registers; the backward, whose registers the two inputs and the weight
+// gradients fill, through shared memory by asynchronous copies, each lane its own: 8192 tokens of
+// 40 heads of 128 in bf16 61 -> 55 us, 252 MB at 4.6 TB/s); the token's cos and sin stay in
+// registers over its heads, so the fp32 tables, as wide as a head itself, are read once a
+// token instead of once a head.  The backward forms sum v^2 and sum v dn w in the same
+// shuffles.
 //
 // The weight gradients are summed per lane over a CTA's whole share in fp32, over the CTA
 // in shared memory, and over the CTAs by a second kernel, each in a fixed order.
@@ -23,6 +26,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/lora_linear.h"
 #include "block.h"
@@ -33,13 +37,14 @@ namespace {
 using namespace lora;
 
 constexpr int WARPS = 8;
-// Heads of a group in flight.  Forward: two, at three CTAs an SM (16384 tokens of 40 heads of
+// Heads of a group at a time.  Forward: two, at three CTAs an SM (16384 tokens of 40 heads of
 // 128 in bf16: 61 us; three heads at three CTAs 69, two at four 68, four at two 72, registers
-// spilling or loads too few).  Backward, two inputs: one where a vector holds 8 elements (8192
-// tokens: 60 us; two 61, spilling), two where it holds 4 (1999 tokens of 10 fp32 heads: 11.4 us
-// against 14.0).
+// spilling or loads too few).  Backward, whose loads run ahead through shared memory: one, three
+// steps of it, where a vector holds 8 elements (8192 tokens: 55 us; with loads to registers
+// 61); two, two steps, where it holds 4.
 constexpr int FWD_HEADS = 2;
 __host__ __device__ constexpr int bwd_heads(int V) { return V == 4 ? 2 : 1; }
+__host__ __device__ constexpr int bwd_stages(int V) { return V == 4 ? 2 : 3; }
 constexpr int SMS = 148;
 
 // One of q and k.
@@ -154,6 +159,15 @@ struct Vec {
             w[0] = v.x, w[1] = v.y;
         }
     }
+    __device__ void load_shared(const uint8_t *p) {
+        if constexpr (W == 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        }
+    }
     __device__ void store(T *p) const {
         // written once: streaming stores keep them from evicting what is still to be read
         // (16384 tokens of 40 heads of 128 in bf16: 65.7 -> 62.5 us)
@@ -211,44 +225,43 @@ struct Lane {
     // and 1); INTER, of each slot's pairs, an angle twice.  Without a rotation 1 and 0; a
     // position outside the table reads nothing and gives NaN.
     static constexpr int TURNS = INTER ? 2 : 1;
-    __device__ void angles(const HeadArgs &a, int64_t pos, f2 (&c)[TURNS][P], f2 (&s)[TURNS][P]) const {
+    static constexpr int FLOATS = INTER ? V / 2 : V;   // angles of a turn
+    __device__ bool turns(int rot, int i) const { return rot > 0 && has[i] && (!INTER || off[i] < rot); }
+    __device__ int first_angle(int i) const { return INTER ? off[i] / 2 : off[0]; }
+
+    // from the turns' angles, cos and sin: read(i, e, sine) gives angles e, e + 1 of turn i
+    template <class Read>
+    __device__ void angles(int rot, float bad, f2 (&c)[TURNS][P], f2 (&s)[TURNS][P], Read read) const {
 #pragma unroll
-        for (int i = 0; i < TURNS; ++i)
+        for (int i = 0; i < TURNS; ++i) {
 #pragma unroll
             for (int e = 0; e < P; ++e) {
                 c[i][e] = pack2(1.0f, 1.0f);
                 s[i][e] = 0;
             }
-        if (a.rot == 0) return;
-        const bool ok = pos >= 0 && pos < a.n_pos;
-        const float bad = ok ? 0.0f : __int_as_float(0x7fc00000);
-        const float *cr = a.cos + (ok ? pos * (a.rot / 2) : 0), *sr = a.sin + (ok ? pos * (a.rot / 2) : 0);
-        if constexpr (INTER) {
+            if (!turns(rot, i)) continue;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!has[i] || off[i] >= a.rot) continue;
-#pragma unroll
-                for (int e = 0; e < P; e += 2) {  // entry e belongs to the elements 2 e, 2 e + 1
-                    const float2 fc = __ldg(reinterpret_cast<const float2 *>(cr + off[i] / 2 + e));
-                    const float2 fs = __ldg(reinterpret_cast<const float2 *>(sr + off[i] / 2 + e));
+            for (int e = 0; e < FLOATS; e += 2) {
+                const float2 fc = read(i, e, 0), fs = read(i, e, 1);
+                if constexpr (INTER) {  // angle e belongs to the elements 2 e, 2 e + 1
                     c[i][e] = pack2(fc.x + bad, fc.x + bad);
                     c[i][e + 1] = pack2(fc.y + bad, fc.y + bad);
                     s[i][e] = pack2(fs.x, fs.x);
                     s[i][e + 1] = pack2(fs.y, fs.y);
+                } else {
+                    c[i][e / 2] = pack2(fc.x + bad, fc.y + bad);
+                    s[i][e / 2] = pack2(fs.x, fs.y);
                 }
             }
-        } else {
-            if (!has[0]) return;
-#pragma unroll
-            for (int e = 0; e < P; e += 2) {
-                const float4 fc = __ldg(reinterpret_cast<const float4 *>(cr + off[0] + 2 * e));
-                const float4 fs = __ldg(reinterpret_cast<const float4 *>(sr + off[0] + 2 * e));
-                c[0][e] = pack2(fc.x + bad, fc.y + bad);
-                c[0][e + 1] = pack2(fc.z + bad, fc.w + bad);
-                s[0][e] = pack2(fs.x, fs.y);
-                s[0][e + 1] = pack2(fs.z, fs.w);
-            }
         }
+    }
+    __device__ void angles(const HeadArgs &a, int64_t pos, f2 (&c)[TURNS][P], f2 (&s)[TURNS][P]) const {
+        const bool ok = pos >= 0 && pos < a.n_pos;
+        const int64_t at = a.rot && ok ? pos * (a.rot / 2) : 0;
+        const float *cr = a.cos + at, *sr = a.sin + at;
+        angles(a.rot, ok ? 0.0f : __int_as_float(0x7fc00000), c, s, [&](int i, int e, int sine) {
+            return __ldg(reinterpret_cast<const float2 *>((sine ? sr : cr) + first_angle(i) + e));
+        });
     }
     static __device__ f2 partner(const f2 (&v)[SLOTS][P], int i, int e) { return INTER ? swap2(v[i][e]) : v[1 - i][e]; }
 };
@@ -408,10 +421,33 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 2 : 3) k_heads_fwd(const __gr
 }
 
 // ------------------------------------------------------------------ backward
+// Each lane copies its own part of the heads ahead of their use to shared memory (and reads it back
+// itself: no barrier), a ring of BWD_STAGES steps, and with a unit's first step its angles.
+template <class T, int V, int SL>
+struct BwdRing {
+    static constexpr int VEC = V * sizeof(T);            // bytes of a vector
+    static constexpr int HEADS = bwd_heads(V), STAGES = bwd_stages(V);
+    static constexpr int HEAD = 2 * SL * VEC * 32;        // a warp's x and dy of a head a group
+    static constexpr int STEP = HEADS * HEAD;
+    static constexpr int TURN = 2 * V * 4 * 32;           // and cos and sin of a unit
+    static constexpr int WARP = STAGES * (STEP + TURN);
+    static constexpr int BYTES = WARPS * WARP;
+};
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <class T, int V, bool INTER, int NS>
 __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __grid_constant__ HeadArgs a) {
     using LaneT = Lane<V, INTER, NS>;
-    constexpr int SL = LaneT::SLOTS, P = V / 2, BWD_HEADS = bwd_heads(V);
+    constexpr int SL = LaneT::SLOTS, P = V / 2;
+    using R = BwdRing<T, V, SL>;
+    constexpr int S = R::STAGES, H = R::HEADS;
+    extern __shared__ __align__(16) uint8_t ring_all[];
     __shared__ float red[WARPS][256];
     grid_dep_wait();
     grid_dep_launch_dependents();
@@ -430,48 +466,129 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
     for (int i = 0; i < SL; ++i)
 #pragma unroll
         for (int e = 0; e < P; ++e) dw[i][e] = 0;
-    const int64_t stride = static_cast<int64_t>(t.ctas) * WARPS;
-    int64_t u = static_cast<int64_t>(cta) * WARPS + warp;
-    int h_lo = 0;
-    int64_t token = u < t.units ? unit_token(t, u, h_lo) : 0;
-    int64_t pos = u < t.units ? position(a, token) : 0;  // one unit ahead of its use
-    while (u < t.units) {
-        const int h_hi = min(t.heads, h_lo + t.per_unit);
-        const T *in = static_cast<const T *>(t.in) + token * t.in_ts + (h_lo + g) * t.in_hs;
-        const T *dy = static_cast<const T *>(t.dy) + token * t.dy_ts + (h_lo + g) * t.dy_hs;
-        T *out = static_cast<T *>(t.out) + token * t.out_ts + (h_lo + g) * t.out_hs;
-        int next_lo = 0;
-        int64_t next_token = 0;
-        f2 c[LaneT::TURNS][P], s[LaneT::TURNS][P];
-        for (int h0 = h_lo; h0 < h_hi; h0 += G * BWD_HEADS) {
-            Vec<T, V> x[BWD_HEADS][SL], d[BWD_HEADS][SL];
+    uint8_t *ring = ring_all + warp * R::WARP + lane * R::VEC;         // slots of a lane: 32 vectors apart
+    uint8_t *turn = ring_all + warp * R::WARP + S * R::STEP;            // [S][cos, sin][lane][V]
+    // this warp's units: u0, u0 + stride, ..., as (token, split) without a division each
+    const int stride = t.ctas * WARPS, u0 = cta * WARPS + warp;
+    const int d_token = stride / t.splits, d_split = stride - d_token * t.splits;
+    struct Unit {
+        int64_t token;
+        int split;
+    };
+    const int64_t M = t.units / t.splits;
+    const Unit first{u0 / t.splits, u0 % t.splits};
+    auto step = [&](Unit &v) {
+        v.token += d_token;
+        v.split += d_split;
+        if (v.split >= t.splits) {
+            v.split -= t.splits;
+            ++v.token;
+        }
+    };
+
+    // the copies' cursor: a step is one head a group of lanes
+    Unit fu = first;
+    int64_t f_pos = 0, f_next = fu.token < M ? position(a, fu.token) : 0;  // a position is loaded a unit ahead
+    int f_lo = 0, f_h = 0, f_hi = 0, f_slot = 0, f_turn = 0;
+    const T *f_in = nullptr, *f_dy = nullptr;
+    auto enter = [&]() {
+        const int64_t token = fu.token;
+        if (token >= M) return;
+        f_lo = fu.split * t.per_unit;
+        f_h = f_lo;
+        f_hi = min(t.heads, f_lo + t.per_unit);
+        f_in = static_cast<const T *>(t.in) + token * t.in_ts + (f_lo + g) * t.in_hs;
+        f_dy = static_cast<const T *>(t.dy) + token * t.dy_ts + (f_lo + g) * t.dy_hs;
+        f_pos = f_next;
+        Unit next = fu;
+        step(next);
+        if (next.token < M) f_next = position(a, next.token);
+    };
+    auto fetch = [&]() {
+        if (fu.token < M) {
+            const bool first_step = f_h == f_lo;
 #pragma unroll
-            for (int j = 0; j < BWD_HEADS; ++j) {
-                const bool mine = h0 + g + j * G < h_hi;
+            for (int j = 0; j < H; ++j) {
+                const uint32_t dst = smem_u32(ring + f_slot * R::STEP + j * R::HEAD);
+                if (f_h + g < f_hi)
+#pragma unroll
+                    for (int i = 0; i < SL; ++i)
+                        if (ln.has[i]) {
+                            copy_async<R::VEC>(dst + 2 * i * 32 * R::VEC, f_in + ln.off[i]);
+                            copy_async<R::VEC>(dst + (2 * i + 1) * 32 * R::VEC, f_dy + ln.off[i]);
+                        }
+                f_h += G;
+                f_in += in_step;
+                f_dy += dy_step;
+            }
+            if (first_step && a.rot) {
+                const bool ok = f_pos >= 0 && f_pos < a.n_pos;
+                float *to = reinterpret_cast<float *>(turn + f_turn * R::TURN) + lane * V;
+#pragma unroll
+                for (int i = 0; i < LaneT::TURNS; ++i) {
+                    if (!ln.turns(a.rot, i)) continue;
+                    constexpr int F = LaneT::FLOATS, B = F % 4 ? 8 : 16;
+                    const int64_t at = ok ? f_pos * (a.rot / 2) + ln.first_angle(i) : 0;
+#pragma unroll
+                    for (int e = 0; e < F; e += B / 4) {
+                        if (ok) {
+                            copy_async<B>(smem_u32(to + i * F + e), a.cos + at + e);
+                            copy_async<B>(smem_u32(to + 32 * V + i * F + e), a.sin + at + e);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < B / 4; ++k) to[i * F + e + k] = __int_as_float(0x7fc00000);
+                        }
+                    }
+                }
+                f_turn = f_turn + 1 == S ? 0 : f_turn + 1;
+            }
+            f_slot = f_slot + 1 == S ? 0 : f_slot + 1;
+            if (f_h >= f_hi) {
+                step(fu);
+                enter();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    enter();
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fetch();
+
+    int slot = 0, used_turn = 0;
+    for (Unit u = first; u.token < M; step(u)) {
+        const int64_t token = u.token;
+        const int h_lo = u.split * t.per_unit, h_hi = min(t.heads, h_lo + t.per_unit);
+        T *out = static_cast<T *>(t.out) + token * t.out_ts + (h_lo + g) * t.out_hs;
+        f2 c[LaneT::TURNS][P], s[LaneT::TURNS][P];
+        for (int h0 = h_lo; h0 < h_hi; h0 += G * H) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            Vec<T, V> x[H][SL], d[H][SL];
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const uint8_t *from = ring + slot * R::STEP + j * R::HEAD;
 #pragma unroll
                 for (int i = 0; i < SL; ++i) {
                     x[j][i].clear();
                     d[j][i].clear();
-                    if (mine && ln.has[i]) {
-                        x[j][i].load(in + ln.off[i]);
-                        d[j][i].load(dy + ln.off[i]);
+                    if (h0 + g + j * G < h_hi && ln.has[i]) {
+                        x[j][i].load_shared(from + 2 * i * 32 * R::VEC);
+                        d[j][i].load_shared(from + (2 * i + 1) * 32 * R::VEC);
                     }
                 }
-                in += in_step;
-                dy += dy_step;
             }
+            slot = slot + 1 == S ? 0 : slot + 1;
             if (h0 == h_lo) {
-                ln.angles(a, pos, c, s);
-                u += stride;
-                if (u < t.units) {
-                    next_token = unit_token(t, u, next_lo);
-                    pos = position(a, next_token);
-                }
+                const float *cs = reinterpret_cast<const float *>(turn + used_turn * R::TURN) + lane * V;
+                ln.angles(a.rot, 0.0f, c, s, [&](int i, int e, int sine) {
+                    return *reinterpret_cast<const float2 *>(cs + sine * 32 * V + i * LaneT::FLOATS + e);
+                });
+                if (a.rot) used_turn = used_turn + 1 == S ? 0 : used_turn + 1;
             }
-            f2 dn[BWD_HEADS][SL][P];         // the gradient rotated back
-            float sums[2 * BWD_HEADS];       // of v^2 and of v dn w
+            fetch();  // into the slots of the step before, which has been read
+            f2 dn[H][SL][P];         // the gradient rotated back
+            float sums[2 * H];       // of v^2 and of v dn w
 #pragma unroll
-            for (int j = 0; j < BWD_HEADS; ++j) {
+            for (int j = 0; j < H; ++j) {
                 f2 sq = 0, st = 0;
 #pragma unroll
                 for (int i = 0; i < SL; ++i)
@@ -491,7 +608,7 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
             }
             sum_head(sums, a.log_l);
 #pragma unroll
-            for (int j = 0; j < BWD_HEADS; ++j) {
+            for (int j = 0; j < H; ++j) {
                 const float inv = a.norm ? rsqrtf(sums[2 * j] * a.inv_d + a.eps) : 1.0f;
                 // i (dn w - v i^2 mean(v dn w)) = i dn w + v k
                 const float k = a.norm ? -(inv * inv) * (sums[2 * j + 1] * a.inv_d) * inv : 0.0f;
@@ -512,9 +629,8 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
                 out += out_step;
             }
         }
-        token = next_token;
-        h_lo = next_lo;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.partials) return;
     // over the warp's groups, then over the CTA's warps
 #pragma unroll
@@ -632,11 +748,30 @@ void fill_units(HeadTensor &t, int64_t M, int group_heads, int batch, int64_t wa
     t.units = M * t.splits;
 }
 
+// A kernel's limit of dynamic shared memory raised, once a device.
+template <auto *KERNEL>
+cudaError_t allow_shared(int bytes) {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int d = 0;
+    const cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    const std::lock_guard<std::mutex> lk(mu);
+    if (done[d]) return cudaSuccess;
+    const cudaError_t s = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    done[d] = s == cudaSuccess;
+    return s;
+}
+
 template <class T, int V, bool INTER, int NS>
 cudaError_t launch(const HeadArgs &a, bool bwd, cudaStream_t st) {
-    if (bwd)
-        return lora_host::launch_pdl(k_heads_bwd<T, V, INTER, NS>, dim3(a.t[0].ctas + a.t[1].ctas), dim3(WARPS * 32), 0,
+    if (bwd) {
+        constexpr int BYTES = BwdRing<T, V, Lane<V, INTER, NS>::SLOTS>::BYTES;
+        const cudaError_t e = allow_shared<k_heads_bwd<T, V, INTER, NS>>(BYTES);
+        if (e != cudaSuccess) return e;
+        return lora_host::launch_pdl(k_heads_bwd<T, V, INTER, NS>, dim3(a.t[0].ctas + a.t[1].ctas), dim3(WARPS * 32), BYTES,
                                      st, a);
+    }
     const int64_t ctas = (a.t[0].units + a.t[1].units + WARPS - 1) / WARPS;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
     return lora_host::launch_pdl(k_heads_fwd<T, V, INTER, NS>, dim3(static_cast<unsigned>(ctas)), dim3(WARPS * 32), 0,

@@ -262,3 +262,36 @@ def test_autograd_on_the_stacked_projection():
     assert torch.equal(dh2[:, (hq + hk) * D:], dv.reshape(M, -1))
     empty = block.qkv_heads(h[:0], hq, hk, D, wq, wk, cos, sin, pos[:0])
     assert [t.shape[0] for t in empty] == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype,D,rot", [(torch.bfloat16, 256, 128), (torch.float16, 72, 24), (torch.float32, 256, 64)])
+def test_backward_runs_ahead_of_itself(dtype, D, rot):
+    """Many units for each warp, of one step and of several, their loads in flight while others are
+    computed: in place (dq over dq_out), with positions outside the table here and there, twice."""
+    g = torch.Generator().manual_seed(31)
+    M, hq, hk = 3000, 9, 1
+    q, k, dq, dk = (torch.randn(M, h, D, generator=g).to(dtype).cuda() for h in (hq, hk, hq, hk))
+    w = (1 + 0.1 * torch.randn(2, D, generator=g)).to(dtype).cuda()
+    cos, sin = block.rope_table(512, rot, device="cuda")
+    pos = torch.randint(0, 512, (M,), generator=g).cuda()
+    bad = torch.arange(0, M, 97, device="cuda")
+    good = torch.ones(M, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    ws = torch.empty(L.lora_qk_norm_rope_workspace_size(M, hq + hk, D), dtype=torch.uint8, device="cuda")
+    runs = []
+    for p in (pos, pos.clone().index_fill_(0, bad, -5), pos):
+        oq, ok = dq.clone(), dk.clone()
+        dw = torch.empty(2, D, device="cuda")
+        L.lora_qk_norm_rope_bwd(oq, ok, q, k, w[0], w[1], cos, sin, p, oq, ok, dw[0], dw[1], ws, EPS)
+        runs.append((oq, ok, dw))
+    for a, b in zip(runs[0], runs[2]):
+        assert torch.equal(a, b)
+    for a, b in zip(runs[0][:2], runs[1][:2]):
+        assert torch.equal(a[good], b[good]) and b[bad].isnan().all()
+    # dw_j = sum dn_j e_j: only the rotated dimensions see the angles
+    assert runs[1][2][:, :rot].isnan().all() and torch.equal(runs[1][2][:, rot:], runs[0][2][:, rot:])
+    c64, s64 = cos[pos].double(), sin[pos].double()
+    for t, wt, dy, got, dw in ((q, w[0], dq, runs[0][0], runs[0][2][0]), (k, w[1], dk, runs[0][1], runs[0][2][1])):
+        _, _, dx, db, want, wb = _reference(t, wt, c64, s64, False, True, dy)
+        _check("dx", got, dx, db)
+        _check("dw", dw, want, wb)
