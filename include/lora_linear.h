@@ -445,7 +445,7 @@ LORA_API lora_status_t lora_glu_bwd(const uint16_t *dP, const uint16_t *gu, cons
  * Projection with bias, activation and residual in its epilogue:
  *     pre = x.W^T + s.(x.A^T).B^T + bias        out = act(pre) + residual
  *   bias      [d_out] (bf16) or NULL;  residual [M, d_out] (bf16) or NULL.
- *   out       output [M, d_out] (bf16), rounded once from fp32.
+ *   out       output [M, d_out] (bf16), rounded once from fp32.  It may be residual, in place.
  *   pre_save  optional output [M, d_out] (bf16): pre, for the backward of an activation.
  * Everything else as lora_linear_fwd; the workspace is that of
  * lora_linear_act_workspace_size(the format's forward op, ...).  Needs CTA pairs for more

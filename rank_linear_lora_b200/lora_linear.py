@@ -635,7 +635,7 @@ def lora_glu_bwd(dP, gu, x, W, A, B, xa_save, dGU, dX, dA, dB, alpha, act, ws, s
 
 def lora_linear_act_fwd(x, W, A, B, bias, residual, out, pre_save, xa_save, alpha, act, ws, stream=None):
     """out = act(x.W^T + s.(x.A^T).B^T + bias) + residual; W: a bf16 tensor or a FrozenWeight;
-    bias [d_out], residual, pre_save [M, d_out] and xa_save may each be None."""
+    bias [d_out], residual, pre_save [M, d_out] and xa_save may each be None; out may be residual."""
     code, dev = _act(act), torch.cuda.current_device()
     w, n, d_in, keep = _weight(W, dev)
     M, r = x.shape[0], A.shape[0]

@@ -190,6 +190,22 @@ def test_linear_act_forward(case, save):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("M,d,n,fmt", [(1, 264, 136, "bf16"), (16, 5064, 4112, "bf16"), (17, 520, 264, "bf16"),
+                                       (33, 4104, 520, "bf16"), (300, 336, 392, "fp8"), (200, 4160, 264, "q4"),
+                                       (1280, 2056, 4096, "bf16"), (1280, 264, 4104, "bf16")])
+def test_residual_in_place(M, d, n, fmt):
+    """out over residual: each element is read before it is written, by the thread that writes it."""
+    y = Layer(M, d, n, 16, fmt, seed=61)
+    ws = L.act_workspace(y.wt.ops()[0], M, d, n, 16)
+    want = _bf(M, n)
+    L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, y.residual, want, None, None, y.alpha, "silu", ws)
+    for _ in range(5):
+        got = y.residual.clone()
+        L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, got, got, None, None, y.alpha, "silu", ws)
+        assert torch.equal(got, want)
+    L.lora_linear_check(ws)
+
+
 ACT_BWD = [
     (1, 264, 136, 16, "bf16", "none", True),
     (1, 264, 8, 16, "bf16", "gelu", True),
