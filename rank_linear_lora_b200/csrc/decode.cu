@@ -30,8 +30,9 @@
 // with x's fragments read from L2 stage by stage it was 151 and 170).
 //
 // Codes are widened in registers, and no decoded weight is rounded.  A 4-bit code under the
-// exponent of 128 is 128 + q; the products take that, and 136 times the block's sum of x
-// comes off afterwards, since the code stands for q - 8.  E4M3
+// exponent of 128 is 128 + q, and stands for q - 8: the products take 128 + q and start from -136
+// times the block's sum of x (8192 -> 2 x 28672, four tokens: 64.3 us, with an addition
+// afterwards 65.5; 621 instructions a stage, 0.56 issued a cycle and scheduler).  E4M3
 // codes enter with their exact values.  The scale (one a row, or one a row and 64 k, fetched
 // a tile ahead) multiplies the fp32 sums.  Codebook values are rounded once to bf16 and looked
 // up two codes at a time in a table of a byte's 256 pairs, a copy in every bank.
@@ -70,7 +71,7 @@ struct Cfg {
     static constexpr bool NIBBLE = FMT == F_Q4 || FMT == F_CB;
     static constexpr int GROUP_ROWS = OP == D_GLU ? ROWS : MT * ROWS;  // of each projection
     // Widening 4-bit codes is bound by instructions, not by memory: more warps, and the ring they
-    // leave room for (8192 -> 2 x 28672, four tokens: 66 us; 8 warps x 4 stages 78, 16 x 2, which
+    // leave room for (8192 -> 2 x 28672, four tokens: 64 us; 8 warps x 4 stages 78, 16 x 2, which
     // spill, 94).  The other formats stream at 8 x 4 (4096 -> 2 x 11008 in bf16, one token: 30 us).
     // With x in segments a 4-bit stage is one box, so that a short segment still has stages for all
     // warps, and 12 warps pay only where their sums leave the segments room (28672 -> 8192 in groups
@@ -109,6 +110,13 @@ __device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// From C = (lo, hi) in both rows.
+__device__ __forceinline__ void mma_bf16_from(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float lo, float hi) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(lo), "f"(hi));
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
@@ -500,6 +508,13 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
                     // Widening alternates with the products of the m-tiles, so that a product's latency is spent
                     // on the next one's operands.
                     float p4[MT][NT][4], xo[NT][4];  // xo: -136 times the sum of x, of the lane's tokens
+                    if constexpr (FMT == F_Q4 && !SEG) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 v = lds8(xsum0 + ((s * BLOCKS + b) * 8 * NT + n * 8) * 4);
+                            xo[n][0] = __uint_as_float(v.x), xo[n][1] = __uint_as_float(v.y);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -510,7 +525,9 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 if constexpr (C_::NIBBLE) {
-                                    if (i == 0) mma_bf16_zero(p4[m][n], a0, a1, a2, a3, xb[n][0], xb[n][1]);
+                                    if (i == 0 && FMT == F_Q4 && !SEG)
+                                        mma_bf16_from(p4[m][n], a0, a1, a2, a3, xb[n][0], xb[n][1], xo[n][0], xo[n][1]);
+                                    else if (i == 0) mma_bf16_zero(p4[m][n], a0, a1, a2, a3, xb[n][0], xb[n][1]);
                                     else mma_bf16(p4[m][n], a0, a1, a2, a3, xb[n][2 * i], xb[n][2 * i + 1]);
                                 } else {
                                     mma_bf16(acc[m][n], a0, a1, a2, a3, xb[n][2 * i], xb[n][2 * i + 1]);
@@ -526,13 +543,6 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
                             }
                         }
                     }
-                    if constexpr (FMT == F_Q4 && !SEG) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const uint2 v = lds8(xsum0 + ((s * BLOCKS + b) * 8 * NT + n * 8) * 4);
-                            xo[n][0] = __uint_as_float(v.x), xo[n][1] = __uint_as_float(v.y);
-                        }
-                    }
                     if constexpr (C_::NIBBLE) {
                         // the block's sums times the scale of each of the lane's rows; a 4-bit code stands for
                         // q - 8 = (128 + q) - 136
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const float v = FMT == F_Q4 ? p4[m][n][e] + xo[n][e & 1] : p4[m][n][e];
+                                    const float v = FMT == F_Q4 && SEG ? p4[m][n][e] + xo[n][e & 1] : p4[m][n][e];
                                     acc[m][n][e] = fmaf(e < 2 ? s0 : s1, v, acc[m][n][e]);
                                 }
                         }
