@@ -666,7 +666,7 @@ FEW = [
     (8, 13056, 4112, 16, "nf4"),
     (1, 528, 4112, 16, "fp8"),
     (11, 528, 4112, 16, "fp8"),
-    (8, 13072, 4112, 16, "fp8"),
+    (8, 13088, 4112, 16, "fp8"),
 ]
 
 
