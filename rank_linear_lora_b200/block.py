@@ -10,7 +10,8 @@
 
 The projections take the frozen weight as a bf16 tensor or as a ``FrozenWeight`` of any format, and
 trainable adapters A, B of the (stacked) layer; gradients flow to x, A, B, the bias and the
-residual.  As ``autograd.lora_linear``: the library's kernels run, or torch's unfused
+residual, in reverse mode, once (a second derivative, or a tensor with a tangent of forward mode,
+is an error).  As ``autograd.lora_linear``: the library's kernels run, or torch's unfused
 composition where the library answers LORA_ERR_UNSUPPORTED or LORA_LINEAR_FUSED=0 asks for
 it (warned once); a missing library raises.
 

@@ -188,6 +188,16 @@ bool trained(const OptTensor &t) { return has(t) && t->requires_grad(); }
 template <class... Ts>
 bool wants_grad(const Ts &...ts) { return at::GradMode::is_enabled() && (trained(ts) || ...); }
 
+// The operators have no forward-mode derivative, and forward mode is on under no_grad too: a result
+// without its tangent would be a wrong one.
+bool has_tangent(const Tensor &t) { return t.defined() && t._fw_grad(/*level=*/0).defined(); }
+bool has_tangent(const OptTensor &t) { return has(t) && has_tangent(*t); }
+template <class... Ts>
+void no_tangents(const char *name, const Ts &...ts) {
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode())
+        TORCH_CHECK_NOT_IMPLEMENTED(!(has_tangent(ts) || ...), name, ": derivatives in forward mode are not implemented");
+}
+
 // What a node keeps besides its tensors.
 struct Kept : torch::CustomClassHolder {
     Weight w;
@@ -286,6 +296,7 @@ struct Glu : torch::autograd::Function<Glu> {
 
 Tensor glu(const Tensor &x, const Tensor &A, const Tensor &B, double alpha, int64_t act, int64_t format, const Tensor &data,
            const OptTensor &scale, const std::vector<float> &codebook) {
+    no_tangents("lora_glu", x, A, B, data, scale);
     const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
     if (wants_grad(x, A, B))
         return Glu::apply(x, A, B, alpha, w, act);
@@ -372,6 +383,7 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
 Tensor linear_act(const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias, const OptTensor &residual,
                   double alpha, int64_t act, int64_t format, const Tensor &data, const OptTensor &scale,
                   const std::vector<float> &codebook) {
+    no_tangents("lora_linear_act", x, A, B, bias, residual, data, scale);
     const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
     if (wants_grad(x, A, B, bias, residual))
         return LinearAct::apply(x, A, B, bias, residual, alpha, w, act);
@@ -563,6 +575,7 @@ struct QkvHeads : torch::autograd::Function<QkvHeads> {
 std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, const OptTensor &wq, const OptTensor &wk,
                                        const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, double eps,
                                        bool interleaved, bool norm) {
+    no_tangents("qk_norm_rope", q_in, k_in, wq, wk, cos, sin);
     const Tensor q = addressable(q_in), k = addressable(k_in);
     if (wants_grad(q, k, wq, wk)) {
         const variable_list o = QkNormRope::apply(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
@@ -574,6 +587,7 @@ std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, c
 std::tuple<Tensor, Tensor, Tensor> qkv_heads(const Tensor &h, const OptTensor &wq, const OptTensor &wk, const OptTensor &cos,
                                              const OptTensor &sin, const OptTensor &positions, int64_t hq, int64_t hk,
                                              int64_t D, double eps, bool interleaved, bool norm) {
+    no_tangents("qkv_heads", h, wq, wk, cos, sin);
     TORCH_CHECK_VALUE(h.dim() == 2 && hq > 0 && hk > 0 && D > 0 && h.size(1) == (hq + 2 * hk) * D, "h: expected ",
                       (hq + 2 * hk) * D, " columns, got ", h.sizes());
     if (wants_grad(h, wq, wk)) {

@@ -1,0 +1,39 @@
+"""The operators around the layer at their edges, on the CPU: what is refused before any device work,
+and the unfused compositions."""
+import ctypes
+
+import pytest
+import torch
+
+from rank_linear_lora_b200 import block
+from rank_linear_lora_b200 import build as B
+from rank_linear_lora_b200 import lora_linear as L
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return L.load_library()
+
+
+def _bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("grad", [True, False], ids=["grad", "no_grad"])
+def test_tangents_are_refused(lib, grad):
+    """Before anything else is looked at."""
+    import torch.autograd.forward_ad as fw
+    x, W, A, Bm, q, h = _bf(4, 64), _bf(96, 64), _bf(8, 64), _bf(96, 8), _bf(4, 2, 16), _bf(4, 96)
+    with torch.set_grad_enabled(grad), fw.dual_level():
+        def dual(t):
+            return fw.make_dual(t, torch.ones_like(t))
+
+        for f in (lambda: block.lora_glu(dual(x), W, A, Bm, 8.0), lambda: block.lora_glu(x, dual(W), A, Bm, 8.0),
+                  lambda: block.lora_linear_act(x, W, A, dual(Bm), 8.0),
+                  lambda: block.lora_linear_act(x, W, A, Bm, 8.0, residual=dual(_bf(4, 96))),
+                  lambda: block.qk_norm_rope(q, dual(q)), lambda: block.qkv_heads(dual(h), 2, 2, 16)):
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                f()

@@ -1,0 +1,60 @@
+"""The operators around the layer at their edges: what a caller may pass and rarely does."""
+import os
+import subprocess
+import sys
+import threading
+
+import pytest
+import torch
+
+from block_cases import F32, HALF, Layer, act64, assert_within
+from rank_linear_lora_b200 import autograd as LA
+from rank_linear_lora_b200 import block
+from rank_linear_lora_b200 import lora_linear as L
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _bf(*shape):
+    return torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+
+
+def _heads_inputs(M, hq, hk, D, rot, seed=0, dtype=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    h = torch.randn(M, (hq + 2 * hk) * D, generator=g).to(dtype).cuda()
+    w = (1 + 0.1 * torch.randn(2, D, generator=g)).to(dtype).cuda()
+    cos, sin = block.rope_table(64, rot, device="cuda")
+    return h, w[0], w[1], cos, sin, torch.randint(0, 64, (M,), generator=g).cuda()
+
+
+def _split(h, hq, hk, D):
+    return h[:, :hq * D].unflatten(1, (hq, D)), h[:, hq * D:(hq + hk) * D].unflatten(1, (hk, D))
+
+
+@pytest.mark.parametrize("grad", [True, False], ids=["grad", "no_grad"])
+def test_forward_mode_is_an_error(grad):
+    """Tangents do not go through the kernels: a dual tensor is refused (not computed without its
+    tangent), with gradients enabled or not, wherever it comes in; and taken where forward mode is off."""
+    import torch.autograd.forward_ad as fw
+    y = Layer(20, 64, 96, 8, seed=1)
+    W = y.wt.tensors[0]
+    h, wq, wk, cos, sin, pos = _heads_inputs(20, 3, 2, 32, 16)
+    q, k = (t.contiguous() for t in _split(h, 3, 2, 32))
+    calls = [
+        (lambda x, A, B, W: block.lora_glu(x, W, A, B, y.alpha), (y.x, y.A, y.B, W)),
+        (lambda x, A, B, W, b, r: block.lora_linear_act(x, W, A, B, y.alpha, bias=b, residual=r),
+         (y.x, y.A, y.B, W, y.bias, y.residual)),
+        (lambda q, k, a, b, c, s: block.qk_norm_rope(q, k, a, b, c, s, pos), (q, k, wq, wk, cos, sin)),
+        (lambda h, a, b, c, s: block.qkv_heads(h, 3, 2, 32, a, b, c, s, pos), (h, wq, wk, cos, sin)),
+    ]
+    with torch.set_grad_enabled(grad), fw.dual_level():
+        for f, args in calls:
+            for i, t in enumerate(args):
+                dual = fw.make_dual(t, torch.ones_like(t))
+                with pytest.raises(NotImplementedError, match="forward mode"):
+                    f(*args[:i], dual, *args[i + 1:])
+                with fw._set_fwd_grad_enabled(False):
+                    f(*args[:i], dual, *args[i + 1:])
+            f(*args)
