@@ -13,7 +13,9 @@ trainable adapters A, B of the (stacked) layer; gradients flow to x, A, B, the b
 residual, in reverse mode, once (a second derivative, or a tensor with a tangent of forward mode,
 is an error).  As ``autograd.lora_linear``: the library's kernels run, or torch's unfused
 composition where the library answers LORA_ERR_UNSUPPORTED or LORA_LINEAR_FUSED=0 asks for
-it (warned once); a missing library raises.
+it (warned once); a missing library raises.  Activations, adapters, biases, norm weights and
+gradients may start at any address (one off a 16-byte boundary is copied); frozen weights and the
+rotation's tables start at multiples of 16 bytes.
 
 Workspaces are kept per device, stream and shape, so calls on two streams never share one;
 a call that is being captured into a CUDA graph takes a workspace of its own from the

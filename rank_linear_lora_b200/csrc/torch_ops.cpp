@@ -108,6 +108,14 @@ Weight make_weight(int64_t format, const Tensor &data, const OptTensor &scale, c
     return w;
 }
 
+// The library reads 16 bytes at a time: a tensor that starts elsewhere is copied (contiguous tensors
+// keep their layout).  Frozen weights and the rotation's tables are not: a copy a call would hide
+// what it costs, so the library refuses them.
+Tensor on_16_bytes(const Tensor &t) {
+    return t.defined() && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 ? t.clone() : t;
+}
+OptTensor on_16_bytes(const OptTensor &t) { return has(t) ? OptTensor(on_16_bytes(*t)) : t; }
+
 Tensor new_bf16(const Tensor &like, at::IntArrayRef shape) { return at::empty(shape, like.options().dtype(at::kBFloat16)); }
 
 // fp32 gradients of bf16 parameters next to each other, and all of them rounded to bf16 by one
@@ -278,7 +286,7 @@ struct Glu : torch::autograd::Function<Glu> {
         const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
         Tensor dX = ctx->needs_input_grad(0) ? at::empty_like(x) : Tensor();
         if (M == 0) return once({dX, at::zeros_like(A), at::zeros_like(B), Tensor(), Tensor(), Tensor()}, up);
-        const Tensor dP = up[0].contiguous();
+        const Tensor dP = on_16_bytes(up[0].contiguous());
         need(dP, "the gradient of p", at::kBFloat16, {M, n / 2}, dev);
         const Grads d({A, B});
         const Tensor dGU = at::empty_like(gu);
@@ -294,9 +302,10 @@ struct Glu : torch::autograd::Function<Glu> {
     }
 };
 
-Tensor glu(const Tensor &x, const Tensor &A, const Tensor &B, double alpha, int64_t act, int64_t format, const Tensor &data,
-           const OptTensor &scale, const std::vector<float> &codebook) {
-    no_tangents("lora_glu", x, A, B, data, scale);
+Tensor glu(const Tensor &x_in, const Tensor &A_in, const Tensor &B_in, double alpha, int64_t act, int64_t format,
+           const Tensor &data, const OptTensor &scale, const std::vector<float> &codebook) {
+    no_tangents("lora_glu", x_in, A_in, B_in, data, scale);
+    const Tensor x = on_16_bytes(x_in), A = on_16_bytes(A_in), B = on_16_bytes(B_in);
     const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
     if (wants_grad(x, A, B))
         return Glu::apply(x, A, B, alpha, w, act);
@@ -364,7 +373,7 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
         if (M == 0)
             return once({dX, at::zeros_like(A), at::zeros_like(B), want_bias ? at::zeros_like(bias) : Tensor(), dRes, Tensor(),
                          Tensor(), Tensor()}, up);
-        const Tensor dOut = up[0].contiguous();
+        const Tensor dOut = on_16_bytes(up[0].contiguous());
         need(dOut, "the gradient of out", at::kBFloat16, {M, n}, dev);
         const Grads d({A, B, want_bias ? bias : Tensor()});
         const Tensor dPre = k.act != LORA_ACT_NONE ? at::empty_like(dOut) : Tensor();
@@ -380,10 +389,12 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
     }
 };
 
-Tensor linear_act(const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias, const OptTensor &residual,
-                  double alpha, int64_t act, int64_t format, const Tensor &data, const OptTensor &scale,
-                  const std::vector<float> &codebook) {
-    no_tangents("lora_linear_act", x, A, B, bias, residual, data, scale);
+Tensor linear_act(const Tensor &x_in, const Tensor &A_in, const Tensor &B_in, const OptTensor &bias_in,
+                  const OptTensor &residual_in, double alpha, int64_t act, int64_t format, const Tensor &data,
+                  const OptTensor &scale, const std::vector<float> &codebook) {
+    no_tangents("lora_linear_act", x_in, A_in, B_in, bias_in, residual_in, data, scale);
+    const Tensor x = on_16_bytes(x_in), A = on_16_bytes(A_in), B = on_16_bytes(B_in);
+    const OptTensor bias = on_16_bytes(bias_in), residual = on_16_bytes(residual_in);
     const Weight w = make_weight(format, data, scale, codebook, c10::cuda::current_device());
     if (wants_grad(x, A, B, bias, residual))
         return LinearAct::apply(x, A, B, bias, residual, alpha, w, act);
@@ -408,7 +419,7 @@ Tensor addressable(const Tensor &t) {
     if (t.stride(2) == 1 && named(M, t.stride(0)) && named(H, t.stride(1)) &&
         reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
         return t;
-    return t.contiguous();
+    return on_16_bytes(t.contiguous());
 }
 
 lora_heads_t heads(const Tensor &t, const char *name, const Tensor &like, int dev) {
@@ -572,11 +583,12 @@ struct QkvHeads : torch::autograd::Function<QkvHeads> {
     }
 };
 
-std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, const OptTensor &wq, const OptTensor &wk,
+std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, const OptTensor &wq_in, const OptTensor &wk_in,
                                        const OptTensor &cos, const OptTensor &sin, const OptTensor &positions, double eps,
                                        bool interleaved, bool norm) {
-    no_tangents("qk_norm_rope", q_in, k_in, wq, wk, cos, sin);
+    no_tangents("qk_norm_rope", q_in, k_in, wq_in, wk_in, cos, sin);
     const Tensor q = addressable(q_in), k = addressable(k_in);
+    const OptTensor wq = on_16_bytes(wq_in), wk = on_16_bytes(wk_in);
     if (wants_grad(q, k, wq, wk)) {
         const variable_list o = QkNormRope::apply(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
         return {o[0], o[1]};
@@ -584,10 +596,12 @@ std::pair<Tensor, Tensor> qk_norm_rope(const Tensor &q_in, const Tensor &k_in, c
     return heads_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
 }
 
-std::tuple<Tensor, Tensor, Tensor> qkv_heads(const Tensor &h, const OptTensor &wq, const OptTensor &wk, const OptTensor &cos,
-                                             const OptTensor &sin, const OptTensor &positions, int64_t hq, int64_t hk,
-                                             int64_t D, double eps, bool interleaved, bool norm) {
-    no_tangents("qkv_heads", h, wq, wk, cos, sin);
+std::tuple<Tensor, Tensor, Tensor> qkv_heads(const Tensor &h_in, const OptTensor &wq_in, const OptTensor &wk_in,
+                                             const OptTensor &cos, const OptTensor &sin, const OptTensor &positions,
+                                             int64_t hq, int64_t hk, int64_t D, double eps, bool interleaved, bool norm) {
+    no_tangents("qkv_heads", h_in, wq_in, wk_in, cos, sin);
+    const Tensor h = on_16_bytes(h_in);
+    const OptTensor wq = on_16_bytes(wq_in), wk = on_16_bytes(wk_in);
     TORCH_CHECK_VALUE(h.dim() == 2 && hq > 0 && hk > 0 && D > 0 && h.size(1) == (hq + 2 * hk) * D, "h: expected ",
                       (hq + 2 * hk) * D, " columns, got ", h.sizes());
     if (wants_grad(h, wq, wk)) {

@@ -58,3 +58,44 @@ def test_forward_mode_is_an_error(grad):
                 with fw._set_fwd_grad_enabled(False):
                     f(*args[:i], dual, *args[i + 1:])
             f(*args)
+
+
+def _odd(t):
+    """The same values, contiguous, off every 16-byte boundary."""
+    buf = torch.empty(t.numel() + 3, dtype=t.dtype, device=t.device)
+    v = buf[3:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+def test_tensors_at_odd_offsets():
+    """Inputs, adapters, bias, residual and norm weights off a 16-byte boundary are copied, in every
+    operator; so are gradients, whose place is autograd's choice."""
+    y = Layer(20, 64, 96, 8, seed=4)
+    h, wq, wk, cos, sin, pos = _heads_inputs(20, 3, 2, 32, 16)
+    calls = [
+        (lambda x, A, B: block.lora_glu(x, y.wt, A, B, y.alpha), (y.x, y.A, y.B)),
+        (lambda x, A, B, b, r: block.lora_linear_act(x, y.wt, A, B, y.alpha, bias=b, residual=r, act="silu"),
+         (y.x, y.A, y.B, y.bias, y.residual)),
+        (lambda x, A, B: block.lora_linear_act(x, y.wt, A, B, y.alpha), (y.x, y.A, y.B)),
+        (lambda q, k, a, b: torch.cat(block.qk_norm_rope(q, k, a, b, cos, sin, pos), 1),
+         (*(t.contiguous() for t in _split(h, 3, 2, 32)), wq, wk)),
+        (lambda h, a, b: torch.cat(block.qkv_heads(h, 3, 2, 32, a, b, cos, sin, pos), 1), (h, wq, wk)),
+    ]
+    aux = torch.ones(3, dtype=torch.bfloat16, device="cuda")
+    for f, args in calls:
+        leaves = [t.clone().requires_grad_(True) for t in args]
+        out = f(*leaves)
+        up = torch.randn(out.shape, device="cuda").to(out.dtype)
+        want = torch.autograd.grad(out, leaves, up)
+        odd = [_odd(t).requires_grad_(True) for t in args]
+        with torch.no_grad():
+            assert torch.equal(f(*odd), out)
+        got = f(*odd)
+        assert torch.equal(got, out)
+        # the gradient of `got` is a slice of the gradient of the whole, 3 elements in
+        whole = torch.cat((aux, got.flatten()))
+        grads = torch.autograd.grad(whole, odd, torch.cat((aux, up.flatten())))
+        for a, b in zip(grads, want):
+            assert torch.equal(a, b)
