@@ -716,21 +716,23 @@ size_t dw_bytes(int D) { return (static_cast<size_t>(BWD_CTAS) + 2) * D * sizeof
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// The strides of a tensor as the kernels take them: one over a single token or head leads nowhere,
+// whatever it is.
+int64_t token_stride(const lora_heads_t &t, int64_t M) { return M > 1 ? t.token_stride : 0; }
+int64_t head_stride(const lora_heads_t &t) { return t.heads > 1 ? t.head_stride : 0; }
+
 // A tensor's checks: 0 or a status.
 lora_status_t check_heads(const lora_heads_t *t, int heads, int esize, int vec_bytes, int64_t M, int D) {
     if (!t->data || t->heads < 1 || t->heads > 4096 || t->heads != heads) return LORA_ERR_INVALID_ARG;
-    const int64_t most = int64_t(1) << 40;
-    if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride > most || t->head_stride > most)
-        return LORA_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 40, ts = token_stride(*t, M), hs = head_stride(*t);
+    if (ts < 0 || hs < 0 || ts > most || hs > most) return LORA_ERR_INVALID_ARG;
     // no element twice: tokens outside heads, or heads outside tokens
-    const __int128 over_tokens = __int128(M - 1) * t->token_stride + D, over_heads = __int128(heads - 1) * t->head_stride + D;
+    const __int128 over_tokens = __int128(M - 1) * ts + D, over_heads = __int128(heads - 1) * hs + D;
     if (over_tokens + over_heads > (__int128(1) << 58)) return LORA_ERR_INVALID_ARG;  // bytes in 63 bits
-    const bool tokens_outside = M == 1 || t->token_stride >= over_heads;
-    const bool heads_outside = heads == 1 || t->head_stride >= over_tokens;
-    if ((M > 1 && t->token_stride < D) || (heads > 1 && t->head_stride < D) || (!tokens_outside && !heads_outside))
-        return LORA_ERR_INVALID_ARG;
-    if (!aligned(t->data, 16) || (t->token_stride * esize) % vec_bytes || (t->head_stride * esize) % vec_bytes)
-        return LORA_ERR_MISALIGNED;
+    const bool tokens_outside = M == 1 || ts >= over_heads;
+    const bool heads_outside = heads == 1 || hs >= over_tokens;
+    if ((M > 1 && ts < D) || (heads > 1 && hs < D) || (!tokens_outside && !heads_outside)) return LORA_ERR_INVALID_ARG;
+    if (!aligned(t->data, 16) || (ts * esize) % vec_bytes || (hs * esize) % vec_bytes) return LORA_ERR_MISALIGNED;
     return LORA_OK;
 }
 
@@ -846,15 +848,15 @@ lora_status_t run(int dtype, const lora_heads_t *const in[2], const lora_heads_t
         if (!in[i]) continue;
         HeadTensor &t = a.t[i];
         t.in = in[i]->data;
-        t.in_ts = in[i]->token_stride;
-        t.in_hs = in[i]->head_stride;
+        t.in_ts = token_stride(*in[i], M);
+        t.in_hs = head_stride(*in[i]);
         t.out = out[i]->data;
-        t.out_ts = out[i]->token_stride;
-        t.out_hs = out[i]->head_stride;
+        t.out_ts = token_stride(*out[i], M);
+        t.out_hs = head_stride(*out[i]);
         if (bwd) {
             t.dy = dy[i]->data;
-            t.dy_ts = dy[i]->token_stride;
-            t.dy_hs = dy[i]->head_stride;
+            t.dy_ts = token_stride(*dy[i], M);
+            t.dy_hs = head_stride(*dy[i]);
         }
         t.weight = weight[i];
         t.heads = in[i]->heads;

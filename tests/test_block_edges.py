@@ -37,3 +37,18 @@ def test_tangents_are_refused(lib, grad):
                   lambda: block.qk_norm_rope(q, dual(q)), lambda: block.qkv_heads(dual(h), 2, 2, 16)):
             with pytest.raises(NotImplementedError, match="forward mode"):
                 f()
+
+
+def test_strides_over_one_token_or_head_are_not_looked_at(lib):
+    """Up to the check behind the strides' (4: no workspace for the weight gradient): any stride, even a
+    negative or an odd one, where there is one token or head; refused as before where there are two."""
+    def bwd(M, heads, ts, hs):
+        t = [ctypes.byref(L.lora_heads_t(p, ts, hs, heads)) for p in (0x7000, 0x1000, 0x5000)]
+        return lib.lora_qk_norm_rope_bwd(0, t[0], None, t[1], None, None, None, P(0x2000), P(0x3000), P(0x4000), 16, t[2],
+                                         None, P(0x8000), None, M, 128, 128, 0, 1, 1e-6, None, 0, None)
+
+    assert bwd(1, 8, 1024, 128) == 4
+    for ts in (0, 2057, -1, 1 << 50):
+        assert bwd(1, 8, ts, 128) == 4 and bwd(1, 1, ts, ts) == 4
+        assert bwd(3, 1, 1024, ts) == 4
+        assert bwd(2, 8, ts, 128) in (1, 2) and bwd(1, 2, 1024, ts) in (1, 2)

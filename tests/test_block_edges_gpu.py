@@ -99,3 +99,32 @@ def test_tensors_at_odd_offsets():
         grads = torch.autograd.grad(whole, odd, torch.cat((aux, up.flatten())))
         for a, b in zip(grads, want):
             assert torch.equal(a, b)
+
+
+def test_one_token_or_one_head_with_any_stride():
+    """The stride over a single token or head leads nowhere: rows of any pitch."""
+    M, hq, hk, D = 6, 3, 2, 32
+    h, wq, wk, cos, sin, pos = _heads_inputs(M, hq, hk, D, 16)
+    n = h.shape[1]
+    want = block.qkv_heads(h, hq, hk, D, wq, wk, cos, sin, pos)
+    for pitch in (n + 3, n + 1):
+        buf = torch.zeros(1, pitch, dtype=h.dtype, device="cuda")
+        row = buf[:, :n]
+        row.copy_(h[2:3])
+        assert row.stride(0) == pitch
+        row.requires_grad_(True)
+        got = block.qkv_heads(row, hq, hk, D, wq, wk, cos, sin, pos[2:3])
+        assert all(torch.equal(a, b[2:3]) for a, b in zip(got, want))
+        q, k = _split(row, hq, hk, D)
+        for a, b in zip(block.qk_norm_rope(q, k, wq, wk, cos, sin, pos[2:3]), want):
+            assert torch.equal(a, b[2:3])
+        q_out, k_out = (torch.empty_like(t) for t in (q, k))
+        L.lora_qk_norm_rope_fwd(q.detach(), k.detach(), wq, wk, cos, sin, pos[2:3], q_out, k_out)
+        assert torch.equal(q_out, want[0][2:3])
+        d, = torch.autograd.grad(got, row, tuple(torch.ones_like(t) for t in got))
+        assert d.shape == row.shape
+    # one head, its own stride odd
+    buf = torch.zeros(M, 3, D + 1, dtype=h.dtype, device="cuda")
+    one = buf.view(M, -1)[:, :96].as_strided((M, 1, D), (96, 1000003, 1))
+    assert torch.equal(block.qk_norm_rope(one, one, wq, wq, cos, sin, pos)[0],
+                       block.qk_norm_rope(one.contiguous(), one.contiguous(), wq, wq, cos, sin, pos)[0])
