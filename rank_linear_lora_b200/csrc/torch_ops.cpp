@@ -411,13 +411,16 @@ int head_type(const Tensor &t) {
     }
 }
 
-// t [M, heads, D] itself if the library's strides can name it, else a contiguous copy.
+// t [M, heads, D] itself if the library's strides can name it, else a contiguous copy: strides of
+// whole 16-byte units, tokens outside heads or heads outside tokens (what names an element twice, or
+// might, can still be read as an input).
 Tensor addressable(const Tensor &t) {
     if (t.dim() != 3) return t;
     const int64_t M = t.size(0), H = t.size(1), D = t.size(2), unit = 16 / t.element_size();
-    auto named = [&](int64_t n, int64_t stride) { return n == 1 || (stride >= D && stride % unit == 0); };
-    if (t.stride(2) == 1 && named(M, t.stride(0)) && named(H, t.stride(1)) &&
-        reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
+    const int64_t ts = M > 1 ? t.stride(0) : 0, hs = H > 1 ? t.stride(1) : 0;
+    auto named = [&](int64_t n, int64_t stride) { return n <= 1 || (stride >= D && stride % unit == 0); };
+    const bool apart = M <= 1 || H <= 1 || ts >= (H - 1) * hs + D || hs >= (M - 1) * ts + D;
+    if (t.stride(2) == 1 && named(M, ts) && named(H, hs) && apart && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
         return t;
     return on_16_bytes(t.contiguous());
 }

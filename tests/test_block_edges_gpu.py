@@ -128,3 +128,13 @@ def test_one_token_or_one_head_with_any_stride():
     one = buf.view(M, -1)[:, :96].as_strided((M, 1, D), (96, 1000003, 1))
     assert torch.equal(block.qk_norm_rope(one, one, wq, wq, cos, sin, pos)[0],
                        block.qk_norm_rope(one.contiguous(), one.contiguous(), wq, wq, cos, sin, pos)[0])
+
+
+def test_heads_that_overlap_are_copied():
+    """Inputs by strides that name an element twice (windows over one row) can only be read: a copy."""
+    _, wq, wk, cos, sin, pos = _heads_inputs(6, 3, 2, 32, 16)
+    flat = torch.randn(8 * 32, device="cuda").to(torch.bfloat16)
+    win = flat.as_strided((6, 3, 32), (32, 32, 1))
+    for a, b in zip(block.qk_norm_rope(win, win[:, :2], wq, wk, cos, sin, pos),
+                    block.qk_norm_rope(win.contiguous(), win[:, :2].contiguous(), wq, wk, cos, sin, pos)):
+        assert torch.equal(a, b)
