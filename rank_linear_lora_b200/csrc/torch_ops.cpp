@@ -206,9 +206,28 @@ void no_tangents(const char *name, const Ts &...ts) {
         TORCH_CHECK_NOT_IMPLEMENTED(!(has_tangent(ts) || ...), name, ": derivatives in forward mode are not implemented");
 }
 
-// What a node keeps besides its tensors.
+// A tensor that a node keeps but does not save: a constant of the call (the frozen weight, the
+// rotation's tables), which no hook on saved tensors should move to the host and back each step.  Like
+// a saved one it must not change before the backward.
+struct Constant {
+    Tensor t;
+    int64_t version = 0;
+
+    Constant() = default;
+    Constant(const Tensor &v) : t(v), version(now()) {}
+    Constant(const OptTensor &v) : Constant(has(v) ? *v : Tensor()) {}
+    int64_t now() const { return t.defined() && !t.is_inference() ? static_cast<int64_t>(t._version()) : 0; }
+    const Tensor &unchanged(const char *name) const {
+        TORCH_CHECK(now() == version, "one of the variables needed for gradient computation has been modified by an inplace "
+                    "operation: ", name, " is at version ", now(), "; expected version ", version);
+        return t;
+    }
+};
+
+// What a node keeps besides its saved tensors.
 struct Kept : torch::CustomClassHolder {
     Weight w;
+    Constant data, scale, cos, sin;
     double alpha = 0, eps = 0;
     int act = 0;
     bool interleaved = false, norm = true, bias = false, residual = false;
@@ -268,9 +287,11 @@ struct Glu : torch::autograd::Function<Glu> {
     static Tensor forward(AutogradContext *ctx, const Tensor &x, const Tensor &A, const Tensor &B, double alpha,
                           const Weight &w, int64_t act) {
         GluOut o = glu_forward(x, A, B, alpha, w, static_cast<int>(act), true);
-        ctx->save_for_backward({x, A, B, o.xa, o.gu, w.data, w.scale});
+        ctx->save_for_backward({x, A, B, o.xa, o.gu});
         auto k = c10::make_intrusive<Kept>();
         k->w = w;
+        k->data = w.data;
+        k->scale = w.scale;
         k->alpha = alpha;
         k->act = static_cast<int>(act);
         keep(ctx, std::move(k));
@@ -281,6 +302,8 @@ struct Glu : torch::autograd::Function<Glu> {
         const variable_list s = ctx->get_saved_variables();
         c10::intrusive_ptr<torch::CustomClassHolder> hold;
         const Kept &k = kept(ctx, hold);
+        k.data.unchanged("the frozen weight");
+        k.scale.unchanged("the frozen weight's scales");
         const Tensor &x = s[0], &A = s[1], &B = s[2], &xa = s[3], &gu = s[4];
         const int dev = c10::cuda::current_device();
         const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
@@ -348,9 +371,11 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
     static Tensor forward(AutogradContext *ctx, const Tensor &x, const Tensor &A, const Tensor &B, const OptTensor &bias,
                           const OptTensor &residual, double alpha, const Weight &w, int64_t act) {
         ActOut o = act_forward(x, A, B, bias, residual, alpha, w, static_cast<int>(act), true);
-        ctx->save_for_backward({x, A, B, o.xa, o.pre, has(bias) ? *bias : Tensor(), w.data, w.scale});
+        ctx->save_for_backward({x, A, B, o.xa, o.pre, has(bias) ? *bias : Tensor()});
         auto k = c10::make_intrusive<Kept>();
         k->w = w;
+        k->data = w.data;
+        k->scale = w.scale;
         k->alpha = alpha;
         k->act = static_cast<int>(act);
         k->bias = has(bias);
@@ -363,6 +388,8 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
         const variable_list s = ctx->get_saved_variables();
         c10::intrusive_ptr<torch::CustomClassHolder> hold;
         const Kept &k = kept(ctx, hold);
+        k.data.unchanged("the frozen weight");
+        k.scale.unchanged("the frozen weight's scales");
         const Tensor &x = s[0], &A = s[1], &B = s[2], &xa = s[3], &pre = s[4], &bias = s[5];
         const int dev = c10::cuda::current_device();
         const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
@@ -485,7 +512,7 @@ std::pair<Tensor, Tensor> heads_forward(const Tensor &q, const Tensor &k, const 
 }
 
 // dq, dk and the weights' gradients from up[0], up[1]; the saved tensors from s[at] on are the
-// weights, cos, sin and positions.  `edge`: the first weight's place among the tensors that were
+// weights and positions.  `edge`: the first weight's place among the tensors that were
 // given, which needs_input_grad counts.
 std::pair<Tensor, Tensor> heads_backward(AutogradContext *ctx, const Kept &kp, const variable_list &up, const Tensor &q,
                                          const Tensor &k, const variable_list &s, size_t at, int edge, const Tensor &dq,
@@ -498,7 +525,7 @@ std::pair<Tensor, Tensor> heads_backward(AutogradContext *ctx, const Kept &kp, c
     if (wk.defined() && ctx->needs_input_grad(edge++)) dwk = M ? at::empty_like(wk) : at::zeros_like(wk);
     if (M > 0) {
         const Tensor dqo = addressable(up[0]), dko = addressable(up[1]);
-        const Rope t = rope(s[at + 2], s[at + 3], s[at + 4], M, dev);
+        const Rope t = rope(kp.cos.unchanged("cos"), kp.sin.unchanged("sin"), s[at + 2], M, dev);
         const lora_heads_t qi = heads(q, "q", q, dev), ki = heads(k, "k", k, dev), gq = heads(dqo, "the gradient of q", q, dev),
                            gk = heads(dko, "the gradient of k", k, dev), qo = heads(dq, "dq", q, dev),
                            ko = heads(dk, "dk", k, dev);
@@ -522,8 +549,10 @@ struct QkNormRope : torch::autograd::Function<QkNormRope> {
                                  double eps, bool interleaved, bool norm) {
         auto o = heads_forward(q, k, wq, wk, cos, sin, positions, eps, interleaved, norm);
         auto t = [](const OptTensor &v) { return has(v) ? *v : Tensor(); };
-        ctx->save_for_backward({q, k, t(wq), t(wk), t(cos), t(sin), t(positions)});
+        ctx->save_for_backward({q, k, t(wq), t(wk), t(positions)});
         auto kp = c10::make_intrusive<Kept>();
+        kp->cos = cos;
+        kp->sin = sin;
         kp->eps = eps;
         kp->interleaved = interleaved;
         kp->norm = norm;
@@ -557,8 +586,10 @@ struct QkvHeads : torch::autograd::Function<QkvHeads> {
         auto qkv = split_heads(h, hq, hk, D);
         auto o = heads_forward(qkv[0], qkv[1], wq, wk, cos, sin, positions, eps, interleaved, norm);
         auto t = [](const OptTensor &v) { return has(v) ? *v : Tensor(); };
-        ctx->save_for_backward({h, t(wq), t(wk), t(cos), t(sin), t(positions)});
+        ctx->save_for_backward({h, t(wq), t(wk), t(positions)});
         auto kp = c10::make_intrusive<Kept>();
+        kp->cos = cos;
+        kp->sin = sin;
         kp->eps = eps;
         kp->interleaved = interleaved;
         kp->norm = norm;

@@ -138,3 +138,53 @@ def test_heads_that_overlap_are_copied():
     for a, b in zip(block.qk_norm_rope(win, win[:, :2], wq, wk, cos, sin, pos),
                     block.qk_norm_rope(win.contiguous(), win[:, :2].contiguous(), wq, wk, cos, sin, pos)):
         assert torch.equal(a, b)
+
+
+def test_what_is_saved_for_the_backward():
+    """The frozen weight and the rotation's tables are constants of the call: no hook on saved
+    tensors (save_on_cpu among them) gets them to move, and the gradients stay the same bits."""
+    y = Layer(24, 64, 96, 8, "q4", seed=2)
+    h, wq, wk, cos, sin, pos = _heads_inputs(24, 3, 2, 32, 16)
+
+    def steps():
+        x, A, B = (t.clone().requires_grad_(True) for t in (y.x, y.A, y.B))
+        hh, a, b = (t.clone().requires_grad_(True) for t in (h, wq, wk))
+        for f, leaves in ((lambda: block.lora_glu(x, y.wt, A, B, y.alpha), (x, A, B)),
+                          (lambda: block.lora_linear_act(x, y.wt, A, B, y.alpha, act="silu"), (x, A, B)),
+                          (lambda: torch.cat(block.qk_norm_rope(*_split(hh, 3, 2, 32), a, b, cos, sin, pos), 1), (hh, a, b)),
+                          (lambda: torch.cat(block.qkv_heads(hh, 3, 2, 32, a, b, cos, sin, pos), 1), (hh, a, b))):
+            out = f()
+            yield from torch.autograd.grad(out, leaves, torch.ones_like(out))
+
+    want = list(steps())
+    constants = {t.data_ptr() for t in (*y.wt.tensors, cos, sin)}
+    packed = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (packed.append(t.data_ptr()), t)[1], lambda t: t):
+        got = list(steps())
+    assert len(packed) >= 16 and not constants & set(packed)
+    with torch.autograd.graph.save_on_cpu():
+        moved = list(steps())
+    for a, b, c in zip(want, got, moved):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_constants_changed_before_the_backward():
+    """The weight, its scales or the tables changed in place between forward and backward: an error,
+    as for every tensor that a backward needs."""
+    y = Layer(24, 64, 96, 8, "q4", seed=2)
+    h, wq, wk, cos, sin, pos = _heads_inputs(24, 3, 2, 32, 16)
+    h.requires_grad_(True)
+    x = y.x.clone().requires_grad_(True)
+    for f, constants in ((lambda: block.lora_glu(x, y.wt, y.A, y.B, y.alpha), y.wt.tensors),
+                         (lambda: block.lora_linear_act(x, y.wt, y.A, y.B, y.alpha), y.wt.tensors),
+                         (lambda: block.qkv_heads(h, 3, 2, 32, wq, wk, cos, sin, pos)[0], (cos, sin, pos)),
+                         (lambda: block.qk_norm_rope(*_split(h, 3, 2, 32), wq, wk, cos, sin, pos)[0], (cos, sin, pos))):
+        for t in constants:
+            out = f()
+            t.add_(0)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                out.backward(torch.ones_like(out))
+        out = f()
+        out.backward(torch.ones_like(out))
+        with pytest.raises(RuntimeError, match="second time"):
+            out.backward(torch.ones_like(out))
