@@ -239,13 +239,11 @@ const Kept &kept(AutogradContext *ctx, c10::intrusive_ptr<torch::CustomClassHold
     return static_cast<const Kept &>(*hold);
 }
 
-// The kernels' gradients have no graph of their own: differentiating through them is an error, not
-// a silent zero.
-variable_list once(variable_list grads, const variable_list &ups) {
-    bool any = false;
-    if (at::GradMode::is_enabled())
-        for (const Tensor &t : ups) any |= t.defined() && t.requires_grad();
-    if (!any) return grads;
+// The kernels' gradients have no graph of their own: where one is asked for (create_graph),
+// differentiating through them is an error, not a term that is silently missing.  They depend on the
+// saved tensors too, so an upstream gradient that is a constant changes nothing.
+variable_list once(variable_list grads) {
+    if (!at::GradMode::is_enabled()) return grads;
     for (Tensor &t : grads)
         if (t.defined()) t = t.detach().requires_grad_(true);
     auto err = std::make_shared<torch::autograd::DelayedError>(
@@ -308,7 +306,7 @@ struct Glu : torch::autograd::Function<Glu> {
         const int dev = c10::cuda::current_device();
         const int64_t M = x.size(0), r = A.size(0), n = k.w.d_out;
         Tensor dX = ctx->needs_input_grad(0) ? at::empty_like(x) : Tensor();
-        if (M == 0) return once({dX, at::zeros_like(A), at::zeros_like(B), Tensor(), Tensor(), Tensor()}, up);
+        if (M == 0) return once({dX, at::zeros_like(A), at::zeros_like(B), Tensor(), Tensor(), Tensor()});
         const Tensor dP = on_16_bytes(up[0].contiguous());
         need(dP, "the gradient of p", at::kBFloat16, {M, n / 2}, dev);
         const Grads d({A, B});
@@ -321,7 +319,7 @@ struct Glu : torch::autograd::Function<Glu> {
                            static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
               "lora_glu_bwd");
         const variable_list g = d.rounded();
-        return once({dX, g[0], g[1], Tensor(), Tensor(), Tensor()}, up);
+        return once({dX, g[0], g[1], Tensor(), Tensor(), Tensor()});
     }
 };
 
@@ -399,7 +397,7 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
         Tensor dX = ctx->needs_input_grad(0) ? at::empty_like(x) : Tensor(), dRes = want_res ? up[0] : Tensor();
         if (M == 0)
             return once({dX, at::zeros_like(A), at::zeros_like(B), want_bias ? at::zeros_like(bias) : Tensor(), dRes, Tensor(),
-                         Tensor(), Tensor()}, up);
+                         Tensor(), Tensor()});
         const Tensor dOut = on_16_bytes(up[0].contiguous());
         need(dOut, "the gradient of out", at::kBFloat16, {M, n}, dev);
         const Grads d({A, B, want_bias ? bias : Tensor()});
@@ -412,7 +410,7 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
                                   static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
               "lora_linear_act_bwd");
         const variable_list g = d.rounded();
-        return once({dX, g[0], g[1], g[2], dRes, Tensor(), Tensor(), Tensor()}, up);
+        return once({dX, g[0], g[1], g[2], dRes, Tensor(), Tensor(), Tensor()});
     }
 };
 
@@ -567,7 +565,7 @@ struct QkNormRope : torch::autograd::Function<QkNormRope> {
         const Tensor &q = s[0], &k = s[1];
         const Tensor dq = at::empty(q.sizes(), q.options()), dk = at::empty(k.sizes(), k.options());
         const auto dw = heads_backward(ctx, kp, up, q, k, s, 2, 2, dq, dk);
-        return once({dq, dk, dw.first, dw.second, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()}, up);
+        return once({dq, dk, dw.first, dw.second, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()});
     }
 };
 
@@ -613,7 +611,7 @@ struct QkvHeads : torch::autograd::Function<QkvHeads> {
         out[0] = dh;
         out[1] = dw.first;
         out[2] = dw.second;
-        return once(std::move(out), up);
+        return once(std::move(out));
     }
 };
 

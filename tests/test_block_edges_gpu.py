@@ -188,3 +188,21 @@ def test_constants_changed_before_the_backward():
         out.backward(torch.ones_like(out))
         with pytest.raises(RuntimeError, match="second time"):
             out.backward(torch.ones_like(out))
+
+
+def test_second_derivatives_are_errors():
+    """A gradient taken with create_graph carries a node that refuses to be differentiated, also where
+    the upstream gradient itself is a constant: the term is not dropped."""
+    y = Layer(12, 64, 96, 8, seed=5)
+    h, wq, wk, cos, sin, pos = _heads_inputs(12, 3, 2, 32, 16)
+    for f, t in ((lambda x: block.lora_glu(x, y.wt, y.A, y.B, y.alpha), y.x),
+                 (lambda x: block.lora_linear_act(x, y.wt, y.A, y.B, y.alpha), y.x),
+                 (lambda h: block.qkv_heads(h, 3, 2, 32, wq, wk, cos, sin, pos)[0], h),
+                 (lambda h: block.qk_norm_rope(*_split(h, 3, 2, 32), wq, wk, cos, sin, pos)[0], h)):
+        x = t.clone().requires_grad_(True)
+        out = f(x)
+        want, = torch.autograd.grad(out.sum(), x, retain_graph=True)
+        g, = torch.autograd.grad(out.sum(), x, create_graph=True)
+        assert torch.equal(g, want)
+        with pytest.raises(RuntimeError, match="twice"):
+            (x.square().sum() + g.square().sum()).backward()
