@@ -13,6 +13,7 @@
 
 #include <array>
 #include <list>
+#include <memory>
 #include <mutex>
 #include <optional>
 #include <string>
@@ -150,44 +151,79 @@ struct Grads {
 // ------------------------------------------------------------------ workspaces
 // Kept per device, stream, shape and plan, so that calls on two streams never share one; under
 // capture a new one from the graph's pool, so that two graphs can replay at the same time.  Two
-// threads may call on one stream: a call holds its lock until all its kernels are enqueued, so
-// that none of another call's, which would use the same workspace, come between them.
+// threads may call on one stream: a call holds its workspace's lock until all its kernels are
+// enqueued, so that none of another call's, which would use the same workspace, come between them.
+// No lock is held over an allocation or a release, which may want the interpreter's lock (a recorded
+// stack) or wait for another thread, and the list's lock not over a launch, which may wait for the
+// device.
 struct Workspaces {
     using Key = std::tuple<int, void *, bool, int, int64_t, int64_t, int64_t, int, uint64_t>;
+    struct Entry {
+        Key key;
+        Tensor ws;
+        std::mutex mu;
+        Entry(const Key &k, Tensor t) : key(k), ws(std::move(t)) {}
+    };
+    using List = std::list<std::shared_ptr<Entry>>;
     static constexpr size_t KEPT = 64;  // the least recently used goes first
+
     std::mutex mu;
-    std::list<std::pair<Key, Tensor>> kept;
+    List kept;
+
+    std::shared_ptr<Entry> find(const Key &key) {  // the list's lock is held
+        for (auto it = kept.begin(); it != kept.end(); ++it)
+            if ((*it)->key == key) {
+                kept.splice(kept.begin(), kept, it);
+                return kept.front();
+            }
+        return nullptr;
+    }
+
+    static Workspaces &all() {
+        static Workspaces *const w = new Workspaces;  // never destroyed: tensors must not outlive the device at exit
+        return *w;
+    }
 };
 
 struct Lease {
-    std::unique_lock<std::mutex> lock;
     Tensor ws;
+    std::shared_ptr<Workspaces::Entry> entry;  // null: a captured call's own
+    std::unique_lock<std::mutex> lock;
+
+    explicit Lease(Tensor own) : ws(std::move(own)) {}
+    explicit Lease(std::shared_ptr<Workspaces::Entry> e) : ws(e->ws), entry(std::move(e)), lock(entry->mu) {}
     void *data() const { return ws.data_ptr(); }
     size_t bytes() const { return ws.nbytes(); }
 };
 
 // `layer`: the layer's own workspace (lora_linear_workspace_size), else lora_linear_act_workspace_size's.
 Lease workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int r, const c10::cuda::CUDAStream &st) {
-    static Workspaces *const w = new Workspaces;  // never destroyed: tensors must not outlive the device at exit
+    Workspaces &w = Workspaces::all();
     auto make = [&] {
         const size_t n = layer ? lora_linear_workspace_size(op, M, d_in, d_out, r)
                                : lora_linear_act_workspace_size(op, M, d_in, d_out, r);
         TORCH_CHECK_VALUE(n > 0, "invalid sizes: ", M, " tokens, ", d_in, " -> ", d_out, ", rank ", r);
         return at::zeros({static_cast<int64_t>(n)}, at::TensorOptions().dtype(at::kByte).device(st.device()));
     };
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return {{}, make()};
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return Lease(make());
     const Workspaces::Key key(st.device_index(), st.stream(), layer, op, M, d_in, d_out, r, lora_linear_plan_epoch());
-    std::unique_lock<std::mutex> lk(w->mu);
-    for (auto it = w->kept.begin(); it != w->kept.end(); ++it)
-        if (it->first == key) {
-            w->kept.splice(w->kept.begin(), w->kept, it);
-            return {std::move(lk), w->kept.front().second};
-        }
+    std::shared_ptr<Workspaces::Entry> known;
+    {
+        const std::lock_guard<std::mutex> lk(w.mu);
+        known = w.find(key);
+    }
+    if (known) return Lease(std::move(known));
+    auto fresh = std::make_shared<Workspaces::Entry>(key, make());
     // a workspace that goes returns to its stream's pool of the caching allocator, in stream order
     // behind the kernels that still use it
-    while (w->kept.size() >= Workspaces::KEPT) w->kept.pop_back();
-    w->kept.emplace_front(key, make());
-    return {std::move(lk), w->kept.front().second};
+    Workspaces::List gone;
+    {
+        const std::lock_guard<std::mutex> lk(w.mu);
+        if (auto e = w.find(key)) fresh.swap(e), gone.push_back(std::move(e));  // another thread was first
+        else w.kept.push_front(fresh);
+        while (w.kept.size() > Workspaces::KEPT) gone.splice(gone.end(), w.kept, std::prev(w.kept.end()));
+    }
+    return Lease(std::move(fresh));
 }
 
 // ------------------------------------------------------------------ autograd
@@ -312,12 +348,14 @@ struct Glu : torch::autograd::Function<Glu> {
         const Grads d({A, B});
         const Tensor dGU = at::empty_like(gu);
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Lease ws = workspace(true, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = k.w.c();
-        check(lora_glu_bwd(bf16(dP), bf16(gu), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dGU),
-                           addr<uint16_t>(dX), d[0], d[1], M, k.w.d_in, n / 2, static_cast<int>(r),
-                           static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
-              "lora_glu_bwd");
+        {
+            const Lease ws = workspace(true, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+            check(lora_glu_bwd(bf16(dP), bf16(gu), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dGU),
+                               addr<uint16_t>(dX), d[0], d[1], M, k.w.d_in, n / 2, static_cast<int>(r),
+                               static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
+                  "lora_glu_bwd");
+        }
         const variable_list g = d.rounded();
         return once({dX, g[0], g[1], Tensor(), Tensor(), Tensor()});
     }
@@ -403,12 +441,14 @@ struct LinearAct : torch::autograd::Function<LinearAct> {
         const Grads d({A, B, want_bias ? bias : Tensor()});
         const Tensor dPre = k.act != LORA_ACT_NONE ? at::empty_like(dOut) : Tensor();
         const auto st = c10::cuda::getCurrentCUDAStream(dev);
-        const Lease ws = workspace(false, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
         const lora_weight_t cw = k.w.c();
-        check(lora_linear_act_bwd(bf16(dOut), bf16(pre), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dPre),
-                                  addr<uint16_t>(dX), d[0], d[1], d[2], M, k.w.d_in, n, static_cast<int>(r),
-                                  static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
-              "lora_linear_act_bwd");
+        {
+            const Lease ws = workspace(false, k.w.op(true), M, k.w.d_in, n, static_cast<int>(r), st);
+            check(lora_linear_act_bwd(bf16(dOut), bf16(pre), bf16(x), &cw, bf16(A), bf16(B), bf16(xa), addr<uint16_t>(dPre),
+                                      addr<uint16_t>(dX), d[0], d[1], d[2], M, k.w.d_in, n, static_cast<int>(r),
+                                      static_cast<float>(k.alpha), k.act, ws.data(), ws.bytes(), st.stream()),
+                  "lora_linear_act_bwd");
+        }
         const variable_list g = d.rounded();
         return once({dX, g[0], g[1], g[2], dRes, Tensor(), Tensor(), Tensor()});
     }
@@ -658,8 +698,8 @@ PYBIND11_MODULE(_ops, m) {
             PyErr_SetObject(type.ptr(), value.ptr());
         }
     });
-    m.def("glu", &glu);
-    m.def("linear_act", &linear_act);
-    m.def("qk_norm_rope", &qk_norm_rope);
-    m.def("qkv_heads", &qkv_heads);
+    m.def("glu", &glu, py::call_guard<py::gil_scoped_release>());
+    m.def("linear_act", &linear_act, py::call_guard<py::gil_scoped_release>());
+    m.def("qk_norm_rope", &qk_norm_rope, py::call_guard<py::gil_scoped_release>());
+    m.def("qkv_heads", &qkv_heads, py::call_guard<py::gil_scoped_release>());
 }

@@ -206,3 +206,36 @@ def test_second_derivatives_are_errors():
         assert torch.equal(g, want)
         with pytest.raises(RuntimeError, match="twice"):
             (x.square().sum() + g.square().sum()).backward()
+
+
+LOCKS = """
+import sys, threading, torch
+sys.path.insert(0, sys.argv[1])
+from rank_linear_lora_b200 import block
+def r(*s): return torch.randn(*s, device="cuda").to(torch.bfloat16)
+x, W, A, B = r(200, 64), r(96, 64), r(8, 64), r(96, 8)
+up = r(200, 96)
+torch.cuda.memory._record_memory_history(context="all", stacks="python")
+def train():
+    for m in range(1, 200):
+        t = x[:m].clone().requires_grad_(True)
+        block.lora_linear_act(t, W, A, B, 8.0, act="silu").backward(up[:m])
+def serve():
+    with torch.cuda.stream(torch.cuda.Stream()), torch.no_grad():
+        for m in range(1, 200):
+            block.lora_linear_act(x[:m], W, A, B, 8.0)
+            block.lora_glu(x[:m], W, A, B, 8.0)
+ts = [threading.Thread(target=f) for f in (train, serve, train, serve)]
+[t.start() for t in ts]
+[t.join() for t in ts]
+torch.cuda.synchronize()
+print("done")
+"""
+
+
+def test_no_lock_is_held_over_an_allocation():
+    """Threads that train and serve while every allocation records Python's stack, for which it takes
+    the interpreter's lock: none waits for that lock while another waits for it (a process of its own,
+    so that one that stood still would not hold up this one)."""
+    r = subprocess.run([sys.executable, "-c", LOCKS, ROOT], capture_output=True, text=True, timeout=180)
+    assert r.returncode == 0 and r.stdout.strip().endswith("done"), r.stderr[-2000:]
