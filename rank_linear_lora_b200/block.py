@@ -19,7 +19,8 @@ rotation's tables start at multiples of 16 bytes.
 
 Workspaces are kept per device, stream and shape, so calls on two streams never share one;
 a call that is being captured into a CUDA graph takes a workspace of its own from the
-graph's memory pool, so two graphs can replay at the same time.  To capture a backward,
+graph's memory pool, so two graphs can replay at the same time.  The kernels' waits are bounded;
+``check_workspaces`` tells whether one ran out.  To capture a backward,
 capture the forward with it in the same graph (autograd runs a backward on the streams of
 its forward), while no eager graph of the same leaves lives: as with torch's own operators,
 autograd would accumulate on that graph's stream, and the capture raises.
@@ -50,6 +51,15 @@ def _ops():
                                f"rank_linear_lora_b200/build.py): {e}") from e
         _native = native
     return _native
+
+
+def check_workspaces():
+    """Wait for the current device, then raise LoraError (LORA_ERR_TIMEOUT) if a kernel's bounded wait
+    has run out in any of the operators' workspaces since the last check: the outputs of calls since
+    then are not to be used.  The workspaces are zeroed again, so that later calls are right.  It sees
+    the workspaces that are kept (the 64 used last); a captured call's belongs to its graph and is
+    zeroed by each replay.  Synchronising: for tests and diagnostics, as lora_linear_check."""
+    _ops().check_workspaces()
 
 
 def _frozen(W) -> LA.FrozenWeight:

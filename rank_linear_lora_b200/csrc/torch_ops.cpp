@@ -226,6 +226,41 @@ Lease workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int 
     return Lease(std::move(fresh));
 }
 
+// The workspaces kept on the current device.
+std::vector<std::shared_ptr<Workspaces::Entry>> kept_here() {
+    const int dev = c10::cuda::current_device();
+    Workspaces &w = Workspaces::all();
+    std::vector<std::shared_ptr<Workspaces::Entry>> out;
+    const std::lock_guard<std::mutex> lk(w.mu);
+    for (const auto &e : w.kept)
+        if (std::get<0>(e->key) == dev) out.push_back(e);
+    return out;
+}
+
+// Waits for the device's work on every kept workspace and reads its error word.  One whose bounded
+// wait ran out is zeroed whole, as lora_linear.h asks: a hand-over flag that came late must not meet
+// the next call.
+void check_workspaces() {
+    lora_status_t worst = LORA_OK;
+    for (const auto &e : kept_here()) {
+        const std::lock_guard<std::mutex> lk(e->mu);  // no call enqueues on it meanwhile
+        c10::cuda::device_synchronize();
+        const lora_status_t s = lora_linear_check(e->ws.data_ptr(), c10::cuda::getCurrentCUDAStream().stream());
+        if (s == LORA_OK) continue;
+        worst = s;
+        if (s != LORA_ERR_TIMEOUT) break;
+        e->ws.zero_();
+        c10::cuda::device_synchronize();
+    }
+    check(worst, "block.check_workspaces");
+}
+
+std::vector<Tensor> kept_workspaces() {
+    std::vector<Tensor> out;
+    for (const auto &e : kept_here()) out.push_back(e->ws);
+    return out;
+}
+
 // ------------------------------------------------------------------ autograd
 bool trained(const Tensor &t) { return t.requires_grad(); }
 bool trained(const OptTensor &t) { return has(t) && t->requires_grad(); }
@@ -698,6 +733,8 @@ PYBIND11_MODULE(_ops, m) {
             PyErr_SetObject(type.ptr(), value.ptr());
         }
     });
+    m.def("check_workspaces", &check_workspaces, py::call_guard<py::gil_scoped_release>());
+    m.def("kept_workspaces", &kept_workspaces, py::call_guard<py::gil_scoped_release>());
     m.def("glu", &glu, py::call_guard<py::gil_scoped_release>());
     m.def("linear_act", &linear_act, py::call_guard<py::gil_scoped_release>());
     m.def("qk_norm_rope", &qk_norm_rope, py::call_guard<py::gil_scoped_release>());

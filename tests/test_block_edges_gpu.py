@@ -239,3 +239,31 @@ def test_no_lock_is_held_over_an_allocation():
     so that one that stood still would not hold up this one)."""
     r = subprocess.run([sys.executable, "-c", LOCKS, ROOT], capture_output=True, text=True, timeout=180)
     assert r.returncode == 0 and r.stdout.strip().endswith("done"), r.stderr[-2000:]
+
+
+def test_waits_that_ran_out_are_reported():
+    """block.check_workspaces: silent while all is well; after a bounded wait ran out in any kept
+    workspace LORA_ERR_TIMEOUT, once, and the workspace is as new (zeroed whole) for the next call."""
+    y = Layer(40, 64, 96, 8, seed=3)
+    stream = torch.cuda.Stream()
+    out = block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha)
+    with torch.cuda.stream(stream):
+        block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha)
+    block.check_workspaces()
+    kept = block._ops().kept_workspaces()
+    mine = [w for w in kept if w.numel() == L.lora_linear_act_workspace_size(L.OP_FWD, 40, 64, 96, 8)]
+    assert len(mine) >= 2
+    torch.cuda.synchronize()
+    for ws in mine:
+        ws[256:].fill_(0x5A)
+        L.lora_linear_selftest_timeout(ws, 1000)
+    with pytest.raises(L.LoraError, match="block.check_workspaces") as e:
+        block.check_workspaces()
+    assert e.value.status == 6
+    assert not any(ws.any().item() for ws in mine)
+    block.check_workspaces()
+    assert torch.equal(block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha), out)
+    with torch.cuda.stream(stream):
+        again = block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
