@@ -300,7 +300,8 @@ class LoraProjections(torch.nn.Module):
 class LoraQKV(LoraProjections):
     """The q, k and v projections of x with the norms of the heads of q and k (their weights
     q_norm and k_norm [D] are parameters; norm=False: none) and the rotation of the positions
-    (rotary dimensions `rot`, 0: none)."""
+    0 .. max_positions - 1 (its first `rot` dimensions, None: all D, 0: none; max_positions=0 leaves
+    the module without a table, and then it takes no positions)."""
 
     def __init__(self, W, hq: int, hk: int, D: int, r: int = 8, alpha: float = 16.0, *, max_positions: int = 0,
                  rot: int = None, theta: float = 10000.0, eps: float = 1e-6, interleaved: bool = False, norm: bool = True):
@@ -310,6 +311,9 @@ class LoraQKV(LoraProjections):
         for name in ("q_norm", "k_norm"):
             w = torch.nn.Parameter(torch.ones(D, dtype=torch.bfloat16, device=dev)) if norm else None
             self.register_parameter(name, w)
+        if rot and not max_positions:
+            raise ValueError(f"rot={rot} needs max_positions, the rows of its table")
+        self.turned = rot != 0
         rot = D if rot is None else rot
         cos, sin = rope_table(max_positions, rot, theta, device=dev) if max_positions and rot else (None, None)
         self.register_buffer("cos", cos, persistent=False)
@@ -326,6 +330,9 @@ class LoraQKV(LoraProjections):
     def forward(self, x, positions=None):
         """(q [..., hq, D], k [..., hk, D], v [..., hk, D]); positions [...] int64."""
         if self.cos is None:
+            if positions is not None and self.turned:
+                raise ValueError("positions: the module has no table to rotate by (max_positions=0; rot=0 says that "
+                                 "nothing is to be rotated)")
             positions = None
         elif positions is None:
             raise ValueError("positions: the tokens' positions, int64, one for each")

@@ -52,3 +52,23 @@ def test_strides_over_one_token_or_head_are_not_looked_at(lib):
         assert bwd(1, 8, ts, 128) == 4 and bwd(1, 1, ts, ts) == 4
         assert bwd(3, 1, 1024, ts) == 4
         assert bwd(2, 8, ts, 128) in (1, 2) and bwd(1, 2, 1024, ts) in (1, 2)
+
+
+def test_positions_without_a_table(monkeypatch):
+    """LoraQKV does not drop positions that it has no table for; without positions, or where rot=0 says
+    that nothing is rotated, it is as it was."""
+    monkeypatch.setenv("LORA_LINEAR_FUSED", "0")
+    W, x, pos = torch.randn(96, 32).to(torch.bfloat16), torch.randn(3, 32).to(torch.bfloat16), torch.arange(3)
+    plain = block.LoraQKV(W, hq=2, hk=2, D=16, r=8)
+    with pytest.raises(ValueError, match="no table"):
+        plain(x, pos)
+    with pytest.raises(ValueError, match="max_positions"):
+        block.LoraQKV(W, hq=2, hk=2, D=16, r=8, rot=8)
+    none = block.LoraQKV(W, hq=2, hk=2, D=16, r=8, rot=0, max_positions=64)
+    none.load_state_dict(plain.state_dict())
+    turned = block.LoraQKV(W, hq=2, hk=2, D=16, r=8, max_positions=64)
+    turned.load_state_dict(plain.state_dict())
+    want = plain(x)
+    for got in (none(x, pos), none(x), turned(x, 0 * pos)):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not torch.equal(turned(x, pos)[0], want[0])
