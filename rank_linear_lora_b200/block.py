@@ -168,7 +168,12 @@ def _unfused_heads(v, w, cos, sin, positions, eps, interleaved, norm):
         f = f * w.float()
     if cos is not None:
         rot = 2 * cos.shape[1]
-        c, s = cos[positions][:, None], sin[positions][:, None]
+        n = cos.shape[0]
+        if n < 1 and positions.numel():
+            raise ValueError("cos, sin: tables without a row")
+        inside = (positions >= 0) & (positions < n)
+        at = positions.clamp(0, n - 1)  # a position outside the table reads no row of it: NaN, as the kernels
+        c, s = (t[at].masked_fill(~inside[:, None], float("nan"))[:, None] for t in (cos, sin))
         head = f[..., :rot]
         a, b = (head[..., 0::2], head[..., 1::2]) if interleaved else head.chunk(2, dim=-1)
         ra, rb = a * c - b * s, b * c + a * s

@@ -72,3 +72,22 @@ def test_positions_without_a_table(monkeypatch):
     for got in (none(x, pos), none(x), turned(x, 0 * pos)):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert not torch.equal(turned(x, pos)[0], want[0])
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "interleaved"])
+def test_unfused_positions_outside_the_table(interleaved, monkeypatch):
+    """As the kernels: no row is read, the token's rotated dimensions are NaN, everything else is right.
+    (Indexing with them would be an error on the CPU, a fault on a GPU, and another row for -1.)"""
+    monkeypatch.setenv("LORA_LINEAR_FUSED", "0")
+    g = torch.Generator().manual_seed(7)
+    h = torch.randn(6, (3 + 2 * 2) * 16, generator=g)
+    cos, sin = block.rope_table(32, 8)
+    good, bad = torch.arange(6), torch.tensor([0, -1, 2, 32, 4, 1 << 40])
+    want = block.qkv_heads(h, 3, 2, 16, None, None, cos, sin, good, interleaved=interleaved)
+    got = block.qkv_heads(h, 3, 2, 16, None, None, cos, sin, bad, interleaved=interleaved)
+    for a, b in zip(got[:2], want[:2]):
+        assert a[[1, 3, 5], :, :8].isnan().all()
+        a[[1, 3, 5], :, :8] = b[[1, 3, 5], :, :8]
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="row"):
+        block.qkv_heads(h, 3, 2, 16, None, None, cos[:0], sin[:0], good)
