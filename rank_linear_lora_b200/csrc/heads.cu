@@ -266,16 +266,19 @@ struct Lane {
     static __device__ f2 partner(const f2 (&v)[SLOTS][P], int i, int e) { return INTER ? swap2(v[i][e]) : v[1 - i][e]; }
 };
 
-// v rotated back by the angles, in place:  v_a c + v_b s,  v_b c - v_a s.
+// v rotated back by the angles, in place:  v_a c + v_b s,  v_b c - v_a s.  `turned`: INTER, the
+// slots inside the rotation.
 template <int V, bool INTER, int NS>
 __device__ __forceinline__ void rotate_back(f2 (&v)[Lane<V, INTER, NS>::SLOTS][V / 2],
-                                            const f2 (&c)[INTER ? 2 : 1][V / 2], const f2 (&s)[INTER ? 2 : 1][V / 2]) {
+                                            const f2 (&c)[INTER ? 2 : 1][V / 2], const f2 (&s)[INTER ? 2 : 1][V / 2],
+                                            const bool (&turned)[2]) {
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
         if constexpr (INTER) {
             const f2 sign = pack2(1.0f, -1.0f);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) v[i][e] = fma2(swap2(v[i][e]), mul2(s[i][e], sign), mul2(v[i][e], c[i][e]));
+            for (int i = 0; i < 2; ++i)
+                if (turned[i]) v[i][e] = fma2(swap2(v[i][e]), mul2(s[i][e], sign), mul2(v[i][e], c[i][e]));
         } else {
             const f2 a = v[0][e], b = v[1][e];
             v[0][e] = fma2(b, s[0][e], mul2(a, c[0][e]));
@@ -350,6 +353,11 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 2 : 3) k_heads_fwd(const __gr
     T *out = static_cast<T *>(t.out) + token * t.out_ts + (h_lo + g) * t.out_hs;
     const int64_t in_step = G * t.in_hs, out_step = G * t.out_hs;
     f2 c[2][P], q[2][P], w[SL][P];
+    // INTER: a slot behind the rotation has partners that it must not see, not even times zero (an
+    // infinity times zero is NaN)
+    bool turned[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) turned[i] = !INTER || ln.turns(a.rot, i);
     for (int h0 = h_lo; h0 < h_hi; h0 += G * FWD_HEADS) {
         Vec<T, V> x[FWD_HEADS][SL];
 #pragma unroll
@@ -409,8 +417,8 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 2 : 3) k_heads_fwd(const __gr
                 Vec<T, V> y;
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
-                    const f2 r = i < 2 ? fma2(LaneT::partner(v, i, e), q[i < 2 ? i : 0][e], mul2(v[i][e], c[i < 2 ? i : 0][e]))
-                                       : mul2(v[i][e], w[i][e]);
+                    f2 r = mul2(v[i][e], i < 2 ? c[i < 2 ? i : 0][e] : w[i][e]);
+                    if (i < 2 && turned[i < 2 ? i : 0]) r = fma2(LaneT::partner(v, i, e), q[i < 2 ? i : 0][e], r);
                     y.put(e, mul2(r, inv2));
                 }
                 if (mine && ln.has[i]) y.store(out + ln.off[i]);
@@ -459,6 +467,9 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
     LaneT ln;
     ln.place(a.D, a.rot, lane & (L - 1), L);
     const int64_t in_step = G * t.in_hs, dy_step = G * t.dy_hs, out_step = G * t.out_hs;
+    bool turned[2];  // as in the forward
+#pragma unroll
+    for (int i = 0; i < 2; ++i) turned[i] = !INTER || ln.turns(a.rot, i);
     Vec<T, V> w[SL];  // as loaded: half the registers
     f2 dw[SL][P];
     load_weight<T, V>(t, ln, w);
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(WARPS * 32, NS ? 1 : 2) k_heads_bwd(const __gr
                 for (int i = 0; i < SL; ++i)
 #pragma unroll
                     for (int e = 0; e < P; ++e) dn[j][i][e] = d[j][i].get(e);
-                rotate_back<V, INTER, NS>(dn[j], c, s);
+                rotate_back<V, INTER, NS>(dn[j], c, s, turned);
 #pragma unroll
                 for (int i = 0; i < SL; ++i)
 #pragma unroll

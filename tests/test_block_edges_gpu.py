@@ -267,3 +267,43 @@ def test_waits_that_ran_out_are_reported():
         again = block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha)
     torch.cuda.synchronize()
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_infinities_and_nan_in_heads(inter, dtype):
+    """An infinity or NaN reaches its own head alone; without the norm, its own dimension (and its
+    partner in the rotation) alone, forward and backward."""
+    M, hq, hk, D, rot = 9, 3, 2, 40, 16
+    h, wq, wk, cos, sin, pos = _heads_inputs(M, hq, hk, D, rot, dtype=dtype)
+    inf, nan = float("inf"), float("nan")
+    dy = torch.randn(M, (hq + hk), D, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+
+    def run(h, dy, norm):
+        q, k = (t.clone().requires_grad_(True) for t in _split(h, hq, hk, D))
+        out = torch.cat(block.qk_norm_rope(q, k, wq, wk, cos, sin, pos, interleaved=inter, norm=norm), 1)
+        return out.detach(), torch.cat(torch.autograd.grad(out, (q, k), dy), 1)
+
+    odd = [(1, 0, 20, inf), (2, 1, 37, -inf), (3, 2, 22, nan), (4, 3, 39, inf), (5, 4, 30, nan)]  # behind the rotation
+    for norm in (False, True):
+        out0, dv0 = run(h, dy, norm)
+        h1, dy1 = h.clone(), dy.clone()
+        for m, hd, j, v in odd:
+            h1[m, hd * D + j] = v
+            dy1[m, hd, j] = v
+        out, _ = run(h1, dy, norm)
+        _, dv = run(h, dy1, norm)
+        same = torch.ones_like(out, dtype=torch.bool)
+        for m, hd, j, v in odd:
+            if norm:
+                same[m, hd] = False
+                assert out[m, hd, j].isnan()  # inf / inf
+                if v == v:
+                    assert not out[m, hd, [i for i in range(D) if i != j]].any()  # over an infinite root
+            else:
+                same[m, hd, j] = False
+                w = (wq if hd < hq else wk)[j]
+                for t in (out, dv):
+                    assert t[m, hd, j].isnan() if v != v else t[m, hd, j] == v * w.sign()
+        assert torch.equal(out[same], out0[same])
+        assert torch.equal(dv[same], dv0[same])
