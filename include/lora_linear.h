@@ -385,6 +385,10 @@ LORA_API lora_status_t lora_linear_selftest_timeout(void *workspace, size_t ws_b
  * given at each entry point.
  */
 
+/* Infinities and NaN follow fp32 arithmetic on the formulas, in every format and number of tokens: a
+ * token that has them does not change another's outputs.  Up to 16 tokens, a coded weight's scale
+ * multiplies sums of code times x, which have to stay within fp32 (E4M3: |x| up to 2^118 / d_in). */
+
 /* Activations.  Values: relu max(v, 0); silu v / (1 + e^-v); gelu v P(v) with the normal
  * distribution P; gelu_tanh v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
 typedef enum {

@@ -32,10 +32,12 @@
 // Codes are widened in registers, and no decoded weight is rounded.  A 4-bit code under the
 // exponent of 128 is 128 + q, and stands for q - 8: the products take 128 + q and start from -136
 // times the block's sum of x (8192 -> 2 x 28672, four tokens: 64.3 us, with an addition
-// afterwards 65.5; 621 instructions a stage, 0.56 issued a cycle and scheduler).  E4M3
-// codes enter with their exact values.  The scale (one a row, or one a row and 64 k, fetched
-// a tile ahead) multiplies the fp32 sums.  Codebook values are rounded once to bf16 and looked
-// up two codes at a time in a table of a byte's 256 pairs, a copy in every bank.
+// afterwards 65.5; 621 instructions a stage, 0.56 issued a cycle and scheduler).  A 4-bit sum that
+// is not finite is formed again from the codes by the finishing warps: an infinite x (or a finite
+// one that 128 + q takes past fp32) keeps the sign of its product, where 128 + q and the offset give
+// inf - inf.  E4M3 codes enter with their exact values.  The scale (one a row, or one a row and
+// 64 k, fetched a tile ahead) multiplies the fp32 sums.  Codebook values are rounded once to bf16
+// and looked up two codes at a time in a table of a byte's 256 pairs, a copy in every bank.
 //
 // s.xa comes from k_decode_xa just before; this kernel starts its stream beside it and waits
 // for it only before the low-rank term (programmatic dependent launch: that kernel lets this
@@ -170,6 +172,30 @@ __device__ __forceinline__ uint32_t cb_pair(uint32_t table_lane, uint32_t v, int
     uint32_t w;
     asm("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(table_lane + ((v >> (8 * byte)) & 0xFFu) * 128u));
     return w;
+}
+
+// sum_k (q - 8) scale / 7 x of one row and token, from memory: for the few sums that products with
+// 128 + q cannot give.
+__device__ __forceinline__ float q4_sum(const DecodeArgs &a, int64_t row, int token) {
+    const uint8_t *codes = a.w + row * (a.K / 2);
+    const uint16_t *scales = a.wscale + row * (a.K / 64), *x = a.x + static_cast<int64_t>(token) * a.K;
+    float v = 0.0f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < a.K; k0 += 64) {
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int k = k0; k < k0 + 64; k += 8) {
+            const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(codes + k / 2));
+            const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(x + k));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum = fmaf(static_cast<float>(static_cast<int>((q >> (4 * e)) & 15u) - 8),
+                           __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16), sum);
+        }
+        v = fmaf(bf16_f32(__ldg(scales + k0 / 64)), sum, v);
+    }
+    return v * (1.0f / 7.0f);
 }
 
 // Barrier of the finishing warps; true where any of their threads brings true.
@@ -628,9 +654,14 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
             *reinterpret_cast<float4 *>(&tail[fw * TILE + lane * 4]) = make_float4(c[0], c[1], c[2], c[3]);
         }
     };
+    // this thread's value of n-tile n and m-tile m of group u: its token, and its row in W (gated: the
+    // m-th projection's), up to the projection's last
+    auto token_of = [&](int n) { return n * 8 + 2 * (l & 3) + (oi & 1); };
+    auto row_of = [&](int u, int m) {
+        return u * GROUP_ROWS + tile_row<C_::NIBBLE>(l >> 2) + 8 * (oi >> 1) + m * (OP == D_GLU ? a.N : ROWS);
+    };
     auto epilogue = [&](int u, int n, const float (&v)[MT]) {
-        const int col0 = u * GROUP_ROWS + tile_row<C_::NIBBLE>(l >> 2) + 8 * (oi >> 1);
-        const int token = n * 8 + 2 * (l & 3) + (oi & 1);
+        const int col0 = row_of(u, 0), token = token_of(n);
         if (token >= a.M) return;
         const int64_t row = static_cast<int64_t>(token) * a.N;
         if constexpr (OP == D_GLU) {
@@ -684,6 +715,12 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
                 v[n][m] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) v[n][m] += red[(sums * WARPS + w) * OUT + (m * NT + n) * TILE + o];
+                if (FMT == F_Q4 && __builtin_expect(!(fabsf(v[n][m]) < INFINITY), 0)) {
+                    // 128 + q or the offset went past fp32 (an infinite x: inf - inf, which is NaN where
+                    // (q - 8) x is not), or the sum itself is not finite: formed again from the codes
+                    const int token = token_of(n), row = row_of(u, m);
+                    if (token < a.M && row < (OP == D_GLU ? m + 1 : 1) * a.N) v[n][m] = q4_sum(a, row, token);
+                }
                 v[n][m] += tail[(m * NT + n) * TILE + o];
             }
         named_bar_sync(1, FIN_WARPS * 32);  // read by all before the next group's low-rank term
@@ -902,6 +939,7 @@ cudaError_t launch_decode(const uint16_t *A, uint16_t *xa, float s, int format, 
     count_launch();
     if (e != cudaSuccess) return e;
     a.xa = xa;
+    a.w = static_cast<const uint8_t *>(w);
     return glu ? launch_fmt<D_GLU>(format, a, sms, st) : launch_fmt<D_ACT>(format, a, sms, st);
 }
 

@@ -17,6 +17,7 @@ constexpr int64_t DECODE_MAX_M = 16;
 struct DecodeArgs {
     CUtensorMap tmW;          // set by launch_decode
     const uint16_t *x;        // [M, K]
+    const uint8_t *w;         // the weight, or its codes; set by launch_decode
     const uint16_t *wscale;
     float cb[16];             // LORA_W_NF4
     const uint16_t *B;        // [N or 2 N, r]

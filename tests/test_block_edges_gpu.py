@@ -307,3 +307,63 @@ def test_infinities_and_nan_in_heads(inter, dtype):
                     assert t[m, hd, j].isnan() if v != v else t[m, hd, j] == v * w.sign()
         assert torch.equal(out[same], out0[same])
         assert torch.equal(dv[same], dv0[same])
+
+
+# M, d_in, d_out, format: a few tokens with x whole and in segments, groups of 16 and of 32 rows; a
+# prompt; tiles cut along K
+ODD_VALUES = [
+    (4, 512, 144, "bf16"), (4, 512, 4112, "q4"), (5, 576, 144, "q4"), (13, 576, 4112, "q4"), (16, 448, 272, "q4"),
+    (8, 12992, 4112, "q4"), (16, 5056, 1040, "q4"), (4, 20032, 272, "q4"), (7, 576, 4112, "nf4"), (8, 12992, 272, "nf4"),
+    (11, 528, 4112, "fp8"), (6, 20016, 272, "fp8"), (140, 320, 272, "bf16"), (140, 320, 272, "q4"),
+    (140, 320, 272, "nf4"), (140, 336, 272, "fp8"), (40, 4160, 272, "q4"), (200, 4104, 272, "bf16"),
+]
+
+
+@pytest.mark.parametrize("M,d,n,fmt", ODD_VALUES, ids=["-".join(map(str, c)) for c in ODD_VALUES])
+def test_infinities_nan_and_large_values(M, d, n, fmt):
+    """What 64 bits give, whichever kernel runs: a token with an infinity has infinities of the
+    products' signs (NaN where signs meet or a weight is zero), one with a NaN is NaN, values near the
+    end of bf16 keep theirs, and the other tokens the bits that they have without these."""
+    y = Layer(M, d, n, 8, fmt, seed=70 + M, alpha=8.0)
+    y.A, y.B = y.A.abs(), y.B.abs()
+    x = y.x.clone()
+    ws = L.act_workspace(y.wt.ops()[0], M, d, n, 8)
+
+    def run(x):
+        out, p = _bf(M, n), _bf(M, n // 2)
+        L.lora_linear_act_fwd(x, y.wt, y.A, y.B, None, y.residual, out, None, None, y.alpha, "none", ws)
+        L.lora_glu_fwd(x, y.wt, y.A, y.B, p, None, None, y.alpha, "relu", ws)
+        L.lora_linear_check(ws)
+        return out, p
+
+    plain = run(y.x)
+    # E4M3 codes multiply x before the row's scale does: up to 448 times more than the result
+    big = 2.0 ** 112 if fmt == "fp8" else 2.0 ** 121
+    x[0, 7], x[1, d - 3], x[2, d // 2], x[3, 70] = float("inf"), float("-inf"), float("nan"), big
+    if M > 4:
+        x[M - 1, 11], x[M - 1, d - 11] = float("inf"), float("inf")
+    out, p = run(x)
+    odd = [0, 1, 2, 3] + ([M - 1] if M > 4 else [])
+    rest = [i for i in range(M) if i not in odd]
+    assert torch.equal(out[rest], plain[0][rest]) and torch.equal(p[rest], plain[1][rest])
+    y.x = x
+    h, err = y.h()
+    h, err = h[odd], err[odd]
+    g, u = h[:, :n // 2], h[:, n // 2:]
+    a = torch.where(g < 0, torch.zeros_like(g), g)  # relu: 0 of -inf, NaN of NaN
+    for name, got, want in (("out", out[odd], (h + y.residual[odd].double()).float()), ("p", p[odd], a.float() * u.float())):
+        want = want.to(torch.bfloat16)  # what passes fp32 is an infinity
+        if name == "p":
+            # a finite g or u that is smaller than the bound of its own error has no certain sign (a weight
+            # that cancels the low-rank term), and the product of the large row overflows with either
+            unsure = (h.isfinite() & (h.abs() <= err))
+            unsure = unsure[:, :n // 2] | unsure[:, n // 2:]
+            unsure[[i for i in range(len(odd)) if odd[i] != 3]] = False
+            assert unsure[3].float().mean() < 0.1
+            got, want = got.masked_fill(unsure, 0), want.masked_fill(unsure, 0)
+        assert torch.equal(got.isnan(), want.isnan()), name
+        inf = want.isinf()
+        assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf]), name
+    assert out[0].isposinf().any() and out[1].isneginf().any() and out[2].isnan().all() and out[3].isfinite().all()
+    want, err = h[3] + y.residual[3].double(), err[3]
+    assert_within("large", out[3], want, err + (HALF[torch.bfloat16] + 2 * F32) * (want.abs() + err))
