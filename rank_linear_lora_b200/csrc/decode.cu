@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
         }
     };
     const int fills = (mine + GROUPS - 1) / GROUPS * n_seg;
+    int filled = 1;  // segments asked for, by warp fw == 0
     bool ok = true;
     for (int base = 0; ok && base < mine; base += GROUPS) {
         // segments of x: each while the products use the one before, the next batch's first at the end
@@ -697,7 +698,10 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
                     ok = wait_bounded(smem_u32(&x_empty[f & 1]), static_cast<uint32_t>((f >> 1) - 1) & 1u, abort_flag, a.err,
                                       DERR_WAIT_EMPTY);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) x_fill(seg < n_seg ? seg : 0, f & 1);
+                if (ok) {
+                    x_fill(seg < n_seg ? seg : 0, f & 1);
+                    filled = f + 1;
+                }
             }
         if (base == 0) grid_dep_wait();  // s.xa is there, and no earlier kernel still reads what is stored here
         for (int i = 0; i < min(GROUPS, mine - base); ++i) {
@@ -729,6 +733,13 @@ __global__ void __launch_bounds__(Cfg<FMT, OP, NT, SEG, MT>::THREADS, 1) k_decod
         for (int n = 0; n < NT; ++n) epilogue(u, n, v[n]);
         }
     }
+    // After a wait that ran out: the last copy into each buffer lands before the CTA leaves (product
+    // warps that gave up no longer wait for it).
+    if (SEG && !ok && fw == 0 && lane == 0)
+        for (int f = max(0, filled - 2); f < filled; ++f) {
+            volatile int never = 0;
+            wait_bounded(smem_u32(&x_full[f & 1]), static_cast<uint32_t>(f >> 1) & 1u, &never, a.err, DERR_WAIT_DRAIN);
+        }
 }
 
 // ------------------------------------------------------------------ s.xa = bf16(s . x.A^T)
