@@ -7,13 +7,16 @@
 //   gelu_tanh  v/2 (1 + tanh z) = v s(2z),            s(2z) (1 + v (1 - s(2z)) 2 z'),
 //              z = c (v + 0.044715 v^3), c = sqrt(2/pi)   z' = c (1 + 3 * 0.044715 v^2)
 //
-// gelu's P(v) = 1 - P(-v) comes from erfc(z) = t(a1 + t(a2 + t(a3 + t(a4 + t a5)))) e^-z^2 with
-// t = 1 / (1 + p z), z >= 0 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26:
-// off by at most 1.5e-7), which shares its exponential with the density and costs about half of
-// erff: at most 8e-8 |v| of absolute error, far inside one bf16 rounding of v.
+// gelu's P(v) = 1 - P(-v) comes from erfc(z) = e^-z^2 t(a1 + t(a2 + ... + t a6)), t = 1 / (1 + p z),
+// z >= 0: the polynomial is this file's own fit of e^z^2 erfc(z) over 0 <= z <= 9.3 (where e^-z^2
+// leaves fp32), the one of smallest relative error: 4e-6.  It shares its exponential with the
+// density and costs about half of erff.  The relative error matters on the negative side, where P
+// is as small as its tail: v P(v) is off by less than 2^-15 of itself down to v = -12.5, far inside
+// one bf16 rounding (a fit of smallest absolute error, 1.5e-7, has every digit wrong there).
 // The logistic function goes through __expf and __fdividef (a few units in the last place of
-// fp32, far inside the one bf16 rounding that every result takes); at the ends, e^-v =
-// inf gives s = 0 and e^-v = 0 gives s = 1.  NaN stays NaN in each of them.
+// fp32, far inside the one bf16 rounding that every result takes); at the ends, e^-v above 2^126
+// (v < -87.3) gives s = 0, for which silu is 0 and not v e^v, 1e-36 and less, and e^-v = 0 gives
+// s = 1.  NaN stays NaN in each of them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -49,9 +52,9 @@ constexpr float INV_SQRT2 = 0.70710678118654752f, INV_SQRT_2PI = 0.3989422804014
 __device__ __forceinline__ float normal_cdf(float v, float &e) {
     const float z = fabsf(v) * INV_SQRT2;
     e = __expf(-z * z);
-    const float t = __fdividef(1.0f, 1.0f + 0.3275911f * z);
+    const float t = __fdividef(1.0f, 1.0f + 0.4344f * z);
     const float half_erfc =
-        0.5f * t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f)))) * e;
+        0.5f * e * t * (0.245644301f + t * (0.236326128f + t * (0.276168525f + t * (0.00657896465f + t * (0.387573302f + t * -0.152294233f)))));
     return v < 0.0f ? half_erfc : 1.0f - half_erfc;
 }
 

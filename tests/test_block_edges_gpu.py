@@ -367,3 +367,26 @@ def test_infinities_nan_and_large_values(M, d, n, fmt):
     assert out[0].isposinf().any() and out[1].isneginf().any() and out[2].isnan().all() and out[3].isfinite().all()
     want, err = h[3] + y.residual[3].double(), err[3]
     assert_within("large", out[3], want, err + (HALF[torch.bfloat16] + 2 * F32) * (want.abs() + err))
+
+
+@pytest.mark.parametrize("M", [4, 64])
+def test_the_tail_of_gelu(M):
+    """v P(v) far on the negative side, where P is small: one bf16 rounding of the value itself.  Beside
+    it stand the density's exponential, whose argument v^2 / 2 <= 80 is rounded by 80 * 2^-23 in fp32, and
+    __expf's own 2 + 1.2 * 80 units of 2^-23: 2^-15 together, and the fp32 rest: 2^-13 covers them."""
+    d = 256
+    v = -torch.linspace(1.0, 12.5, M * d, dtype=torch.float64).view(M, d).to(torch.bfloat16).cuda()
+    eye = torch.eye(d, dtype=torch.bfloat16, device="cuda")
+    A, B = torch.zeros(8, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(d, 8, dtype=torch.bfloat16, device="cuda")
+    want, slope = act64(v.double(), "gelu")
+    lim = HALF[torch.bfloat16] + 2.0 ** -13
+    out = block.lora_linear_act(v, eye, A, B, 8.0, act="gelu")
+    assert ((out.double() - want).abs() <= lim * want.abs()).all()
+    p = block.lora_glu(v, torch.cat((eye, eye)), A, torch.cat((B, B)), 8.0, act="gelu")
+    assert ((p.double() - want * v.double()).abs() <= (lim + F32) * (want * v.double()).abs()).all()
+    dpre, dx = _bf(M, d), _bf(M, d)
+    one, dA, dB = torch.ones_like(v), torch.empty(8, d, device="cuda"), torch.empty(d, 8, device="cuda")
+    L.lora_linear_act_bwd(one, v, v, eye, A, B, None, dpre, dx, dA, dB, None, 8.0, "gelu",
+                          L.act_workspace(L.OP_BWD, M, d, d, 8))
+    # P + v p: its terms meet at -0.75 only
+    assert ((dpre.double() - slope).abs() <= lim * slope.abs()).all()
