@@ -484,6 +484,13 @@ LORA_API lora_status_t lora_linear_act_bwd(const uint16_t *dOut, const uint16_t 
  * along K.  Pure host function. */
 LORA_API size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d_out, int r);
 
+/* The plan of lora_linear_act_fwd, and of lora_glu_fwd with d_out = 2 d_ff, for `op`, a forward's
+ * lora_op_t: side_fwd, xa_cluster, fwd_tail (3: tiles cut along K, here in two or three pieces and
+ * for every format) and splitk[0] as lora_linear_get_plan gives them; all 0 where the few-token
+ * kernel takes the call (M <= 16).  Host-only; LORA_ERR_INVALID_ARG for invalid sizes or op. */
+LORA_API lora_status_t lora_linear_act_get_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r,
+                                                lora_plan_t *plan);
+
 /* Element types of the head operators' tensors; LORA_T_WEIGHT_GRADS is or-ed to one of them. */
 typedef enum { LORA_T_BF16 = 0, LORA_T_FP16 = 1, LORA_T_FP32 = 2, LORA_T_WEIGHT_GRADS = 0x100 } lora_dtype_t;
 

@@ -1652,6 +1652,21 @@ size_t lora_linear_act_workspace_size(int op, int64_t M, int64_t d_in, int64_t d
     return pl.total;
 }
 
+lora_status_t lora_linear_act_get_plan(int op, int64_t M, int64_t d_in, int64_t d_out, int r, lora_plan_t *plan) {
+    if (!plan || op < LORA_OP_FWD || op > LORA_OP_BWD_NF4 || op % 2) return LORA_ERR_INVALID_ARG;
+    static_assert(LORA_OP_FWD_Q4 == 2 * WF_Q4 && LORA_OP_FWD_FP8 == 2 * WF_FP8 && LORA_OP_FWD_NF4 == 2 * WF_CB, "op codes");
+    if (check_shapes(M, d_in, d_out, r, 1.0f, op / 2) != LORA_OK) return LORA_ERR_INVALID_ARG;
+    std::memset(plan, 0, sizeof(*plan));
+    if (M <= lora_host::DECODE_MAX_M) return LORA_OK;
+    Plan pl;
+    make_plan(op, M, d_in, d_out, r, PLAN_SMS, &pl, true);
+    plan->side_fwd = pl.side ? 1 : 2;
+    plan->xa_cluster = pl.side ? pl.sx.C : 0;
+    plan->fwd_tail = pl.fused_slots > 0 ? 3 : pl.fwd_tail ? 1 : 2;
+    plan->splitk[0] = pl.side ? 0 : pl.s_xa.splits;
+    return LORA_OK;
+}
+
 lora_status_t lora_linear_check(void *workspace, void *stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(st) != cudaSuccess) return LORA_ERR_CUDA;

@@ -66,6 +66,8 @@ def load_library():
     lib.lora_linear_act_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I, F, I, P, SZ, P]
     lib.lora_linear_act_workspace_size.argtypes = [I, I64, I64, I64, I]
     lib.lora_linear_act_workspace_size.restype = SZ
+    lib.lora_linear_act_get_plan.argtypes = [I, I64, I64, I64, I, P]
+    lib.lora_linear_act_get_plan.restype = I
     lib.lora_qk_norm_rope_fwd.argtypes = [I, P, P, P, P, P, P, P, I64, P, P, I64, I, I, I, I, F, P]
     lib.lora_qk_norm_rope_bwd.argtypes = [I, P, P, P, P, P, P, P, P, P, I64, P, P, P, P, I64, I, I, I, I, F, P, SZ, P]
     lib.lora_qk_norm_rope_workspace_size.argtypes = [I64, I, I]
@@ -585,6 +587,14 @@ def _act(act) -> int:
 
 def lora_linear_act_workspace_size(op: int, M: int, d_in: int, d_out: int, r: int) -> int:
     return int(load_library().lora_linear_act_workspace_size(op, M, d_in, d_out, r))
+
+
+def lora_linear_act_get_plan(op: int, M: int, d_in: int, d_out: int, r: int) -> dict:
+    """The plan of lora_linear_act_fwd (and of lora_glu_fwd with d_out = 2 d_ff), as
+    lora_linear_get_plan's; `op`: a forward's."""
+    p = lora_plan_t()
+    _check(load_library().lora_linear_act_get_plan(op, M, d_in, d_out, r, ctypes.byref(p)), "lora_linear_act_get_plan")
+    return p.as_dict()
 
 
 def act_workspace(op: int, M: int, d_in: int, d_out: int, r: int, device=None) -> torch.Tensor:

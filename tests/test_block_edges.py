@@ -91,3 +91,20 @@ def test_unfused_positions_outside_the_table(interleaved, monkeypatch):
         assert torch.equal(a, b)
     with pytest.raises(ValueError, match="row"):
         block.qkv_heads(h, 3, 2, 16, None, None, cos[:0], sin[:0], good)
+
+
+def test_plans_of_the_fused_forwards(lib):
+    """s.xa on pairs of CTAs where that leaves it the SMs that the GEMM's last round does not use, on
+    fours elsewhere; tiles cut along K where there are few; nothing where the few-token kernel runs."""
+    def plan(M, d_in=4096, d_out=4096, op=L.OP_FWD, r=8):
+        return L.lora_linear_act_get_plan(op, M, d_in, d_out, r)
+
+    for op in (L.OP_FWD, L.OP_FWD_Q4, L.OP_FWD_FP8, L.OP_FWD_NF4):
+        assert [plan(M, op=op)["xa_cluster"] for M in (512, 1024, 2048, 4096)] == [4, 2, 2, 4]
+    assert plan(256)["fwd_tail"] == 3 and plan(1024)["fwd_tail"] != 3
+    assert not any(sum(v) if isinstance(v, (list, tuple)) else v for v in plan(16).values())
+    assert plan(1024, r=128)["side_fwd"] == 2 and plan(1024, r=128)["splitk"][0] >= 1
+    for bad in (dict(M=0), dict(M=64, op=L.OP_BWD), dict(M=64, op=8), dict(M=64, r=12), dict(M=64, d_in=96, op=L.OP_FWD_Q4)):
+        with pytest.raises(L.LoraError) as e:
+            plan(**bad)
+        assert e.value.status == 1

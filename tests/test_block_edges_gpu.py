@@ -390,3 +390,66 @@ def test_the_tail_of_gelu(M):
                           L.act_workspace(L.OP_BWD, M, d, d, 8))
     # P + v p: its terms meet at -0.75 only
     assert ((dpre.double() - slope).abs() <= lim * slope.abs()).all()
+
+
+def _act_bound(y):
+    h, err = y.h()
+    h, err = h + y.bias.double(), err + F32 * (h.abs() + y.bias.double().abs())
+    want = h.clamp(min=0) + y.residual.double()
+    return want, err + (HALF[torch.bfloat16] + 2 * F32) * (want.abs() + err)
+
+
+def _glu_bound(y):
+    h, err = y.h()
+    n = y.n // 2
+    g, u, eg, eu = h[:, :n].clamp(min=0), h[:, n:], err[:, :n], err[:, n:]
+    e = eg * (u.abs() + eu) + g * eu
+    return g * u, e + (HALF[torch.bfloat16] + 2 * F32) * ((g * u).abs() + e)
+
+
+# M, d_in, rows of W, format: s.xa on pairs of CTAs beside the GEMM's idle SMs
+PAIRS = [(1024, 4096, 4096, "bf16"), (1024, 4096, 4096, "q4"), (1000, 4104, 4080, "bf16"), (2048, 4096, 4096, "fp8")]
+
+
+@pytest.mark.parametrize("M,d,n,fmt", PAIRS, ids=["-".join(map(str, c)) for c in PAIRS])
+def test_rank_r_products_on_pairs_beside_the_gemm(M, d, n, fmt):
+    """The GEMM starts while s.xa still runs: every element, and the same bits when x has only just been
+    written by the kernel before (another projection's output, a copy)."""
+    y = Layer(M, d, n, 16, fmt, seed=81)
+    op = y.wt.ops()[0]
+    assert L.lora_linear_act_get_plan(op, M, d, n, 16)["xa_cluster"] == 2
+    ws = L.act_workspace(op, M, d, n, 16)
+    out, p = _bf(M, n), _bf(M, n // 2)
+
+    def run(x, out, p):
+        L.lora_linear_act_fwd(x, y.wt, y.A, y.B, y.bias, y.residual, out, None, None, y.alpha, "relu", ws)
+        L.lora_glu_fwd(x, y.wt, y.A, y.B, p, None, None, y.alpha, "relu", ws)
+
+    run(y.x, out, p)
+    L.lora_linear_check(ws)
+    assert_within("out", out, *_act_bound(y))
+    assert_within("p", p, *_glu_bound(y))
+    # x is the output of the projection before, over a buffer that held something else
+    W2 = (torch.randn(d, 64, generator=y.g) / 8).to(torch.bfloat16).cuda()
+    A2, B2 = y.randn(8, 64), y.randn(d, 8)
+    z = [y.randn(M, 64) for _ in range(2)]
+    ws2 = L.act_workspace(L.OP_FWD, M, 64, d, 8)
+    x, want = _bf(M, d), []
+    for zi in z:
+        L.lora_linear_act_fwd(zi, W2, A2, B2, None, None, x, None, None, 8.0, "none", ws2)
+        torch.cuda.synchronize()
+        o, q = _bf(M, n), _bf(M, n // 2)
+        run(x.clone(), o, q)
+        torch.cuda.synchronize()
+        want.append((o, q))
+    assert not torch.equal(want[0][0], want[1][0])
+    got = []
+    for i in range(20):
+        L.lora_linear_act_fwd(z[i % 2], W2, A2, B2, None, None, x, None, None, 8.0, "none", ws2)
+        o, q = _bf(M, n), _bf(M, n // 2)
+        L.lora_linear_act_fwd(z[i % 2], W2, A2, B2, None, None, x, None, None, 8.0, "none", ws2)
+        run(x, o, q)
+        got.append((o, q))
+    L.lora_linear_check(ws)
+    for i, (o, q) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(q, want[i % 2][1]), i
