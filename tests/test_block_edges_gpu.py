@@ -453,3 +453,37 @@ def test_rank_r_products_on_pairs_beside_the_gemm(M, d, n, fmt):
     L.lora_linear_check(ws)
     for i, (o, q) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(q, want[i % 2][1]), i
+
+
+def test_offsets_past_32_bits():
+    """Outputs of more than 2^32 bytes and 2^31 elements: the last tokens are what they are alone (in
+    the same tiles: 1024 tokens from a multiple of 1024)."""
+    M, d, n = 290 * 1024, 64, 7424
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def r(*s, k=1.0):
+        return (k * torch.randn(*s, generator=g, device="cuda")).to(torch.bfloat16)
+
+    x, W, A, B, bias = r(M, d), r(n, d, k=0.1), r(8, d, k=0.1), r(n, 8, k=0.1), r(n)
+    assert M * n > 1 << 31
+    res = r(1024, n).expand(290, 1024, n).reshape(M, n)
+    part = slice(M - 1024, M)
+    for f in (lambda x, res: block.lora_linear_act(x, W, A, B, 8.0, bias=bias, residual=res, act="silu"),
+              lambda x, res: block.lora_glu(x, torch.cat((W, W)), A, torch.cat((B, B)), 8.0)):
+        ends = []
+        for rows in (slice(0, M), part):
+            xr = x[rows].clone().requires_grad_(True)
+            out = f(xr, res[rows])
+            up = res[rows]
+            dx, = torch.autograd.grad(out, xr, up)
+            ends.append((out[-1024:].clone(), dx[-1024:].clone()))
+            del out, dx, up, xr
+        # other tiles may be cut along K or N: sums in another order, so half a step and fp32's own
+        for a, b in zip(*ends):
+            assert a.isfinite().all() and (a.double() - b.double()).abs().max() <= 2.0 ** -7 * b.double().abs().max()
+    q = res.view(M, 58, 128)
+    pos = torch.arange(M, device="cuda") % 64
+    cos, sin = block.rope_table(64, 128, device="cuda")
+    whole = block.qk_norm_rope(q, q[:, :2], None, None, cos, sin, pos)
+    last = block.qk_norm_rope(q[part], q[part, :2], None, None, cos, sin, pos[part])
+    assert torch.equal(whole[0][part], last[0]) and torch.equal(whole[1][part], last[1])
