@@ -203,6 +203,7 @@ Lease workspace(bool layer, int op, int64_t M, int64_t d_in, int64_t d_out, int 
         const size_t n = layer ? lora_linear_workspace_size(op, M, d_in, d_out, r)
                                : lora_linear_act_workspace_size(op, M, d_in, d_out, r);
         TORCH_CHECK_VALUE(n > 0, "invalid sizes: ", M, " tokens, ", d_in, " -> ", d_out, ", rank ", r);
+        const c10::InferenceMode off(false);  // kept beyond the mode of this call, and zeroed again outside it
         return at::zeros({static_cast<int64_t>(n)}, at::TensorOptions().dtype(at::kByte).device(st.device()));
     };
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return Lease(make());

@@ -487,3 +487,22 @@ def test_offsets_past_32_bits():
     whole = block.qk_norm_rope(q, q[:, :2], None, None, cos, sin, pos)
     last = block.qk_norm_rope(q[part], q[part, :2], None, None, cos, sin, pos[part])
     assert torch.equal(whole[0][part], last[0]) and torch.equal(whole[1][part], last[1])
+
+
+def test_workspaces_of_inference_mode():
+    """A workspace first used under inference_mode is like any other: for training calls and the check."""
+    y = Layer(44, 64, 96, 8, seed=9)
+    with torch.inference_mode():
+        want = block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha).clone()
+    kept = [w for w in block._ops().kept_workspaces()
+            if w.numel() == L.lora_linear_act_workspace_size(L.OP_FWD, 44, 64, 96, 8)]
+    assert kept and not any(w.is_inference() for w in block._ops().kept_workspaces())
+    for ws in kept:
+        L.lora_linear_selftest_timeout(ws, 1000)
+    with pytest.raises(L.LoraError, match="TIMEOUT"):
+        block.check_workspaces()
+    block.check_workspaces()
+    x = y.x.clone().requires_grad_(True)
+    out = block.lora_linear_act(x, y.wt, y.A, y.B, y.alpha)
+    out.sum().backward()
+    assert torch.equal(out, want) and x.grad is not None
