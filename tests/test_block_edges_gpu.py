@@ -506,3 +506,57 @@ def test_workspaces_of_inference_mode():
     out = block.lora_linear_act(x, y.wt, y.A, y.B, y.alpha)
     out.sum().backward()
     assert torch.equal(out, want) and x.grad is not None
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_recomputed_in_the_backward(reentrant):
+    """Under checkpointing the forward runs again, in the backward's thread: the same bits."""
+    from torch.utils.checkpoint import checkpoint
+    y = Layer(40, 64, 128, 8, seed=12)
+    cos, sin = block.rope_table(64, 16, device="cuda")
+    pos = torch.arange(40, device="cuda")
+
+    def f(x, A, B):
+        p = block.lora_glu(x, y.wt, A, B, y.alpha)
+        h = block.lora_linear_act(p, y.wt.tensors[0], A, B, y.alpha, act="gelu")
+        return torch.cat(block.qkv_heads(h, 2, 1, 32, None, None, cos, sin, pos), 1)
+
+    grads = []
+    for again in (False, True):
+        leaves = [t.clone().requires_grad_(True) for t in (y.x, y.A, y.B)]
+        out = checkpoint(f, *leaves, use_reentrant=reentrant) if again else f(*leaves)
+        out.square().sum().backward()
+        grads.append([out.detach(), *(t.grad for t in leaves)])
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
+
+
+def test_leading_dimensions():
+    """Any leading dimensions, none among them, and one tensor in several places."""
+    y = Layer(12, 64, 64, 8, seed=13)
+    out = block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha, residual=y.x)
+    p = block.lora_glu(y.x, y.wt, y.A, y.B, y.alpha)
+    x4 = y.x.view(2, 3, 2, 64)
+    assert torch.equal(block.lora_linear_act(x4, y.wt, y.A, y.B, y.alpha, residual=x4).view(12, 64), out)
+    assert torch.equal(block.lora_glu(x4, y.wt, y.A, y.B, y.alpha).view(12, 32), p)
+    one = block.lora_linear_act(y.x[0], y.wt, y.A, y.B, y.alpha, residual=y.x[0])
+    assert one.shape == (64,) and block.lora_glu(y.x[0], y.wt, y.A, y.B, y.alpha).shape == (32,)
+    assert torch.equal(one, block.lora_linear_act(y.x[:1], y.wt, y.A, y.B, y.alpha, residual=y.x[:1])[0])
+    empty = block.lora_linear_act(y.x.view(3, 4, 64)[:0], y.wt, y.A, y.B, y.alpha)
+    assert empty.shape == (0, 4, 64)
+    h, wq, wk, cos, sin, pos = _heads_inputs(12, 3, 2, 32, 16)
+    q, k, v = block.qkv_heads(h, 3, 2, 32, wq, wk, cos, sin, pos)
+    for lead in ((12,), (3, 4), (2, 3, 2)):
+        for a, b in zip(block.qkv_heads(h.view(*lead, -1), 3, 2, 32, wq, wk, cos, sin, pos.view(lead)), (q, k, v)):
+            assert torch.equal(a, b.view(*lead, *b.shape[1:]))
+        q2, k2 = (t.unflatten(0, lead) for t in _split(h, 3, 2, 32))
+        for a, b in zip(block.qk_norm_rope(q2, k2, wq, wk, cos, sin, pos.view(lead)), (q, k)):
+            assert torch.equal(a, b.view(*lead, *b.shape[1:]))
+    # q and k one tensor, both weights one parameter: the gradients add up
+    t, w = h[:, :96].unflatten(1, (3, 32)).clone().requires_grad_(True), wq.clone().requires_grad_(True)
+    a, b = block.qk_norm_rope(t, t, w, w, cos, sin, pos)
+    assert torch.equal(a, b)
+    both = torch.autograd.grad((a, b), (t, w), (torch.ones_like(a), torch.ones_like(b)))
+    single = torch.autograd.grad(block.qk_norm_rope(t, t, w, w, cos, sin, pos)[0], (t, w), torch.ones_like(a))
+    for g2, g1 in zip(both, single):
+        assert torch.equal(g2, 2 * g1)
