@@ -560,3 +560,57 @@ def test_leading_dimensions():
     single = torch.autograd.grad(block.qk_norm_rope(t, t, w, w, cos, sin, pos)[0], (t, w), torch.ones_like(a))
     for g2, g1 in zip(both, single):
         assert torch.equal(g2, 2 * g1)
+
+
+# M, d_in, rows of W, r, format
+BOTH = [(1, 264, 272, 16, "bf16"), (7, 448, 528, 24, "q4"), (16, 5056, 1040, 16, "nf4"), (33, 1040, 528, 16, "bf16"),
+        (200, 336, 784, 72, "fp8"), (300, 320, 528, 16, "q4"), (257, 4160, 272, 16, "nf4")]
+
+
+@pytest.mark.parametrize("M,d,n,r,fmt", BOTH, ids=["-".join(map(str, c)) for c in BOTH])
+def test_functions_give_the_entry_points_bits(M, d, n, r, fmt):
+    """Outputs and gradients of the functions are those of the C entry points, which are compared with 64
+    bits element by element; the adapters' and the bias's rounded once to their type."""
+    y = Layer(M, d, n, r, fmt, seed=90 + M)
+    fop, bop = y.wt.ops()
+
+    def f32(*s):
+        return torch.full(s, float("nan"), device="cuda")
+
+    def same(got, want):
+        assert all(torch.equal(a, b.to(a.dtype)) for a, b in zip(got, want))
+
+    for act in ("none", "gelu"):
+        leaves = [t.clone().requires_grad_(True) for t in (y.x, y.A, y.B, y.bias, y.residual)]
+        x, A, B, bias, res = leaves
+        out = block.lora_linear_act(x, y.wt, A, B, y.alpha, bias=bias, residual=res, act=act)
+        up = y.randn(M, n)
+        o, pre, xa = _bf(M, n), _bf(M, n), _bf(M, r)
+        L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, y.residual, o, pre, xa, y.alpha, act, L.act_workspace(fop, M, d, n, r))
+        dPre, dX, dA, dB, db = _bf(M, n), _bf(M, d), f32(r, d), f32(n, r), f32(n)
+        L.lora_linear_act_bwd(up, pre, y.x, y.wt, y.A, y.B, xa, dPre, dX, dA, dB, db, y.alpha, act,
+                              L.act_workspace(bop, M, d, n, r))
+        same((out, *torch.autograd.grad(out, leaves, up)), (o, dX, dA, dB, db, up))
+        x, A, B = leaves[:3]
+        p = block.lora_glu(x, y.wt, A, B, y.alpha, act=act)
+        up = y.randn(M, n // 2)
+        o, gu, dGU = _bf(M, n // 2), _bf(M, n), _bf(M, n)
+        L.lora_glu_fwd(y.x, y.wt, y.A, y.B, o, gu, xa, y.alpha, act, L.act_workspace(fop, M, d, n, r))
+        L.lora_glu_bwd(up, gu, y.x, y.wt, y.A, y.B, xa, dGU, dX, dA, dB, y.alpha, act, L.workspace(bop, M, d, n, r))
+        same((p, *torch.autograd.grad(p, (x, A, B), up)), (o, dX, dA, dB))
+        with torch.no_grad():  # nothing saved: the same bits
+            same((block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha, y.bias, y.residual, act),), (out,))
+            same((block.lora_glu(y.x, y.wt, y.A, y.B, y.alpha, act),), (p,))
+    h, wq, wk, cos, sin, pos = _heads_inputs(M, 5, 2, 64, 32)
+    for inter in (False, True):
+        leaves = [t.clone().requires_grad_(True) for t in (h, wq, wk)]
+        outs = block.qkv_heads(leaves[0], 5, 2, 64, *leaves[1:], cos, sin, pos, eps=1e-5, interleaved=inter)
+        ups = [y.randn(M, k, 64) for k in (5, 2, 2)]
+        q, k = _split(h, 5, 2, 64)
+        qo, ko, dh = _bf(M, 5, 64), _bf(M, 2, 64), _bf(M, 9 * 64)
+        dwq, dwk = _bf(64), _bf(64)
+        L.lora_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, qo, ko, 1e-5, inter)
+        ws = torch.empty(L.lora_qk_norm_rope_workspace_size(M, 7, 64), dtype=torch.uint8, device="cuda")
+        L.lora_qk_norm_rope_bwd(ups[0], ups[1], q, k, wq, wk, cos, sin, pos, *_split(dh, 5, 2, 64), dwq, dwk, ws, 1e-5, inter)
+        dh[:, 7 * 64:] = ups[2].flatten(1)
+        same((*outs[:2], *torch.autograd.grad(outs, leaves, ups)), (qo, ko, dh, dwq, dwk))
