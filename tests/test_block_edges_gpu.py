@@ -614,3 +614,29 @@ def test_functions_give_the_entry_points_bits(M, d, n, r, fmt):
         L.lora_qk_norm_rope_bwd(ups[0], ups[1], q, k, wq, wk, cos, sin, pos, *_split(dh, 5, 2, 64), dwq, dwk, ws, 1e-5, inter)
         dh[:, 7 * 64:] = ups[2].flatten(1)
         same((*outs[:2], *torch.autograd.grad(outs, leaves, ups)), (qo, ko, dh, dwq, dwk))
+
+
+@pytest.mark.parametrize("M,d,n,fmt", [(1280, 2056, 4096, "bf16"), (300, 1088, 784, "q4")])
+def test_plans_installed_for_the_shape(M, d, n, fmt):
+    """A plan for the layer's shape steers s.xa and the last wave of the fused forwards too: any of them
+    computes the same function, on workspaces of its own layout."""
+    y = Layer(M, d, n, 16, fmt, seed=95)
+    op = y.wt.ops()[0]
+    act, glu = _act_bound(y), _glu_bound(y)
+    plans = [dict(side_fwd=2), dict(side_fwd=2, splitk=[5, 0, 0, 0]), *(dict(xa_cluster=c) for c in (1, 2, 4)),
+             *(dict(fwd_tail=t) for t in ((1, 2, 3) if fmt == "bf16" else (1, 2)))]
+    try:
+        for plan in (*plans, None):
+            L.lora_linear_set_plan(M, d, n, 16, plan)
+            ws = L.act_workspace(op, M, d, n, 16)
+            out, p = _bf(M, n), _bf(M, n // 2)
+            L.lora_linear_act_fwd(y.x, y.wt, y.A, y.B, y.bias, y.residual, out, None, None, y.alpha, "relu", ws)
+            L.lora_glu_fwd(y.x, y.wt, y.A, y.B, p, None, None, y.alpha, "relu", ws)
+            L.lora_linear_check(ws)
+            assert_within(f"out {plan}", out, *act)
+            assert_within(f"p {plan}", p, *glu)
+            assert torch.equal(block.lora_linear_act(y.x, y.wt, y.A, y.B, y.alpha, y.bias, y.residual, "relu"), out)
+            assert torch.equal(block.lora_glu(y.x, y.wt, y.A, y.B, y.alpha, "relu"), p)
+    finally:
+        L.lora_linear_set_plan(M, d, n, 16, None)
+    block.check_workspaces()
