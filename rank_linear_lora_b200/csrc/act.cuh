@@ -53,8 +53,8 @@ __device__ __forceinline__ float normal_cdf(float v, float &e) {
     const float z = fabsf(v) * INV_SQRT2;
     e = __expf(-z * z);
     const float t = __fdividef(1.0f, 1.0f + 0.4344f * z);
-    const float half_erfc =
-        0.5f * e * t * (0.245644301f + t * (0.236326128f + t * (0.276168525f + t * (0.00657896465f + t * (0.387573302f + t * -0.152294233f)))));
+    const float tail = 0.276168525f + t * (0.00657896465f + t * (0.387573302f + t * -0.152294233f));
+    const float half_erfc = 0.5f * e * t * (0.245644301f + t * (0.236326128f + t * tail));
     return v < 0.0f ? half_erfc : 1.0f - half_erfc;
 }
 
