@@ -191,11 +191,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     are read in place), weights [D] of the same type, cos and sin [n_pos, rot / 2] fp32 (see
     rope_table), positions [...] int64.  Pairs are (i, i + rot/2), or (2 i, 2 i + 1) if
     interleaved.  New tensors; gradients flow to q, k and the weights."""
-    if q.dim() == 3:
-        q3, k3, pos = q, k, positions
-    else:
-        q3, k3 = q.reshape(-1, *q.shape[-2:]), k.reshape(-1, *k.shape[-2:])
-        pos = None if positions is None else positions.reshape(-1).contiguous()
+    q3, k3 = (q, k) if q.dim() == 3 else (q.reshape(-1, *q.shape[-2:]), k.reshape(-1, *k.shape[-2:]))
+    pos = None if positions is None else positions.reshape(-1).contiguous()
     outs = None
     if LA.fused_enabled():
         try:

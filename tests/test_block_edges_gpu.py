@@ -640,3 +640,17 @@ def test_plans_installed_for_the_shape(M, d, n, fmt):
     finally:
         L.lora_linear_set_plan(M, d, n, 16, None)
     block.check_workspaces()
+
+
+def test_positions_of_any_strides():
+    """Strided and expanded positions are read like contiguous ones, with and without leading dimensions."""
+    h, wq, wk, cos, sin, _ = _heads_inputs(12, 3, 2, 32, 16)
+    q, k = _split(h, 3, 2, 32)
+    for pos in (torch.arange(24, device="cuda")[::2], torch.full((1,), 5, device="cuda").expand(12),
+                torch.arange(24, device="cuda").view(12, 2)[:, 1]):
+        assert not pos.is_contiguous()
+        want = block.qk_norm_rope(q, k, wq, wk, cos, sin, pos.clone())
+        for got in (block.qk_norm_rope(q, k, wq, wk, cos, sin, pos),
+                    block.qkv_heads(h, 3, 2, 32, wq, wk, cos, sin, pos)[:2],
+                    [t[0] for t in block.qk_norm_rope(q[None], k[None], wq, wk, cos, sin, pos[None])]):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
