@@ -2,13 +2,11 @@
 import os
 import subprocess
 import sys
-import threading
 
 import pytest
 import torch
 
 from block_cases import F32, HALF, Layer, act64, assert_within
-from rank_linear_lora_b200 import autograd as LA
 from rank_linear_lora_b200 import block
 from rank_linear_lora_b200 import lora_linear as L
 
