@@ -181,9 +181,9 @@ __device__ __forceinline__ float q4_sum(const DecodeArgs &a, int64_t row, int to
     const uint16_t *scales = a.wscale + row * (a.K / 64), *x = a.x + static_cast<int64_t>(token) * a.K;
     float v = 0.0f;
 #pragma unroll 1
-    for (int k0 = 0; k0 < a.K; k0 += 64) {
+    for (int k0 = 0; k0 < a.K && v == v; k0 += 64) {  // a NaN stays one: the usual case ends early
         float sum = 0.0f;
-#pragma unroll 1
+#pragma unroll 4
         for (int k = k0; k < k0 + 64; k += 8) {
             const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(codes + k / 2));
             const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(x + k));
